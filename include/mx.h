@@ -314,6 +314,101 @@ mx_status mx_linear_dgrad(const void *d_dY, const void *d_W, float *d_dX, int64_
                           int64_t K, int rot, int rot_block, int rnd, uint64_t seed,
                           void *d_ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* Between the GEMMs: norm, activation, gradient clipping                     */
+/* ------------------------------------------------------------------------ */
+/*
+ * The operators of a training step that lie between its GEMMs.  Inputs are
+ * row-major matrices of bf16 or fp32 (mx_type) with a row pitch in elements
+ * (pitch >= columns; columns and pitches multiples of 8, pointers 16-byte
+ * aligned); every sum and product is in fp32.  y can be written in bf16
+ * (d_y, [T][columns], no gaps; for the Wgrad, which encodes it along the
+ * tokens) and/or encoded along its rows as the Fprop GEMM's operand:
+ *   MX_FORMAT_MXFP4  as mx_quantize(y, T, columns, MX_CONTRACT_COLS,
+ *                    MX_ROT_NONE, 32, MX_ROUND_RNE): mx_codes_bytes, mx_scales_bytes
+ *   MX_FORMAT_MXFP8  E4M3 codes [T][columns] (mx_mxfp8_codes_bytes) by the
+ *                    rules of mx_quantize_mxfp8, with the blocks along the
+ *                    rows; mx_scales_bytes
+ * each from y in fp32 (rounded once).  Encoding needs columns % 32 == 0.  Outputs
+ * may be NULL where noted; d_codes and d_scales must be NULL for MX_FORMAT_NONE.
+ * Columns above MX_ROW_COLUMNS_MAX (norm) get MX_ERR_UNSUPPORTED.  T == 0 or no
+ * columns: MX_OK, nothing launched (the weight gradient is zero-filled).
+ */
+typedef enum { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 } mx_type;
+typedef enum { MX_FORMAT_NONE = 0, MX_FORMAT_MXFP4 = 1, MX_FORMAT_MXFP8 = 2 } mx_format;
+#define MX_ROW_COLUMNS_MAX 32768
+
+/*
+ * mx_rmsnorm -- h = x + r;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd w.
+ *   d_x     [T][K] of x_type: the GEMM's result that joins the residual stream
+ *   d_res   [T][K] of res_type: the stream r, or NULL (h = x)
+ *   d_h     [T][K] of res_type, pitch h_pitch: the new stream; may be d_res
+ *           itself (same pitch).  NULL: not written; must be NULL without d_res.
+ *   d_w     [K] of w_type
+ *   d_rstd  [T] fp32, for the gradient; may be NULL
+ * y comes from h before h is rounded to res_type.  A row that holds Inf or NaN
+ * gives what the formula gives in fp32 (blocks that then hold NaN: scale 0xFF).
+ */
+mx_status mx_rmsnorm(const void *d_x, int x_type, int64_t x_pitch, const void *d_res, int res_type,
+                     int64_t res_pitch, const void *d_w, int w_type, float eps, int64_t T,
+                     int64_t K, void *d_h, int64_t h_pitch, void *d_y, int format, void *d_codes,
+                     void *d_scales, float *d_rstd, void *stream);
+
+/*
+ * mx_rmsnorm_backward -- the gradient of y with respect to h and w:
+ *   dx = rstd (dy w - h rstd^2 mean(dy w h)) + dres,   dw = sum over rows of dy h rstd
+ *   d_dy    [T][K] of dy_type: y's gradient (fp32 as mx_linear_dgrad leaves it)
+ *   d_h     [T][K] of h_type, as mx_rmsnorm left it (x where there is no stream)
+ *   d_rstd  [T] fp32 from mx_rmsnorm
+ *   d_dres  [T][K] of h_type: the stream's own gradient, added; or NULL
+ *   d_dx    [T][K] of h_type, pitch dx_pitch: the gradient of x and of r alike;
+ *           may be d_dres itself, or d_dy itself where the types agree (same pitch)
+ *   d_dw    [K] fp32, overwritten; NULL: not computed (no workspace needed then)
+ *   d_ws    mx_rmsnorm_backward_workspace_bytes(T, K) bytes, 256-byte aligned
+ * The rows' sum has a fixed order: the same inputs give the same bits.
+ */
+size_t mx_rmsnorm_backward_workspace_bytes(int64_t T, int64_t K);
+mx_status mx_rmsnorm_backward(const void *d_dy, int dy_type, int64_t dy_pitch, const void *d_h,
+                              int h_type, int64_t h_pitch, const void *d_w, int w_type,
+                              const float *d_rstd, const void *d_dres, int64_t dres_pitch,
+                              int64_t T, int64_t K, void *d_dx, int64_t dx_pitch, float *d_dw,
+                              void *d_ws, size_t ws_bytes, void *stream);
+
+/*
+ * mx_swiglu -- y[T][F] = silu(g) u with g = gu[:, 0:F], u = gu[:, F:2F] (the
+ * gate/up GEMM's result, gu_type), silu(g) = g / (1 + exp(-g)).
+ * mx_swiglu_backward -- d_dgu[T][2F] (bf16, no gaps: dY of the gate/up Wgrad and
+ * Dgrad): dg = dy u s (1 + g (1 - s)), du = dy g s, s = 1 / (1 + exp(-g)).
+ */
+mx_status mx_swiglu(const void *d_gu, int gu_type, int64_t gu_pitch, int64_t T, int64_t F,
+                    void *d_y, int format, void *d_codes, void *d_scales, void *stream);
+mx_status mx_swiglu_backward(const void *d_dy, int dy_type, int64_t dy_pitch, const void *d_gu,
+                             int gu_type, int64_t gu_pitch, int64_t T, int64_t F, void *d_dgu,
+                             void *stream);
+
+/*
+ * mx_grad_norm -- *d_norm = sqrt(sum of g^2 over `count` tensors).
+ * mx_clip_grads -- the same norm, and out_i = g_i * min(1, max_norm / (norm + eps)).
+ *   h_grads, h_sizes, h_types   HOST arrays: device pointer, elements and mx_type
+ *                               of each gradient (read before the call returns)
+ *   h_outs, h_out_types         likewise the outputs, of either type; out_i may be
+ *                               g_i itself (same type).  NULL: all in place.
+ *   d_norm                      one fp32 on the device
+ *   d_ws                        mx_grad_workspace_bytes(count) bytes, 256-byte aligned
+ * Pointers need only their element's alignment (slices of a flat bucket); whole
+ * 16-byte vectors are used where gradient and output are 16-byte aligned.  A size
+ * of 0 is skipped.  No tensors: the norm is 0.  A norm that is NaN makes every
+ * output NaN, an infinite one every finite gradient 0.  In place with nothing to
+ * clip (norm + eps <= max_norm) nothing is written.  The order of the sum is
+ * fixed by the sizes: the same inputs give the same bits.
+ */
+size_t mx_grad_workspace_bytes(int64_t count);
+mx_status mx_grad_norm(const void *const *h_grads, const int64_t *h_sizes, const int *h_types,
+                       int64_t count, float *d_norm, void *d_ws, size_t ws_bytes, void *stream);
+mx_status mx_clip_grads(const void *const *h_grads, const int64_t *h_sizes, const int *h_types,
+                        void *const *h_outs, const int *h_out_types, int64_t count, float max_norm,
+                        float eps, float *d_norm, void *d_ws, size_t ws_bytes, void *stream);
+
 /*
  * mx_linear_wgrad_noalloc -- mx_linear_wgrad without a caller workspace.
  * No counterpart in the paper: this is a deployment convenience.

@@ -17,6 +17,9 @@ from ._binding import (CONTRACT_COLS, CONTRACT_ROWS, OP_DGRAD, OP_FPROP, OP_WGRA
                        gemm_mxfp8_into, linear_wgrad_mxfp8, linear_wgrad_mxfp8_workspace_bytes,
                        nvfp4_scales_bytes, quantize_nvfp4, gemm_nvfp4, linear_wgrad_nvfp4,
                        linear_wgrad_nvfp4_workspace_bytes)
+from ._block import (FMT_MXFP4, FMT_MXFP8, RMSNormOut, SwiGLUOut, clip_grads, grad_norm,
+                     grad_workspace_bytes, rmsnorm, rmsnorm_backward,
+                     rmsnorm_backward_workspace_bytes, swiglu, swiglu_backward)
 
 __all__ = [
     "CONTRACT_COLS", "CONTRACT_ROWS", "OP_DGRAD", "OP_FPROP", "OP_WGRAD", "ROT_HADAMARD_DET",
@@ -29,4 +32,7 @@ __all__ = [
     "mxfp8_codes_bytes", "quantize_mxfp8", "gemm_mxfp8", "gemm_mxfp8_into", "linear_wgrad_mxfp8",
     "linear_wgrad_mxfp8_workspace_bytes", "nvfp4_scales_bytes", "quantize_nvfp4", "gemm_nvfp4",
     "linear_wgrad_nvfp4", "linear_wgrad_nvfp4_workspace_bytes",
+    "FMT_MXFP4", "FMT_MXFP8", "RMSNormOut", "SwiGLUOut", "clip_grads", "grad_norm",
+    "grad_workspace_bytes", "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
+    "swiglu", "swiglu_backward",
 ]

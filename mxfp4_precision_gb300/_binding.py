@@ -29,6 +29,9 @@ EXPORTED = [
     "mx_linear_wgrad_mxfp8_workspace_bytes", "mx_linear_wgrad_mxfp8",
     "mx_nvfp4_scales_bytes", "mx_quantize_nvfp4", "mx_gemm_nvfp4",
     "mx_linear_wgrad_nvfp4_workspace_bytes", "mx_linear_wgrad_nvfp4",
+    "mx_rmsnorm", "mx_rmsnorm_backward_workspace_bytes", "mx_rmsnorm_backward",
+    "mx_swiglu", "mx_swiglu_backward",
+    "mx_grad_workspace_bytes", "mx_grad_norm", "mx_clip_grads",
     "mx_check_status",
     "mx_debug_timeout_probe", "mx_bench_mma", "mx_status_string", "mx_version",
 ]
@@ -106,6 +109,25 @@ def lib() -> ctypes.CDLL:
             L.mx_linear_wgrad_nvfp4_workspace_bytes.restype = sz
             L.mx_linear_wgrad_nvfp4.argtypes = [P, P, P, i64, i64, i64, i32, i32, u64, P, sz, P]
             L.mx_linear_wgrad_nvfp4.restype = i32
+            f32 = ctypes.c_float
+            L.mx_rmsnorm.argtypes = [P, i32, i64, P, i32, i64, P, i32, f32, i64, i64, P, i64, P,
+                                     i32, P, P, P, P]
+            L.mx_rmsnorm.restype = i32
+            L.mx_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+            L.mx_rmsnorm_backward_workspace_bytes.restype = sz
+            L.mx_rmsnorm_backward.argtypes = [P, i32, i64, P, i32, i64, P, i32, P, P, i64, i64,
+                                              i64, P, i64, P, P, sz, P]
+            L.mx_rmsnorm_backward.restype = i32
+            L.mx_swiglu.argtypes = [P, i32, i64, i64, i64, P, i32, P, P, P]
+            L.mx_swiglu.restype = i32
+            L.mx_swiglu_backward.argtypes = [P, i32, i64, P, i32, i64, i64, i64, P, P]
+            L.mx_swiglu_backward.restype = i32
+            L.mx_grad_workspace_bytes.argtypes = [i64]
+            L.mx_grad_workspace_bytes.restype = sz
+            L.mx_grad_norm.argtypes = [P, P, P, i64, P, P, sz, P]
+            L.mx_grad_norm.restype = i32
+            L.mx_clip_grads.argtypes = [P, P, P, P, P, i64, f32, f32, P, P, sz, P]
+            L.mx_clip_grads.restype = i32
             L.mx_check_status.argtypes = [P]
             L.mx_check_status.restype = i32
             L.mx_debug_timeout_probe.argtypes = [i64, P]

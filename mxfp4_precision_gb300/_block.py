@@ -1,0 +1,250 @@
+"""The operators between the GEMMs of a training step (RMS norm with the
+residual's addition, SwiGLU, their gradients, gradient norm and clipping):
+torch-tensor marshalling over include/mx.h, like _binding.py.
+
+Matrices are 2-D CUDA tensors of torch.bfloat16 (or raw 16-bit patterns) or
+torch.float32 whose rows are contiguous; a row pitch (a slice of columns) is
+passed on.  Outputs and workspaces are allocated with torch unless given.  A
+`stream` other than the current one becomes the current one for the call, so
+that what is allocated belongs to it.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _binding as _b
+
+FMT_MXFP4, FMT_MXFP8 = 1, 2
+_BF16, _F32 = 0, 1
+_TYPES = {torch.bfloat16: _BF16, torch.int16: _BF16, torch.uint16: _BF16, torch.float32: _F32}
+
+
+class RMSNormOut(NamedTuple):
+    """h: the new stream (None without a residual); y: bf16 (None if not wanted);
+    codes, scales: the encoded y (None without fmt); rstd: fp32 [T]."""
+    h: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    rstd: torch.Tensor
+
+
+class SwiGLUOut(NamedTuple):
+    y: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    k = _TYPES.get(t.dtype)
+    if k is None:
+        raise ValueError(f"{name} must be bf16 (torch.bfloat16 or raw 16-bit patterns) or float32")
+    return k
+
+
+def _rows(t: torch.Tensor, name: str, shape=None):
+    """(pointer, mx_type, pitch) of a matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be 2-D" + (f" {shape}" if shape else "") + f", got {tuple(t.shape)}")
+    rows, cols = t.shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), _type(t, name), pitch if rows > 1 else cols
+
+
+def _vector(t: torch.Tensor, name: str, n: int) -> int:
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+    return _b._dev_ptr(t, name)
+
+
+def _encoded(fmt, T: int, K: int, device):
+    """Empty (codes, scales) of a row-direction encoding."""
+    if fmt is None:
+        return None, None
+    if fmt not in (FMT_MXFP4, FMT_MXFP8):
+        raise ValueError("fmt must be None, FMT_MXFP4 or FMT_MXFP8")
+    codes = torch.empty((T, K if fmt == FMT_MXFP8 else K // 2), dtype=torch.uint8, device=device)
+    # mx_scales_bytes(T, K), or one byte of an empty operand
+    n = -(-T // 128) * 128 * (8 * -(-K // 256))
+    return codes, torch.empty((n or 1,), dtype=torch.uint8, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def rmsnorm(x, weight, residual=None, eps: float = 1e-5, fmt=None, want_y: bool = True,
+            out_h=None, stream=None) -> RMSNormOut:
+    """h = x + residual, y = h * rstd * weight with rstd = 1 / sqrt(mean(h^2) + eps), over the
+    rows of x [T, K]; y in bf16 (want_y) and / or encoded along its rows (fmt: FMT_MXFP4 or
+    FMT_MXFP8) as the Fprop GEMM's operand.  h has the residual's type; out_h may be the residual
+    itself.  See mx_rmsnorm."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rmsnorm(x, weight, residual, eps, fmt, want_y, out_h)
+    xp, xt, xs = _rows(x, "x")
+    T, K = x.shape
+    d = x.device
+    w = _vector(weight, "weight", K)
+    h, rp, rt, rs, hs = out_h, None, 0, 0, 0
+    if residual is not None:
+        rp, rt, rs = _rows(residual, "residual", (T, K))
+        if h is None:
+            h, hs = torch.empty((T, K), dtype=residual.dtype, device=d), K
+        else:
+            _, ht, hs = _rows(h, "out_h", (T, K))
+            if ht != rt:
+                raise ValueError("out_h must have the residual's type")
+    elif h is not None:
+        raise ValueError("out_h needs a residual")
+    y = torch.empty((T, K), dtype=torch.bfloat16, device=d) if want_y else None
+    codes, scales = _encoded(fmt, T, K, d)
+    rstd = torch.empty((T,), dtype=torch.float32, device=d)
+    st = _b.lib().mx_rmsnorm(xp, xt, xs, rp, rt, rs, w, _type(weight, "weight"), eps, T, K, _ptr(h),
+                             hs, _ptr(y), fmt or 0, _ptr(codes), _ptr(scales), rstd.data_ptr(),
+                             _b._stream())
+    _b._check(st, "mx_rmsnorm")
+    return RMSNormOut(h, y, codes, scales, rstd)
+
+
+def rmsnorm_backward_workspace_bytes(T: int, K: int) -> int:
+    return int(_b.lib().mx_rmsnorm_backward_workspace_bytes(T, K))
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dres=None, want_dw: bool = True, ws=None, out_dx=None,
+                     stream=None):
+    """(dx, dw) of rmsnorm for y's gradient dy [T, K]: dx (of h's type) is the gradient of x and of
+    the residual alike, dres (the stream's own gradient) added; dw fp32 [K].  out_dx may be dres
+    itself.  See mx_rmsnorm_backward."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rmsnorm_backward(dy, h, weight, rstd, dres, want_dw, ws, out_dx)
+    dp, dt, ds = _rows(dy, "dy")
+    T, K = dy.shape
+    hp, ht, hs = _rows(h, "h", (T, K))
+    w = _vector(weight, "weight", K)
+    r = _vector(rstd, "rstd", T)
+    if rstd.dtype != torch.float32:
+        raise ValueError("rstd must be float32")
+    gp, gs = None, 0
+    if dres is not None:
+        gp, gt, gs = _rows(dres, "dres", (T, K))
+        if gt != ht:
+            raise ValueError("dres must have h's type")
+    if out_dx is None:
+        out_dx = torch.empty((T, K), dtype=h.dtype, device=dy.device)
+    op, ot, os_ = _rows(out_dx, "out_dx", (T, K))
+    if ot != ht:
+        raise ValueError("out_dx must have h's type")
+    dw = torch.empty((K,), dtype=torch.float32, device=dy.device) if want_dw else None
+    if ws is None and want_dw:
+        ws = torch.empty((max(rmsnorm_backward_workspace_bytes(T, K), 256),), dtype=torch.uint8,
+                         device=dy.device)
+    st = _b.lib().mx_rmsnorm_backward(dp, dt, ds, hp, ht, hs, w, _type(weight, "weight"), r, gp, gs,
+                                      T, K, op, os_, _ptr(dw), _ptr(ws),
+                                      0 if ws is None else ws.numel() * ws.element_size(),
+                                      _b._stream())
+    _b._check(st, "mx_rmsnorm_backward")
+    return out_dx, dw
+
+
+def swiglu(gu, fmt=None, want_y: bool = True, stream=None) -> SwiGLUOut:
+    """y = silu(g) * u of gu [T, 2F] = [g | u]: in bf16 (want_y) and / or encoded along its rows
+    (fmt) as the down projection's Fprop operand.  See mx_swiglu."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return swiglu(gu, fmt, want_y)
+    p, t, s = _rows(gu, "gu")
+    T, F2 = gu.shape
+    if F2 % 2:
+        raise ValueError("gu must have an even number of columns")
+    F = F2 // 2
+    y = torch.empty((T, F), dtype=torch.bfloat16, device=gu.device) if want_y else None
+    codes, scales = _encoded(fmt, T, F, gu.device)
+    st = _b.lib().mx_swiglu(p, t, s, T, F, _ptr(y), fmt or 0, _ptr(codes), _ptr(scales),
+                            _b._stream())
+    _b._check(st, "mx_swiglu")
+    return SwiGLUOut(y, codes, scales)
+
+
+def swiglu_backward(dy, gu, out=None, stream=None) -> torch.Tensor:
+    """dgu [T, 2F] in bf16 for y's gradient dy [T, F].  See mx_swiglu_backward."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return swiglu_backward(dy, gu, out)
+    dp, dt, ds = _rows(dy, "dy")
+    T, F = dy.shape
+    gp, gt, gs = _rows(gu, "gu", (T, 2 * F))
+    if out is None:
+        out = torch.empty((T, 2 * F), dtype=torch.bfloat16, device=dy.device)
+    elif tuple(out.shape) != (T, 2 * F) or _type(out, "out") != _BF16:
+        raise ValueError(f"out must be bf16 [{T}, {2 * F}]")
+    st = _b.lib().mx_swiglu_backward(dp, dt, ds, gp, gt, gs, T, F, _b._dev_ptr(out, "out"),
+                                     _b._stream())
+    _b._check(st, "mx_swiglu_backward")
+    return out
+
+
+def grad_workspace_bytes(count: int) -> int:
+    return int(_b.lib().mx_grad_workspace_bytes(count))
+
+
+def _tables(tensors, name: str):
+    """Host arrays (pointers, sizes, types) of contiguous CUDA tensors."""
+    n = len(tensors)
+    return ((ctypes.c_void_p * n)(*[_b._dev_ptr(t, name) for t in tensors]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_int * n)(*[_type(t, name) for t in tensors]))
+
+
+def _grad_buffers(tensors, ws):
+    d = tensors[0].device if tensors else "cuda"
+    norm = torch.empty((1,), dtype=torch.float32, device=d)
+    if ws is None:
+        ws = torch.empty((max(grad_workspace_bytes(len(tensors)), 256),), dtype=torch.uint8, device=d)
+    return norm, ws
+
+
+def grad_norm(tensors, ws=None, stream=None) -> torch.Tensor:
+    """L2 norm over all elements of a list of contiguous bf16 / fp32 CUDA tensors, as a
+    one-element fp32 device tensor.  See mx_grad_norm."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return grad_norm(tensors, ws)
+    tensors = list(tensors)
+    p, n, t = _tables(tensors, "gradient")
+    norm, ws = _grad_buffers(tensors, ws)
+    st = _b.lib().mx_grad_norm(p, n, t, len(tensors), norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _b._stream())
+    _b._check(st, "mx_grad_norm")
+    return norm
+
+
+def clip_grads(tensors, max_norm: float, out=None, eps: float = 1e-6, ws=None,
+               stream=None) -> torch.Tensor:
+    """Scales every gradient by min(1, max_norm / (norm + eps)), norm over all of them: in place, or
+    into the tensors of `out` (same sizes, bf16 or fp32).  Returns the norm before clipping, a
+    one-element fp32 device tensor.  See mx_clip_grads."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return clip_grads(tensors, max_norm, out, eps, ws)
+    tensors = list(tensors)
+    p, n, t = _tables(tensors, "gradient")
+    op = ot = None
+    if out is not None:
+        out = list(out)
+        op, on, ot = _tables(out, "out")
+        if len(out) != len(tensors) or bytes(on) != bytes(n):
+            raise ValueError("out must hold one tensor of the same size for each gradient")
+    norm, ws = _grad_buffers(tensors, ws)
+    st = _b.lib().mx_clip_grads(p, n, t, op, ot, len(tensors), max_norm, eps, norm.data_ptr(),
+                                ws.data_ptr(), ws.numel(), _b._stream())
+    _b._check(st, "mx_clip_grads")
+    return norm

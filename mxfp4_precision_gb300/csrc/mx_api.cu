@@ -3,6 +3,8 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -362,6 +364,77 @@ mx_status linear_impl(int op, const void *a_src, int64_t a_rows, int64_t a_cols,
 }  // namespace
 
 namespace {
+// ---- operators between the GEMMs
+bool valid_type(int t) { return t == MX_TYPE_BF16 || t == MX_TYPE_F32; }
+
+mx_status check_row_sizes(int64_t T, int64_t cols) {
+    if (T < 0 || cols < 0 || T > 0x7FFFFFFF || cols > 0x3FFFFFFF) return MX_ERR_SHAPE;
+    return MX_OK;
+}
+
+// A row-major matrix: 16-byte rows at a pitch that holds them.
+mx_status check_rows(const void *p, int64_t pitch, int64_t cols) {
+    if (p == nullptr) return MX_ERR_INVALID_ARG;
+    if (pitch < cols || pitch > 0x7FFFFFFF) return MX_ERR_SHAPE;
+    if (cols % 8 != 0 || pitch % 8 != 0 || !aligned16(p)) return MX_ERR_ALIGN;
+    return MX_OK;
+}
+
+mx_status check_row_encode(const RowEncode &e, int64_t T, int64_t cols) {
+    if (e.fmt == MX_FORMAT_NONE)
+        return e.codes == nullptr && e.scales == nullptr ? MX_OK : MX_ERR_INVALID_ARG;
+    if (e.fmt != MX_FORMAT_MXFP4 && e.fmt != MX_FORMAT_MXFP8) return MX_ERR_INVALID_ARG;
+    if (cols % 32 != 0) return MX_ERR_SHAPE;
+    if (T == 0 || cols == 0) return MX_OK;
+    if (e.codes == nullptr || e.scales == nullptr) return MX_ERR_INVALID_ARG;
+    return aligned16(e.codes) && aligned16(e.scales) ? MX_OK : MX_ERR_ALIGN;
+}
+
+mx_status grad_impl(const void *const *h_grads, const int64_t *h_sizes, const int *h_types,
+                    void *const *h_outs, const int *h_out_types, int64_t count, bool scale,
+                    float max_norm, float eps, float *d_norm, void *ws, size_t ws_bytes,
+                    cudaStream_t stream) {
+    if (count < 0 || count > (1 << 20)) return MX_ERR_SHAPE;
+    if (d_norm == nullptr) return MX_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(d_norm) & 3u) != 0) return MX_ERR_ALIGN;
+    if (count > 0 && (h_grads == nullptr || h_sizes == nullptr || h_types == nullptr))
+        return MX_ERR_INVALID_ARG;
+    if (h_outs != nullptr && h_out_types == nullptr) return MX_ERR_INVALID_ARG;
+    std::vector<GradTensor> g;
+    try {
+        g.reserve(static_cast<size_t>(count));
+    } catch (const std::bad_alloc &) {
+        return MX_ERR_WORKSPACE;
+    }
+    for (int64_t i = 0; i < count; ++i) {
+        if (!valid_type(h_types[i])) return MX_ERR_INVALID_ARG;
+        if (h_sizes[i] < 0) return MX_ERR_SHAPE;
+        if (h_sizes[i] == 0) continue;
+        GradTensor t{h_grads[i], nullptr, h_sizes[i], h_types[i] == MX_TYPE_F32, false};
+        if (t.p == nullptr) return MX_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(t.p) & (t.f32 ? 3u : 1u)) != 0) return MX_ERR_ALIGN;
+        if (scale) {
+            t.out = h_outs != nullptr ? h_outs[i] : const_cast<void *>(t.p);
+            if (h_outs != nullptr && !valid_type(h_out_types[i])) return MX_ERR_INVALID_ARG;
+            t.out_f32 = h_outs != nullptr ? h_out_types[i] == MX_TYPE_F32 : t.f32;
+            if (t.out == nullptr || (t.out == t.p && t.out_f32 != t.f32)) return MX_ERR_INVALID_ARG;
+            if ((reinterpret_cast<uintptr_t>(t.out) & (t.out_f32 ? 3u : 1u)) != 0)
+                return MX_ERR_ALIGN;
+        }
+        g.push_back(t);
+    }
+    const int64_t n = static_cast<int64_t>(g.size());
+    if (n == 0) return from_cuda(cudaMemsetAsync(d_norm, 0, sizeof(float), stream));
+    if (ws == nullptr || ws_bytes < mx_grad_workspace_bytes(n)) return MX_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MX_ERR_ALIGN;
+    const DeviceInfo *dev = nullptr;
+    const mx_status st = device_or_error(&dev);
+    if (st != MX_OK) return st;
+    return from_cuda(launch_grad_clip(g.data(), n, scale, max_norm, eps, d_norm, ws, *dev, stream));
+}
+}  // namespace
+
+namespace {
 // Names each exported call in profiler timelines (NVTX; free without a tool attached).
 struct TraceRange {
     explicit TraceRange(const char *name) { nvtxRangePushA(name); }
@@ -594,6 +667,126 @@ mx_status mx_linear_wgrad_fused(const void *d_dY, const void *d_X, float *d_dW, 
     return linear_impl(MX_OP_WGRAD, d_dY, T, N, MX_CONTRACT_ROWS, d_X, T, K, MX_CONTRACT_ROWS,
                        d_dW, T, N, K, rot, rot_block, rnd, seed, d_ws, ws_bytes,
                        static_cast<cudaStream_t>(stream), true);
+}
+
+mx_status mx_rmsnorm(const void *d_x, int x_type, int64_t x_pitch, const void *d_res, int res_type,
+                     int64_t res_pitch, const void *d_w, int w_type, float eps, int64_t T,
+                     int64_t K, void *d_h, int64_t h_pitch, void *d_y, int format, void *d_codes,
+                     void *d_scales, float *d_rstd, void *stream) {
+    TraceRange trace("mx_rmsnorm");
+    if (!valid_type(x_type) || !valid_type(w_type) || !(eps >= 0.0f)) return MX_ERR_INVALID_ARG;
+    if (d_res != nullptr && !valid_type(res_type)) return MX_ERR_INVALID_ARG;
+    if (d_res == nullptr && d_h != nullptr) return MX_ERR_INVALID_ARG;
+    mx_status st = check_row_sizes(T, K);
+    if (st != MX_OK) return st;
+    const RowEncode e{format, d_codes, d_scales};
+    if ((st = check_row_encode(e, T, K)) != MX_OK || T == 0 || K == 0) return st;
+    if (d_w == nullptr) return MX_ERR_INVALID_ARG;
+    if ((st = check_rows(d_x, x_pitch, K)) != MX_OK) return st;
+    if (d_res != nullptr && (st = check_rows(d_res, res_pitch, K)) != MX_OK) return st;
+    if (d_h != nullptr && (st = check_rows(d_h, h_pitch, K)) != MX_OK) return st;
+    if (!aligned16(d_w) || !aligned16(d_y) || !aligned16(d_rstd)) return MX_ERR_ALIGN;
+    if (K > MX_ROW_COLUMNS_MAX) return MX_ERR_UNSUPPORTED;
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_rmsnorm({d_x, x_pitch, x_type == MX_TYPE_F32},
+                                    {d_res, res_pitch, res_type == MX_TYPE_F32}, d_w,
+                                    w_type == MX_TYPE_F32, eps, T, K, d_h, h_pitch, d_y, e, d_rstd,
+                                    *dev, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_rmsnorm_backward_workspace_bytes(int64_t T, int64_t K) {
+    if (T <= 0 || K <= 0 || K > MX_ROW_COLUMNS_MAX) return 0;
+    return align256(rmsnorm_backward_ws(T, K));
+}
+
+mx_status mx_rmsnorm_backward(const void *d_dy, int dy_type, int64_t dy_pitch, const void *d_h,
+                              int h_type, int64_t h_pitch, const void *d_w, int w_type,
+                              const float *d_rstd, const void *d_dres, int64_t dres_pitch,
+                              int64_t T, int64_t K, void *d_dx, int64_t dx_pitch, float *d_dw,
+                              void *d_ws, size_t ws_bytes, void *stream) {
+    TraceRange trace("mx_rmsnorm_backward");
+    if (!valid_type(dy_type) || !valid_type(h_type) || !valid_type(w_type))
+        return MX_ERR_INVALID_ARG;
+    mx_status st = check_row_sizes(T, K);
+    if (st != MX_OK || K == 0) return st;
+    if (!aligned16(d_dw)) return MX_ERR_ALIGN;
+    if (T == 0)
+        return d_dw == nullptr ? MX_OK
+                               : from_cuda(cudaMemsetAsync(d_dw, 0, static_cast<size_t>(K) * sizeof(float),
+                                                           static_cast<cudaStream_t>(stream)));
+    if (d_w == nullptr || d_rstd == nullptr) return MX_ERR_INVALID_ARG;
+    if ((st = check_rows(d_dy, dy_pitch, K)) != MX_OK) return st;
+    if ((st = check_rows(d_h, h_pitch, K)) != MX_OK) return st;
+    if ((st = check_rows(d_dx, dx_pitch, K)) != MX_OK) return st;
+    if (d_dres != nullptr && (st = check_rows(d_dres, dres_pitch, K)) != MX_OK) return st;
+    if (!aligned16(d_w) || !aligned16(d_rstd)) return MX_ERR_ALIGN;
+    if (K > MX_ROW_COLUMNS_MAX) return MX_ERR_UNSUPPORTED;
+    if (d_dw != nullptr) {
+        if (d_ws == nullptr || ws_bytes < mx_rmsnorm_backward_workspace_bytes(T, K))
+            return MX_ERR_WORKSPACE;
+        if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return MX_ERR_ALIGN;
+    }
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_rmsnorm_backward(
+        {d_dy, dy_pitch, dy_type == MX_TYPE_F32}, {d_h, h_pitch, h_type == MX_TYPE_F32}, d_w,
+        w_type == MX_TYPE_F32, d_rstd, {d_dres, dres_pitch, h_type == MX_TYPE_F32}, T, K, d_dx,
+        dx_pitch, d_dw, d_ws, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_swiglu(const void *d_gu, int gu_type, int64_t gu_pitch, int64_t T, int64_t F,
+                    void *d_y, int format, void *d_codes, void *d_scales, void *stream) {
+    TraceRange trace("mx_swiglu");
+    if (!valid_type(gu_type)) return MX_ERR_INVALID_ARG;
+    mx_status st = check_row_sizes(T, F);
+    if (st != MX_OK) return st;
+    const RowEncode e{format, d_codes, d_scales};
+    if ((st = check_row_encode(e, T, F)) != MX_OK || T == 0 || F == 0) return st;
+    if ((st = check_rows(d_gu, gu_pitch, 2 * F)) != MX_OK) return st;
+    if (F % 8 != 0 || !aligned16(d_y)) return MX_ERR_ALIGN;
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_swiglu({d_gu, gu_pitch, gu_type == MX_TYPE_F32}, T, F, d_y, e, *dev,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_swiglu_backward(const void *d_dy, int dy_type, int64_t dy_pitch, const void *d_gu,
+                             int gu_type, int64_t gu_pitch, int64_t T, int64_t F, void *d_dgu,
+                             void *stream) {
+    TraceRange trace("mx_swiglu_backward");
+    if (!valid_type(dy_type) || !valid_type(gu_type)) return MX_ERR_INVALID_ARG;
+    mx_status st = check_row_sizes(T, F);
+    if (st != MX_OK || T == 0 || F == 0) return st;
+    if ((st = check_rows(d_dy, dy_pitch, F)) != MX_OK) return st;
+    if ((st = check_rows(d_gu, gu_pitch, 2 * F)) != MX_OK) return st;
+    if (d_dgu == nullptr) return MX_ERR_INVALID_ARG;
+    if (F % 8 != 0 || !aligned16(d_dgu)) return MX_ERR_ALIGN;
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_swiglu_backward({d_dy, dy_pitch, dy_type == MX_TYPE_F32},
+                                            {d_gu, gu_pitch, gu_type == MX_TYPE_F32}, T, F, d_dgu,
+                                            *dev, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_grad_workspace_bytes(int64_t count) {
+    return count <= 0 ? 0 : align256(grad_ws(count));
+}
+
+mx_status mx_grad_norm(const void *const *h_grads, const int64_t *h_sizes, const int *h_types,
+                       int64_t count, float *d_norm, void *d_ws, size_t ws_bytes, void *stream) {
+    TraceRange trace("mx_grad_norm");
+    return grad_impl(h_grads, h_sizes, h_types, nullptr, nullptr, count, false, 0.0f, 0.0f, d_norm,
+                     d_ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+mx_status mx_clip_grads(const void *const *h_grads, const int64_t *h_sizes, const int *h_types,
+                        void *const *h_outs, const int *h_out_types, int64_t count, float max_norm,
+                        float eps, float *d_norm, void *d_ws, size_t ws_bytes, void *stream) {
+    TraceRange trace("mx_clip_grads");
+    if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return MX_ERR_INVALID_ARG;
+    return grad_impl(h_grads, h_sizes, h_types, h_outs, h_out_types, count, true, max_norm, eps,
+                     d_norm, d_ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 mx_status mx_check_status(void *stream) {

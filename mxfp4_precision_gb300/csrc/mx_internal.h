@@ -98,4 +98,45 @@ cudaError_t launch_wgrad_fused(const void *dY, const void *X, float *dW, int64_t
                                void *Bs, void *counters, const DeviceInfo &dev,
                                cudaStream_t stream);
 
+// ---- row operators between the GEMMs (mx_norm.cu, mx_glu.cu)
+// A row-major input: pitch in elements, f32 or bf16.
+struct RowIn {
+    const void *p;
+    int64_t pitch;
+    bool f32;
+};
+// Encoded output along the rows (mx_format values), or none.
+enum : int { kEncNone = 0, kEncMX4 = 1, kEncMX8 = 2 };
+struct RowEncode {
+    int fmt;
+    void *codes, *scales;
+};
+// h (the stream, when res.p is given; may be null), y (bf16, may be null) and the encoded y.
+cudaError_t launch_rmsnorm(const RowIn &x, const RowIn &res, const void *w, int w_f32, float eps,
+                           int64_t T, int64_t K, void *h, int64_t h_pitch, void *y,
+                           const RowEncode &e, float *rstd, const DeviceInfo &dev,
+                           cudaStream_t stream);
+size_t rmsnorm_backward_ws(int64_t T, int64_t K);
+cudaError_t launch_rmsnorm_backward(const RowIn &dy, const RowIn &h, const void *w, int w_f32,
+                                    const float *rstd, const RowIn &dres, int64_t T, int64_t K,
+                                    void *dx, int64_t dx_pitch, float *dw, void *ws,
+                                    const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_swiglu(const RowIn &gu, int64_t T, int64_t F, void *y, const RowEncode &e,
+                          const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const RowIn &dy, const RowIn &gu, int64_t T, int64_t F,
+                                   void *dgu, const DeviceInfo &dev, cudaStream_t stream);
+
+// ---- gradient norm and clipping (mx_grad.cu)
+struct GradTensor {
+    const void *p;
+    void *out;  // null: norm only
+    int64_t n;
+    bool f32, out_f32;
+};
+size_t grad_ws(int64_t count);
+// scale == false: the norm alone.
+cudaError_t launch_grad_clip(const GradTensor *t, int64_t count, bool scale, float max_norm,
+                             float eps, float *norm, void *ws, const DeviceInfo &dev,
+                             cudaStream_t stream);
+
 }  // namespace mx
