@@ -10,7 +10,8 @@ that what is allocated belongs to it.
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
+from operator import attrgetter
 from typing import NamedTuple, Optional
 
 import torch
@@ -36,6 +37,12 @@ class SwiGLUOut(NamedTuple):
     y: Optional[torch.Tensor]
     codes: Optional[torch.Tensor]
     scales: Optional[torch.Tensor]
+
+
+def _stream(t: torch.Tensor) -> int:
+    """The current stream of t's device, as torch's own launches look it up (torch.cuda.current_stream
+    builds a Stream object first: 3 us of a call of 20)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _type(t: torch.Tensor, name: str) -> int:
@@ -109,7 +116,7 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-5, fmt=None, want_y: bool 
     rstd = torch.empty((T,), dtype=torch.float32, device=d)
     st = _b.lib().mx_rmsnorm(xp, xt, xs, rp, rt, rs, w, _type(weight, "weight"), eps, T, K, _ptr(h),
                              hs, _ptr(y), fmt or 0, _ptr(codes), _ptr(scales), rstd.data_ptr(),
-                             _b._stream())
+                             _stream(x))
     _b._check(st, "mx_rmsnorm")
     return RMSNormOut(h, y, codes, scales, rstd)
 
@@ -150,7 +157,7 @@ def rmsnorm_backward(dy, h, weight, rstd, dres=None, want_dw: bool = True, ws=No
     st = _b.lib().mx_rmsnorm_backward(dp, dt, ds, hp, ht, hs, w, _type(weight, "weight"), r, gp, gs,
                                       T, K, op, os_, _ptr(dw), _ptr(ws),
                                       0 if ws is None else ws.numel() * ws.element_size(),
-                                      _b._stream())
+                                      _stream(dy))
     _b._check(st, "mx_rmsnorm_backward")
     return out_dx, dw
 
@@ -169,7 +176,7 @@ def swiglu(gu, fmt=None, want_y: bool = True, stream=None) -> SwiGLUOut:
     y = torch.empty((T, F), dtype=torch.bfloat16, device=gu.device) if want_y else None
     codes, scales = _encoded(fmt, T, F, gu.device)
     st = _b.lib().mx_swiglu(p, t, s, T, F, _ptr(y), fmt or 0, _ptr(codes), _ptr(scales),
-                            _b._stream())
+                            _stream(gu))
     _b._check(st, "mx_swiglu")
     return SwiGLUOut(y, codes, scales)
 
@@ -187,7 +194,7 @@ def swiglu_backward(dy, gu, out=None, stream=None) -> torch.Tensor:
     elif tuple(out.shape) != (T, 2 * F) or _type(out, "out") != _BF16:
         raise ValueError(f"out must be bf16 [{T}, {2 * F}]")
     st = _b.lib().mx_swiglu_backward(dp, dt, ds, gp, gt, gs, T, F, _b._dev_ptr(out, "out"),
-                                     _b._stream())
+                                     _stream(dy))
     _b._check(st, "mx_swiglu_backward")
     return out
 
@@ -196,12 +203,26 @@ def grad_workspace_bytes(count: int) -> int:
     return int(_b.lib().mx_grad_workspace_bytes(count))
 
 
+_DATA_PTR, _NUMEL, _IS_CONTIGUOUS = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
+_IS_CUDA, _DTYPE = attrgetter("is_cuda"), attrgetter("dtype")
+
+
 def _tables(tensors, name: str):
-    """Host arrays (pointers, sizes, types) of contiguous CUDA tensors."""
-    n = len(tensors)
-    return ((ctypes.c_void_p * n)(*[_b._dev_ptr(t, name) for t in tensors]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int * n)(*[_type(t, name) for t in tensors]))
+    """Host arrays (pointers, sizes, types) of contiguous CUDA tensors: one pass of `map` for each, a
+    third of the time of a loop over the tensors."""
+    if not all(map(_IS_CUDA, tensors)):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not all(map(_IS_CONTIGUOUS, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    try:
+        types = array("i", map(_TYPES.__getitem__, map(_DTYPE, tensors)))
+    except KeyError:
+        raise ValueError(f"{name} must be bf16 (torch.bfloat16 or raw 16-bit patterns) or float32") from None
+    return array("Q", map(_DATA_PTR, tensors)), array("q", map(_NUMEL, tensors)), types
+
+
+def _at(a):
+    return None if a is None else a.buffer_info()[0]
 
 
 def _grad_buffers(tensors, ws):
@@ -221,8 +242,8 @@ def grad_norm(tensors, ws=None, stream=None) -> torch.Tensor:
     tensors = list(tensors)
     p, n, t = _tables(tensors, "gradient")
     norm, ws = _grad_buffers(tensors, ws)
-    st = _b.lib().mx_grad_norm(p, n, t, len(tensors), norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                               _b._stream())
+    st = _b.lib().mx_grad_norm(_at(p), _at(n), _at(t), len(tensors), norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _stream(norm))
     _b._check(st, "mx_grad_norm")
     return norm
 
@@ -241,10 +262,10 @@ def clip_grads(tensors, max_norm: float, out=None, eps: float = 1e-6, ws=None,
     if out is not None:
         out = list(out)
         op, on, ot = _tables(out, "out")
-        if len(out) != len(tensors) or bytes(on) != bytes(n):
+        if on != n:
             raise ValueError("out must hold one tensor of the same size for each gradient")
     norm, ws = _grad_buffers(tensors, ws)
-    st = _b.lib().mx_clip_grads(p, n, t, op, ot, len(tensors), max_norm, eps, norm.data_ptr(),
-                                ws.data_ptr(), ws.numel(), _b._stream())
+    st = _b.lib().mx_clip_grads(_at(p), _at(n), _at(t), _at(op), _at(ot), len(tensors), max_norm, eps, norm.data_ptr(),
+                                ws.data_ptr(), ws.numel(), _stream(norm))
     _b._check(st, "mx_clip_grads")
     return norm

@@ -15,67 +15,151 @@ namespace {
 
 using namespace rows;
 
+// 1 / (1 + exp(-g)) from the hardware's 2^x and reciprocal.  Their errors (2 and
+// 1 units in the last place) and the rounded product g log2 e leave the
+// sigmoid within (5 + |g|) u, u = 2^-24: far inside both outputs' roundings,
+// and the limits come out by themselves (0 for an exponential that overflows, 1
+// for one that vanishes, NaN for NaN).  expf and a division instead take 54
+// instructions an element, which bounds the kernel (bf16 in, 8192 x 14336: 171
+// us against 87 us for the memory).
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -0x1.715476p+0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0x1p-10f, 0x1p-10f)));
+    return r * 0x1p-10f;  // the reciprocal itself stays normal
+}
+
+// Both kernels: a block is `deep` rows by `wide` chunks of 8 columns (a
+// multiple of 32 threads), `segments` blocks side by side make a row; each
+// thread keeps its columns and takes `turns` rows, two at a time.
 struct GluArgs {
     const uint8_t *gu, *dy;
-    int64_t gu_pitch, dy_pitch;
-    Out y;  // y [T][F], or dgu [T][2F]
+    int64_t gu_pitch, dy_pitch;  // bytes
+    Out y;                       // y [T][F], or dgu [T][2F]
     Encoded enc;
-    int64_t T, F;
-    int64_t chunks;  // chunks of 8 columns per row, padded to a multiple of 32
-    int64_t total;   // chunks over all rows (padded rows included when encoding)
+    int64_t T;
+    uint32_t F;
+    int wide, segments, turns;
+    uint32_t tiles;  // blocks that hold rows; those after them zero the scales' padding lines
+    bool aligned32;
     int *status;
 };
+
+struct Place {
+    int64_t row, end;  // rows row, row + deep, ... below end
+    int deep;
+    uint32_t c;
+};
+__device__ __forceinline__ Place place(const GluArgs &p) {
+    const uint32_t band = blockIdx.x / p.segments, r = threadIdx.x / p.wide;
+    Place at;
+    at.deep = blockDim.x / p.wide;
+    at.row = static_cast<int64_t>(band) * at.deep * p.turns + r;
+    at.end = min(p.T, (static_cast<int64_t>(band) + 1) * at.deep * p.turns);
+    at.c = (blockIdx.x - band * p.segments) * p.wide + (threadIdx.x - r * p.wide);
+    return at;
+}
 
 template <typename G>
 __global__ void __launch_bounds__(256) mx_swiglu_kernel(const __grid_constant__ GluArgs p) {
     griddep_wait();
     griddep_launch_dependents();
-    // total is a multiple of 32: whole warps take part.
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (at >= p.total) return;
-    const int64_t row = at / p.chunks, c = at % p.chunks, col = 8 * c;
-    const bool in = row < p.T && col < p.F;
-    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (in) {
-        Raw8<G> gr, ur;
-        const uint8_t *src = p.gu + (row * p.gu_pitch + col) * G::kBytes;
-        load8(gr, src);
-        load8(ur, src + p.F * G::kBytes);
-        float g[8], u[8];
-        to_f32(gr, g);
-        to_f32(ur, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
-        if (p.y.p != nullptr) store8<BF16>(p.y, row * p.F + col, y, p.status);
+    if (blockIdx.x >= p.tiles) {
+        zero_padding(p.enc, p.T, static_cast<int64_t>(blockIdx.x - p.tiles) * blockDim.x + threadIdx.x,
+                     static_cast<int64_t>(gridDim.x - p.tiles) * blockDim.x, p.status);
+        return;
     }
-    if (p.enc.fmt != kEncNone) encode8(p.enc, row, row < p.T ? p.F : 0, c, y, p.status);
+    const Place at = place(p);
+    const uint32_t col = 8 * at.c;
+    const bool in = col < p.F;
+    const uint8_t *src = p.gu + static_cast<size_t>(col) * G::kBytes;
+    const size_t up = static_cast<size_t>(p.F) * G::kBytes;
+    // Whole warps share a row, so that its blocks are encoded together.
+    for (int64_t row = at.row; row < at.end; row += 2 * at.deep) {
+        Raw8<G> gr[2], ur[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t r = row + k * at.deep;
+            zero8(gr[k]);
+            zero8(ur[k]);
+            if (in && r < at.end) {
+                load8(gr[k], src + r * p.gu_pitch, p.aligned32);
+                load8(ur[k], src + r * p.gu_pitch + up, p.aligned32);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t r = row + k * at.deep;
+            if (r >= at.end) break;
+            float g[8], u[8];
+            floats_of(to_v8(gr[k]), g);
+            floats_of(to_v8(ur[k]), u);
+            V8 y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y.v[i] = pack2(g[2 * i] * sigmoid(g[2 * i]) * u[2 * i],
+                               g[2 * i + 1] * sigmoid(g[2 * i + 1]) * u[2 * i + 1]);
+            if (in && p.y.p != nullptr)
+                store8<BF16>(p.y, p.y.p + (r * p.F + col) * 2, y, p.aligned32, p.status);
+            if (p.enc.fmt != kEncNone && at.c < p.enc.katoms * 16)
+                encode8(p.enc, encoded_row(p.enc, r), at.c, in, y, p.status);
+        }
+    }
 }
 
 template <typename D, typename G>
 __global__ void __launch_bounds__(256) mx_swiglu_backward_kernel(const __grid_constant__ GluArgs p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (at >= p.total) return;
-    const int64_t row = at / p.chunks, col = 8 * (at % p.chunks);
-    Raw8<G> gr, ur;
-    Raw8<D> dr;
-    const uint8_t *src = p.gu + (row * p.gu_pitch + col) * G::kBytes;
-    load8(dr, p.dy + (row * p.dy_pitch + col) * D::kBytes);
-    load8(gr, src);
-    load8(ur, src + p.F * G::kBytes);
-    float g[8], u[8], d[8];
-    to_f32(dr, d);
-    to_f32(gr, g);
-    to_f32(ur, u);
+    const Place at = place(p);
+    const uint32_t col = 8 * at.c;
+    if (col >= p.F) return;
+    const uint8_t *src = p.gu + static_cast<size_t>(col) * G::kBytes;
+    const uint8_t *dsrc = p.dy + static_cast<size_t>(col) * D::kBytes;
+    const size_t up = static_cast<size_t>(p.F) * G::kBytes;
+    for (int64_t row = at.row; row < at.end; row += at.deep) {
+        Raw8<G> gr, ur;
+        Raw8<D> dr;
+        load8(dr, dsrc + row * p.dy_pitch, p.aligned32);
+        load8(gr, src + row * p.gu_pitch, p.aligned32);
+        load8(ur, src + row * p.gu_pitch + up, p.aligned32);
+        float g[8], u[8], d[8];
+        floats_of(to_v8(gr), g);
+        floats_of(to_v8(ur), u);
+        floats_of(to_v8(dr), d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float s = 1.0f / (1.0f + expf(-g[i])), ds = d[i] * s;
-        u[i] = ds * u[i] * (1.0f + g[i] * (1.0f - s));
-        d[i] = ds * g[i];
+        for (int i = 0; i < 8; ++i) {
+            const float s = sigmoid(g[i]), ds = d[i] * s;
+            u[i] = ds * u[i] * fmaf(g[i], 1.0f - s, 1.0f);
+            d[i] = ds * g[i];
+        }
+        V8 dg, du;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dg.v[i] = pack2(u[2 * i], u[2 * i + 1]);
+            du.v[i] = pack2(d[2 * i], d[2 * i + 1]);
+        }
+        uint8_t *dst = p.y.p + (row * 2 * p.F + col) * 2;
+        store8<BF16>(p.y, dst, dg, p.aligned32, p.status);
+        store8<BF16>(p.y, dst + 2 * static_cast<size_t>(p.F), du, p.aligned32, p.status);
     }
-    store8<BF16>(p.y, row * 2 * p.F + col, u, p.status);
-    store8<BF16>(p.y, row * 2 * p.F + p.F + col, d, p.status);
+}
+
+// Tiles of rows whose `chunks` are cut into equal segments of at most 256; several
+// rows a thread once there are blocks enough for every SM to hold `kWaves` full turns.
+constexpr int64_t kWaves = 4;
+bool shape(GluArgs &p, int64_t chunks, int64_t pad_words, int most, const DeviceInfo &dev,
+           int64_t *grid, int *threads) {
+    p.segments = static_cast<int>((chunks + 255) / 256);
+    p.wide = static_cast<int>(((chunks + p.segments - 1) / p.segments + 31) / 32 * 32);
+    const int deep = 256 / p.wide;
+    *threads = p.wide * deep;
+    p.turns = most;
+    auto tiles = [&] { return (p.T + deep * p.turns - 1) / (deep * p.turns) * p.segments; };
+    while (p.turns > 1 && tiles() < kWaves * 8 * dev.sm_count) p.turns /= 2;
+    *grid = tiles() + (pad_words + *threads - 1) / *threads;
+    p.tiles = static_cast<uint32_t>(tiles());
+    return *grid <= 0x7FFFFFFF;
 }
 
 }  // namespace
@@ -84,40 +168,41 @@ cudaError_t launch_swiglu(const RowIn &gu, int64_t T, int64_t F, void *y, const 
                           const DeviceInfo &dev, cudaStream_t stream) {
     GluArgs p{};
     p.gu = static_cast<const uint8_t *>(gu.p);
-    p.gu_pitch = gu.pitch;
+    p.gu_pitch = gu.pitch * (gu.f32 ? 4 : 2);
     p.y = {static_cast<uint8_t *>(y), static_cast<size_t>(T) * F * 2};
     p.enc = row_encoded(e, T, F);
     p.T = T;
-    p.F = F;
-    p.chunks = (F + 255) / 256 * 32;
-    p.total = (e.fmt != kEncNone ? 128 * scale_groups(T) : T) * p.chunks;
+    p.F = static_cast<uint32_t>(F);
+    p.aligned32 = aligned32(gu.p);
     p.status = dev.status;
-    const int64_t grid = (p.total + 255) / 256;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    return gu.f32 ? launch_dependent(mx_swiglu_kernel<F32>, grid, 256, stream, p)
-                  : launch_dependent(mx_swiglu_kernel<BF16>, grid, 256, stream, p);
+    int64_t grid = 0;
+    int threads = 0;
+    if (!shape(p, (F + 255) / 256 * 32, padding_words(p.enc, T), 4, dev, &grid, &threads))
+        return cudaErrorInvalidValue;
+    return gu.f32 ? launch_dependent(mx_swiglu_kernel<F32>, grid, threads, 0, stream, p)
+                  : launch_dependent(mx_swiglu_kernel<BF16>, grid, threads, 0, stream, p);
 }
 
 cudaError_t launch_swiglu_backward(const RowIn &dy, const RowIn &gu, int64_t T, int64_t F,
                                    void *dgu, const DeviceInfo &dev, cudaStream_t stream) {
     GluArgs p{};
     p.dy = static_cast<const uint8_t *>(dy.p);
-    p.dy_pitch = dy.pitch;
+    p.dy_pitch = dy.pitch * (dy.f32 ? 4 : 2);
     p.gu = static_cast<const uint8_t *>(gu.p);
-    p.gu_pitch = gu.pitch;
+    p.gu_pitch = gu.pitch * (gu.f32 ? 4 : 2);
     p.y = {static_cast<uint8_t *>(dgu), static_cast<size_t>(T) * F * 4};
     p.T = T;
-    p.F = F;
-    p.chunks = F / 8;
-    p.total = T * p.chunks;
+    p.F = static_cast<uint32_t>(F);
+    p.aligned32 = aligned32(dy.p) && aligned32(gu.p);
     p.status = dev.status;
-    const int64_t grid = (p.total + 255) / 256;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    int64_t grid = 0;
+    int threads = 0;
+    if (!shape(p, F / 8, 0, 1, dev, &grid, &threads)) return cudaErrorInvalidValue;
     if (dy.f32)
-        return gu.f32 ? launch_dependent(mx_swiglu_backward_kernel<F32, F32>, grid, 256, stream, p)
-                      : launch_dependent(mx_swiglu_backward_kernel<F32, BF16>, grid, 256, stream, p);
-    return gu.f32 ? launch_dependent(mx_swiglu_backward_kernel<BF16, F32>, grid, 256, stream, p)
-                  : launch_dependent(mx_swiglu_backward_kernel<BF16, BF16>, grid, 256, stream, p);
+        return gu.f32 ? launch_dependent(mx_swiglu_backward_kernel<F32, F32>, grid, threads, 0, stream, p)
+                      : launch_dependent(mx_swiglu_backward_kernel<F32, BF16>, grid, threads, 0, stream, p);
+    return gu.f32 ? launch_dependent(mx_swiglu_backward_kernel<BF16, F32>, grid, threads, 0, stream, p)
+                  : launch_dependent(mx_swiglu_backward_kernel<BF16, BF16>, grid, threads, 0, stream, p);
 }
 
 }  // namespace mx

@@ -5,8 +5,8 @@
 //
 // The tensors' addresses and sizes travel as kernel parameters, so a call
 // needs no table in device memory and can be captured in a graph.  Sums run
-// in fp32 per thread and in fp64 across threads and blocks, in an order that
-// the sizes alone fix (no atomics): the same inputs give the same bits.
+// in fp32 per thread and in pairs of fp32 across threads and blocks, in an order
+// that the sizes alone fix (no atomics): the same inputs give the same bits.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -20,9 +20,12 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 256;
-constexpr int kGrid = 608;          // four blocks for each of 152 SMs
-constexpr int64_t kChunk = 8192;    // elements a block takes at a time
+constexpr int kGrid = 608;          // blocks at most: four for each of 152 SMs
 constexpr int kMostTensors = 1024;  // per launch (the table is a kernel parameter)
+constexpr int kUnroll = 4;          // 16-byte or element loads a thread has in flight
+// Elements a block takes at a time: large ones cost fewer table searches, small
+// ones spread a few small tensors over more SMs.
+constexpr int64_t kChunk = 8192, kSmallChunk = 2048;
 
 template <int N>
 struct Table {
@@ -32,11 +35,13 @@ struct Table {
     uint32_t first[N + 1];  // first chunk of each tensor
     uint8_t f32[N], out_f32[N];
     int count;
+    int chunk;
 };
 
 struct Piece {
     int tensor;
-    int64_t begin, len;  // elements of the tensor
+    int64_t begin;
+    int len;
 };
 
 template <int N>
@@ -49,83 +54,127 @@ __device__ __forceinline__ Piece piece_of(const Table<N> &t, uint32_t chunk) {
     }
     Piece r;
     r.tensor = lo;
-    r.begin = static_cast<int64_t>(chunk - t.first[lo]) * kChunk;
+    r.begin = static_cast<int64_t>(chunk - t.first[lo]) * t.chunk;
     const int64_t left = t.n[lo] - r.begin;
-    r.len = left < kChunk ? left : kChunk;
+    r.len = static_cast<int>(left < t.chunk ? left : t.chunk);
     return r;
 }
 
-__device__ __forceinline__ float load1(const uint8_t *p, bool f32, int64_t i) {
-    return f32 ? reinterpret_cast<const float *>(p)[i]
-               : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << 16);
+template <typename T>
+__device__ __forceinline__ float load1(const uint8_t *p, int i) {
+    if constexpr (T::kBytes == 4) return reinterpret_cast<const float *>(p)[i];
+    else return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << 16);
+}
+template <typename T>
+__device__ __forceinline__ void store1(const Out &o, uint8_t *p, int i, float v, int *status) {
+    uint8_t *d = p + static_cast<size_t>(i) * T::kBytes;
+    if (!MX_STORE_OK(d, T::kBytes, o.p, o.bytes, status)) return;
+    if constexpr (T::kBytes == 4) *reinterpret_cast<float *>(d) = v;
+    else *reinterpret_cast<uint16_t *>(d) = static_cast<uint16_t>(bf16x2(v, 0.0f));
 }
 
-// Sum over the block in fp64, the same value in every thread.
-__device__ __forceinline__ double sum_block(double v, double *part) {
+// A piece of a tensor in three parts: elements up to the first boundary of a
+// vector of 8 (16 bytes of bf16, 32 of fp32), such vectors, elements after them.
+struct Parts {
+    int head, whole;
+};
+template <typename T>
+__device__ __forceinline__ Parts parts_of(const uint8_t *p, int len) {
+    Parts r;
+    constexpr uint32_t kLast = 8 * T::kBytes - 1;
+    r.head = static_cast<int>((kLast + 1 - (reinterpret_cast<uintptr_t>(p) & kLast)) & kLast) / T::kBytes;
+    if (r.head > len) r.head = len;
+    r.whole = (len - r.head) / 8;
+    return r;
+}
+
+// A sum as an fp32 value and what its roundings left out (Knuth's two-sum):
+// about 48 bits.  fp64 would do, but a block's few fp64 additions take longer
+// here than the rest of a small call (2 lanes a clock and SM).
+struct Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum add(const Sum &a, const Sum &b) {
+    const float s = a.hi + b.hi, bb = s - a.hi;
+    const float e = (a.hi - (s - bb)) + (b.hi - bb) + (a.lo + b.lo);
+    const float t = s + e;
+    if (!isfinite(t)) return {s, 0.0f};
+    return {t, e - (t - s)};
+}
+
+// Sum over the block, the same value in every thread.
+__device__ __forceinline__ Sum sum_block(Sum v, Sum *part) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = 16; o > 0; o >>= 1)
+        v = add(v, {__shfl_xor_sync(0xFFFFFFFFu, v.hi, o), __shfl_xor_sync(0xFFFFFFFFu, v.lo, o)});
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) v += part[i];
+    v = part[threadIdx.x & 7];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+        v = add(v, {__shfl_xor_sync(0xFFFFFFFFu, v.hi, o), __shfl_xor_sync(0xFFFFFFFFu, v.lo, o)});
     return v;
 }
 
 template <typename T>
-__device__ __forceinline__ float sum_squares(const uint8_t *p, int64_t len) {
-    float s = 0.0f;
-    const int64_t whole = len / 8;
-    for (int64_t i = threadIdx.x; i < whole; i += kThreads) {
-        Raw8<T> r;
-        load8(r, p + i * 8 * T::kBytes);
-        float v[8];
-        to_f32(r, v);
+__device__ __forceinline__ float sum_squares(const uint8_t *p, int len) {
+    const Parts q = parts_of<T>(p, len);
+    const int tail = q.head + 8 * q.whole, t = threadIdx.x;
+    float ends = 0.0f;
+    if (t < q.head) ends = load1<T>(p, t);
+    ends *= ends;
+    if (t < len - tail) {
+        const float v = load1<T>(p, tail + t);
+        ends = fmaf(v, v, ends);
+    }
+    const uint8_t *body = p + q.head * T::kBytes;
+    uint64_t body2[kUnroll] = {};
+    for (int i = t; i < q.whole; i += kUnroll * kThreads) {
+        Raw8<T> r[kUnroll];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
+        for (int k = 0; k < kUnroll; ++k) {
+            zero8(r[k]);
+            // default cache policy: the scaling pass reads the last of this again
+            if (i + k * kThreads < q.whole)
+                load8_again(r[k], body + static_cast<int64_t>(i + k * kThreads) * 8 * T::kBytes);
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const V8 v = to_v8(r[k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) body2[k] = fma2(v.v[j], v.v[j], body2[k]);
+        }
     }
-    for (int64_t i = whole * 8 + threadIdx.x; i < len; i += kThreads) {
-        const float v = load1(p, T::kBytes == 4, i);
-        s = fmaf(v, v, s);
-    }
-    return s;
+    return ends + sum2(add2(add2(body2[0], body2[1]), add2(body2[2], body2[3])));
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) mx_grad_sums_kernel(const __grid_constant__ Table<N> t,
-                                                                double *sums) {
-    __shared__ double part[kThreads / 32];
+                                                                Sum *sums) {
+    __shared__ Sum part[kThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
-    double s = 0.0;
+    float s = 0.0f;
     for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         const Piece q = piece_of(t, c);
         const bool f32 = t.f32[q.tensor] != 0;
         const uint8_t *p = t.p[q.tensor] + q.begin * (f32 ? 4 : 2);
-        float v = 0.0f;
-        if (reinterpret_cast<uintptr_t>(p) & 15u) {
-            for (int64_t i = threadIdx.x; i < q.len; i += kThreads) {
-                const float g = load1(p, f32, i);
-                v = fmaf(g, g, v);
-            }
-        } else {
-            v = f32 ? sum_squares<F32>(p, q.len) : sum_squares<BF16>(p, q.len);
-        }
-        s += static_cast<double>(v);
+        s += f32 ? sum_squares<F32>(p, q.len) : sum_squares<BF16>(p, q.len);
     }
-    s = sum_block(s, part);
-    if (threadIdx.x == 0) sums[blockIdx.x] = s;
+    const Sum all = sum_block({s, 0.0f}, part);
+    if (threadIdx.x == 0) sums[blockIdx.x] = all;
 }
 
 // The norm from the blocks' sums (every block computes the same value).
-__device__ __forceinline__ float norm_of(const double *sums, int64_t n, double *part) {
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) s += sums[i];
-    return static_cast<float>(sqrt(sum_block(s, part)));
+__device__ __forceinline__ float norm_of(const Sum *sums, int n, Sum *part) {
+    Sum s{0.0f, 0.0f};
+    for (int i = threadIdx.x; i < n; i += kThreads) s = add(s, sums[i]);
+    return __fsqrt_rn(sum_block(s, part).hi);
 }
 
-__global__ void __launch_bounds__(kThreads) mx_grad_norm_kernel(const double *sums, int64_t n,
+__global__ void __launch_bounds__(kThreads) mx_grad_norm_kernel(const Sum *sums, int n,
                                                                 float *norm) {
-    __shared__ double part[kThreads / 32];
+    __shared__ Sum part[kThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
     const float v = norm_of(sums, n, part);
@@ -133,111 +182,146 @@ __global__ void __launch_bounds__(kThreads) mx_grad_norm_kernel(const double *su
 }
 
 template <typename T, typename O>
-__device__ __forceinline__ void scale_piece(const uint8_t *p, uint8_t *out, int64_t len, float coef) {
-    const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-    const int64_t whole = wide ? len / 8 : 0;
-    for (int64_t i = threadIdx.x; i < whole; i += kThreads) {
-        Raw8<T> r;
-        load8(r, p + i * 8 * T::kBytes);
-        float v[8];
-        to_f32(r, v);
+__device__ __forceinline__ void scale_piece(const Out &whole, const uint8_t *p, uint8_t *out, int len,
+                                            float coef, int *status) {
+    Parts q = parts_of<T>(p, len);
+    // The vectors' stores need the output's boundary at the same element.
+    if ((reinterpret_cast<uintptr_t>(out) + q.head * O::kBytes) & 15u) q.head = q.whole = 0;
+    const int tail = q.head + 8 * q.whole, t = threadIdx.x;
+    if (t < q.head) store1<O>(whole, out, t, load1<T>(p, t) * coef, status);
+    const uint8_t *body = p + q.head * T::kBytes;
+    uint8_t *dst = out + q.head * O::kBytes;
+    const bool aligned32 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
+    for (int i = t; i < q.whole; i += kUnroll * kThreads) {
+        Raw8<T> r[kUnroll];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= coef;
-        Raw8<O> o;
-        from_f32(o, v);
-        uint4 *d = reinterpret_cast<uint4 *>(out + i * 8 * O::kBytes);
-        d[0] = o.a;
-        if constexpr (O::kBytes == 4) d[1] = o.b;
+        for (int k = 0; k < kUnroll; ++k) {
+            zero8(r[k]);
+            if (i + k * kThreads < q.whole)
+                load8(r[k], body + static_cast<int64_t>(i + k * kThreads) * 8 * T::kBytes, true);
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            if (i + k * kThreads >= q.whole) continue;
+            V8 v = to_v8(r[k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v.v[j] = mul2(v.v[j], same2(coef));
+            store8<O>(whole, dst + static_cast<int64_t>(i + k * kThreads) * 8 * O::kBytes, v, aligned32, status);
+        }
     }
-    for (int64_t i = whole * 8 + threadIdx.x; i < len; i += kThreads) {
-        const float v = load1(p, T::kBytes == 4, i) * coef;
-        if constexpr (O::kBytes == 4) reinterpret_cast<float *>(out)[i] = v;
-        else reinterpret_cast<uint16_t *>(out)[i] = static_cast<uint16_t>(bf16x2(v, 0.0f));
+    for (int i = tail + t; i < len; i += 2 * kUnroll * kThreads) {
+        float v[2 * kUnroll];
+#pragma unroll
+        for (int k = 0; k < 2 * kUnroll; ++k)
+            v[k] = i + k * kThreads < len ? load1<T>(p, i + k * kThreads) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2 * kUnroll; ++k)
+            if (i + k * kThreads < len) store1<O>(whole, out, i + k * kThreads, v[k] * coef, status);
     }
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) mx_grad_scale_kernel(const __grid_constant__ Table<N> t,
-                                                                 const double *sums, int64_t n_sums,
+                                                                 const Sum *sums, int n_sums,
                                                                  float max_norm, float eps,
-                                                                 float *norm) {
-    __shared__ double part[kThreads / 32];
+                                                                 float *norm, int *status) {
+    __shared__ Sum part[kThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
     const float total = norm_of(sums, n_sums, part);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     float coef = max_norm / (total + eps);
     if (coef > 1.0f) coef = 1.0f;  // a NaN stays
-    for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-        const Piece q = piece_of(t, c);
+    // Backwards: what the sums read last is still in L2.
+    const uint32_t chunks = t.first[t.count];
+    for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
+        const Piece q = piece_of(t, chunks - 1 - i);
         const bool f32 = t.f32[q.tensor] != 0, out_f32 = t.out_f32[q.tensor] != 0;
         const uint8_t *p = t.p[q.tensor] + q.begin * (f32 ? 4 : 2);
         uint8_t *out = t.out[q.tensor] + q.begin * (out_f32 ? 4 : 2);
+        const Out whole{t.out[q.tensor], static_cast<size_t>(t.n[q.tensor]) * (out_f32 ? 4 : 2)};
         if (p == out && coef == 1.0f) continue;  // in place and nothing to change
         if (f32) {
-            if (out_f32) scale_piece<F32, F32>(p, out, q.len, coef);
-            else scale_piece<F32, BF16>(p, out, q.len, coef);
+            if (out_f32) scale_piece<F32, F32>(whole, p, out, q.len, coef, status);
+            else scale_piece<F32, BF16>(whole, p, out, q.len, coef, status);
         } else {
-            if (out_f32) scale_piece<BF16, F32>(p, out, q.len, coef);
-            else scale_piece<BF16, BF16>(p, out, q.len, coef);
+            if (out_f32) scale_piece<BF16, F32>(whole, p, out, q.len, coef, status);
+            else scale_piece<BF16, BF16>(whole, p, out, q.len, coef, status);
         }
     }
 }
 
-template <int N>
-bool fill(Table<N> *t, const GradTensor *g, int count) {
-    uint64_t chunks = 0;
-    for (int i = 0; i < count; ++i) {
-        t->p[i] = static_cast<const uint8_t *>(g[i].p);
-        t->out[i] = static_cast<uint8_t *>(g[i].out);
-        t->n[i] = g[i].n;
-        t->f32[i] = g[i].f32;
-        t->out_f32[i] = g[i].out_f32;
-        t->first[i] = static_cast<uint32_t>(chunks);
-        chunks += static_cast<uint64_t>((g[i].n + kChunk - 1) / kChunk);
-        if (chunks > 0x7FFFFFFFull) return false;
-    }
-    t->first[count] = static_cast<uint32_t>(chunks);
-    t->count = count;
-    return true;
+uint64_t chunks_of(const GradTensor *g, int count, int64_t chunk) {
+    uint64_t n = 0;
+    for (int i = 0; i < count; ++i) n += static_cast<uint64_t>((g[i].n + chunk - 1) / chunk);
+    return n;
 }
 
+// Up to N tensors of one launch.
+struct Slice {
+    const GradTensor *g;
+    int count;
+    int chunk, blocks;
+};
+
 template <int N>
-cudaError_t run_slice(const GradTensor *g, int count, bool sums, double *at, int64_t n_sums,
-                      float max_norm, float eps, float *norm, cudaStream_t stream) {
+cudaError_t run_slice(const Slice &s, bool scale, Sum *sums, int n_sums, float max_norm,
+                      float eps, float *norm, int *status, cudaStream_t stream) {
     Table<N> t{};
-    if (!fill(&t, g, count)) return cudaErrorInvalidValue;
-    if (sums) return launch_dependent(mx_grad_sums_kernel<N>, kGrid, kThreads, stream, t, at);
-    return launch_dependent(mx_grad_scale_kernel<N>, kGrid, kThreads, stream, t,
-                            static_cast<const double *>(at), n_sums, max_norm, eps, norm);
+    uint32_t at = 0;
+    for (int i = 0; i < s.count; ++i) {
+        const GradTensor &g = s.g[i];
+        t.p[i] = static_cast<const uint8_t *>(g.p);
+        t.out[i] = static_cast<uint8_t *>(g.out);
+        t.n[i] = g.n;
+        t.f32[i] = g.f32;
+        t.out_f32[i] = g.out_f32;
+        t.first[i] = at;
+        at += static_cast<uint32_t>((g.n + s.chunk - 1) / s.chunk);
+    }
+    t.first[s.count] = at;
+    t.count = s.count;
+    t.chunk = s.chunk;
+    if (!scale) return launch_dependent(mx_grad_sums_kernel<N>, s.blocks, kThreads, 0, stream, t, sums);
+    return launch_dependent(mx_grad_scale_kernel<N>, s.blocks, kThreads, 0, stream, t,
+                            static_cast<const Sum *>(sums), n_sums, max_norm, eps, norm, status);
 }
 
 }  // namespace
 
 size_t grad_ws(int64_t count) {
-    return static_cast<size_t>((count + kMostTensors - 1) / kMostTensors) * kGrid * sizeof(double);
+    return static_cast<size_t>((count + kMostTensors - 1) / kMostTensors) * kGrid * sizeof(Sum);
 }
 
 cudaError_t launch_grad_clip(const GradTensor *g, int64_t count, bool scale, float max_norm,
                              float eps, float *norm, void *ws, const DeviceInfo &dev,
                              cudaStream_t stream) {
-    double *sums = static_cast<double *>(ws);
-    const int64_t slices = (count + kMostTensors - 1) / kMostTensors, n_sums = slices * kGrid;
+    Sum *sums = static_cast<Sum *>(ws);
+    int n_sums = 0;
     for (int pass = 0; pass < (scale ? 2 : 1); ++pass) {
-        for (int64_t s = 0; s < slices; ++s) {
-            const int64_t first = s * kMostTensors;
-            const int n = static_cast<int>(count - first < kMostTensors ? count - first : kMostTensors);
-            double *at = pass == 0 ? sums + s * kGrid : sums;
+        // The last slice first in the second pass, like the chunks within one.
+        const int64_t slices = (count + kMostTensors - 1) / kMostTensors;
+        for (int64_t i = 0; i < slices; ++i) {
+            const int64_t first = (pass == 0 ? i : slices - 1 - i) * kMostTensors;
+            Slice s;
+            s.g = g + first;
+            s.count = static_cast<int>(count - first < kMostTensors ? count - first : kMostTensors);
+            s.chunk = static_cast<int>(chunks_of(s.g, s.count, kChunk) >= kGrid ? kChunk : kSmallChunk);
+            const uint64_t chunks = chunks_of(s.g, s.count, s.chunk);
+            if (chunks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+            s.blocks = static_cast<int>(chunks < kGrid ? chunks : kGrid);
             const cudaError_t e =
-                n <= 64 ? run_slice<64>(g + first, n, pass == 0, at, n_sums, max_norm, eps, norm, stream)
-                        : run_slice<kMostTensors>(g + first, n, pass == 0, at, n_sums, max_norm, eps,
-                                                  norm, stream);
+                s.count <= 64 ? run_slice<64>(s, pass == 1, pass == 0 ? sums + n_sums : sums, n_sums,
+                                              max_norm, eps, norm, dev.status, stream)
+                              : run_slice<kMostTensors>(s, pass == 1, pass == 0 ? sums + n_sums : sums,
+                                                        n_sums, max_norm, eps, norm, dev.status, stream);
             if (e != cudaSuccess) return e;
+            if (pass == 0) n_sums += s.blocks;
         }
     }
     if (scale) return cudaSuccess;
-    return launch_dependent(mx_grad_norm_kernel, 1, kThreads, stream,
-                            static_cast<const double *>(sums), n_sums, norm);
+    return launch_dependent(mx_grad_norm_kernel, 1, kThreads, 0, stream,
+                            static_cast<const Sum *>(sums), n_sums, norm);
 }
 
 }  // namespace mx

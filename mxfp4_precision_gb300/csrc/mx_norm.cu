@@ -21,14 +21,16 @@ using namespace rows;
 
 struct NormArgs {
     const uint8_t *x, *res, *w;
-    int64_t x_pitch, res_pitch, h_pitch;  // in elements
+    int64_t x_pitch, res_pitch, h_pitch;  // bytes
     Out h, y, rstd;
     Encoded enc;
-    int64_t T, K;
-    int64_t rows;  // T, or T padded to the scale layout's 128-line groups
+    int64_t T;
+    uint32_t K;
     float eps;
+    bool aligned32;
     int w_f32;
-    int tpr;  // threads per row, a multiple of 32
+    int tpr;         // threads per row, a multiple of 32
+    uint32_t tiles;  // blocks that hold rows; those after them zero the scales' padding lines
     int *status;
 };
 
@@ -45,219 +47,516 @@ __device__ __forceinline__ float sum_row(float v, int tpr, float *part) {
     return v;
 }
 
-// One row per tpr threads, C chunks of 8 columns per thread, the row in
-// registers between its sum and its output.
-template <typename X, typename S, bool RES, int C>
-__global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const __grid_constant__ NormArgs p) {
+__device__ __forceinline__ float rstd_of(float sum, uint32_t K, float eps) {
+    return __frsqrt_rn(sum / static_cast<float>(K) + eps);
+}
+
+// Where a row's outputs go.
+struct NormRow {
+    uint8_t *h, *y;
+    EncodedRow enc;
+};
+__device__ __forceinline__ NormRow norm_row(const NormArgs &p, int64_t row) {
+    return {p.h.p + row * p.h_pitch, p.y.p + row * 2 * p.K, encoded_row(p.enc, row)};
+}
+// The outputs of one chunk (8 columns) of a row: h, y and y's codes.
+template <typename S, bool RES>
+__device__ __forceinline__ void norm_out(const NormArgs &p, const NormRow &at, uint32_t c, const V8 &h,
+                                         const V8 &w, float rstd) {
+    const bool in = 8 * c < p.K;
+    if (RES && in && p.h.p != nullptr) store8<S>(p.h, at.h + 8 * S::kBytes * c, h, p.aligned32, p.status);
+    V8 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.v[i] = mul2(mul2(h.v[i], same2(rstd)), w.v[i]);
+    if (in && p.y.p != nullptr) store8<BF16>(p.y, at.y + 16 * c, y, true, p.status);
+    // Whole warps: a warp's chunks are all inside the padded width or all beyond it.
+    if (p.enc.fmt != kEncNone && c < p.enc.katoms * 16) encode8(p.enc, at.enc, c, in, y, p.status);
+}
+
+// h = x + r of a chunk, and its squares added to a pair of sums.
+template <typename X, typename S, bool RES>
+__device__ __forceinline__ V8 join(const Raw8<X> &x, const Raw8<S> &r, uint64_t &ss) {
+    V8 h = to_v8(x);
+    if (RES) {
+        const V8 b = to_v8(r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h.v[i] = add2(h.v[i], b.v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss = fma2(h.v[i], h.v[i], ss);
+    return h;
+}
+
+__device__ __forceinline__ void rstd_out(const NormArgs &p, int64_t row, float rstd) {
+    if (p.rstd.p == nullptr) return;
+    float *d = reinterpret_cast<float *>(p.rstd.p) + row;
+    if (MX_STORE_OK(d, 4, p.rstd.p, p.rstd.bytes, p.status)) *d = rstd;
+}
+
+// One row per tpr threads and no turn after it, C chunks of 8 columns per
+// thread, the row in registers between its sum and its output.
+template <typename X, typename S, bool RES, int C, int THREADS>
+__global__ void __launch_bounds__(THREADS) mx_rmsnorm_kernel(const __grid_constant__ NormArgs p) {
     __shared__ float part[32];
     griddep_wait();
     griddep_launch_dependents();
+    if (blockIdx.x >= p.tiles) {
+        zero_padding(p.enc, p.T, static_cast<int64_t>(blockIdx.x - p.tiles) * blockDim.x + threadIdx.x,
+                     static_cast<int64_t>(gridDim.x - p.tiles) * blockDim.x, p.status);
+        return;
+    }
     const int tr = threadIdx.x % p.tpr;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.tpr) + threadIdx.x / p.tpr;
     const bool live = row < p.T;
-    float h[C][8];
     Raw8<X> xr[C];
     Raw8<S> rr[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        const int64_t col = 8 * (static_cast<int64_t>(j) * p.tpr + tr);
-        const bool in = live && col < p.K;
+        const uint32_t col = 8 * (j * p.tpr + tr);
         zero8(xr[j]);
         zero8(rr[j]);
-        if (in) load8(xr[j], p.x + (row * p.x_pitch + col) * X::kBytes);
-        if (RES && in) load8(rr[j], p.res + (row * p.res_pitch + col) * S::kBytes);
+        if (live && col < p.K) {
+            load8(xr[j], p.x + row * p.x_pitch + col * X::kBytes, p.aligned32);
+            if (RES) load8(rr[j], p.res + row * p.res_pitch + col * S::kBytes, p.aligned32);
+        }
     }
-    float ss = 0.0f;
+    V8 h[C];
+    uint64_t ss = 0;
+#pragma unroll
+    for (int j = 0; j < C; ++j) h[j] = join<X, S, RES>(xr[j], rr[j], ss);
+    const float rstd = rstd_of(sum_row(sum2(ss), p.tpr, part), p.K, p.eps);
+    if (!live) return;
+    if (tr == 0) rstd_out(p, row, rstd);
+    const NormRow at = norm_row(p, row);
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        to_f32(xr[j], h[j]);
-        if (RES) {
-            float r[8];
-            to_f32(rr[j], r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[j][i] += r[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-    }
-    ss = sum_row(ss, p.tpr, part);
-    const float rstd = __frsqrt_rn(ss / static_cast<float>(p.K) + p.eps);
-    if (live && tr == 0 && p.rstd.p != nullptr) {
-        float *d = reinterpret_cast<float *>(p.rstd.p) + row;
-        if (MX_STORE_OK(d, 4, p.rstd.p, p.rstd.bytes, p.status)) *d = rstd;
-    }
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const int64_t c = static_cast<int64_t>(j) * p.tpr + tr, col = 8 * c;
-        const bool in = live && col < p.K;
-        if (RES && in && p.h.p != nullptr) store8<S>(p.h, row * p.h_pitch + col, h[j], p.status);
-        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in) {
-            float w[8];
-            load_weight8(p.w, p.w_f32 != 0, col, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = h[j][i] * rstd * w[i];
-            if (p.y.p != nullptr) store8<BF16>(p.y, row * p.K + col, y, p.status);
-        }
-        // Whole warps: a warp's chunks are all inside the padded width or all beyond it.
-        if (p.enc.fmt != kEncNone && row < p.rows && c < p.enc.katoms * 16)
-            encode8(p.enc, row, live ? p.K : 0, c, y, p.status);
+        const uint32_t c = j * p.tpr + tr;
+        const V8 w = 8 * c < p.K ? load_weight8(p.w, p.w_f32 != 0, 8 * c) : zero_v8();
+        norm_out<S, RES>(p, at, c, h[j], w, rstd);
     }
 }
 
+// ---------------------------------------------------------------- rows through a ring
+// For the gradient over many rows: one block per SM, its threads in groups of
+// tpr that each take rows in turn.  A group's next rows are on their way
+// (cp.async.bulk, one per input and row) into its ring of shared-memory slots
+// while it works on the present one, so that the loads never wait for a row's
+// sum.  A group meets once a row, in the barrier of its sum; by then every
+// thread has the row in registers, and the slot is filled again.
+struct Ring {
+    uint8_t *slots;  // of this group
+    uint64_t *full;
+    float *part;     // [2][32]
+    int id, tpr, stages, slot_bytes;
+    int s = 0;
+    uint32_t parity = 0;
+
+    __device__ __forceinline__ uint8_t *slot() const { return slots + s * slot_bytes; }
+    __device__ __forceinline__ void next() {
+        if (++s == stages) s = 0, parity ^= 1;
+    }
+    // Sum over the group, and whether every thread's wait ended well.
+    __device__ __forceinline__ bool sum(float &v, bool ok, int turn) {
+        v = sum_lanes(v, 32);
+        float *at = part + (turn & 1) * 32;
+        const int tr = threadIdx.x % tpr;
+        if ((tr & 31) == 0) at[tr >> 5] = v;
+        ok = bar_and(id, tpr, ok);
+        v = 0.0f;
+        for (int i = 0; i < tpr >> 5; ++i) v += at[i];
+        return ok;
+    }
+    // After a wait that ran out: the slots still being filled, before the block ends.
+    __device__ __forceinline__ void drain(int64_t left) {
+        for (int64_t i = 0; i < left && i < stages; ++i, next())
+            mbar_wait_inl(&full[s], parity, nullptr, nullptr);
+    }
+};
+
+// Carves the block's dynamic shared memory: groups x stages slots, then the
+// barriers, then the groups' partial sums; sets up this thread's group.
+__device__ __forceinline__ Ring ring_of(uint8_t *smem, int tpr, int stages, int slot_bytes) {
+    const int groups = blockDim.x / tpr, g = threadIdx.x / tpr;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + static_cast<size_t>(groups) * stages * slot_bytes);
+    float *parts = reinterpret_cast<float *>(bars + groups * stages);
+    Ring r;
+    r.slots = smem + static_cast<size_t>(g) * stages * slot_bytes;
+    r.full = bars + g * stages;
+    r.part = parts + g * 64;
+    r.id = g + 1;
+    r.tpr = tpr;
+    r.stages = stages;
+    r.slot_bytes = slot_bytes;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < groups * stages; ++i) mbar_init(&bars[i], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    return r;
+}
+
+// ---------------------------------------------------------------- gradient
 struct NormGradArgs {
     const uint8_t *dy, *h, *w, *dres;
     const float *rstd;
-    int64_t dy_pitch, h_pitch, dres_pitch, dx_pitch;
-    Out dx;
-    float *parts;  // [gridDim.x * rows per block][K] partial weight gradients
-    int64_t T, K;
+    int64_t dy_pitch, h_pitch, dres_pitch, dx_pitch;  // bytes
+    Out dx, parts;  // parts [n][K] fp32: partial weight gradients (null: not wanted)
+    int64_t T;
+    uint32_t K;
     int w_f32;
-    int tpr;
+    int tpr, stages;
+    bool aligned32;
     int *status;
 };
 
-// Each group of tpr threads takes rows in turn and keeps its columns' sums of
-// dy * h * rstd in registers; the groups' sums go to the workspace.
-template <typename D, typename S, int C>
-__global__ void __launch_bounds__(C > 4 ? 512 : 1024)
-    mx_rmsnorm_backward_kernel(const __grid_constant__ NormGradArgs p) {
-    __shared__ float part[2][32];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int tr = threadIdx.x % p.tpr, groups = blockDim.x / p.tpr;
-    const int64_t group = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / p.tpr;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
-    float dw[C][8];
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-    // Every group of a block makes the same number of turns (they share barriers).
-    int turn = 0;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < p.T; base += stride, turn ^= 1) {
-        const int64_t row = base + threadIdx.x / p.tpr;
-        const bool live = row < p.T;
-        const float rstd = live ? p.rstd[row] : 0.0f;
-        float a[C][8], x[C][8];  // dy * w, h * rstd
-        float along = 0.0f;
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int64_t col = 8 * (static_cast<int64_t>(j) * p.tpr + tr);
-            const bool in = live && col < p.K;
-            Raw8<D> dr;
-            Raw8<S> hr;
-            zero8(dr);
-            zero8(hr);
-            if (in) {
-                load8(dr, p.dy + (row * p.dy_pitch + col) * D::kBytes);
-                load8(hr, p.h + (row * p.h_pitch + col) * S::kBytes);
-            }
-            to_f32(dr, a[j]);
-            to_f32(hr, x[j]);
-            float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (col < p.K) load_weight8(p.w, p.w_f32 != 0, col, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[j][i] *= rstd;
-                dw[j][i] = fmaf(a[j][i], x[j][i], dw[j][i]);
-                a[j][i] *= w[i];
-                along = fmaf(a[j][i], x[j][i], along);
-            }
-        }
-        along = sum_row(along, p.tpr, part[turn]) / static_cast<float>(p.K);
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int64_t col = 8 * (static_cast<int64_t>(j) * p.tpr + tr);
-            if (!live || col >= p.K) continue;
-            float g[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (p.dres != nullptr) {
-                Raw8<S> gr;
-                load8(gr, p.dres + (row * p.dres_pitch + col) * S::kBytes);
-                to_f32(gr, g);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = fmaf(rstd, a[j][i] - x[j][i] * along, g[i]);
-            store8<S>(p.dx, row * p.dx_pitch + col, g, p.status);
-        }
-    }
-    if (p.parts == nullptr) return;
+// Columns col .. col+7 of partial gradient n.
+__device__ __forceinline__ void part_out(const NormGradArgs &p, int64_t n, uint32_t col, const V8 &v) {
+    store8<F32>(p.parts, p.parts.p + (n * p.K + col) * 4, v, false, p.status);
+}
+
+// The block's partial gradient from its groups', through sums [groups][K].
+template <int C>
+__device__ __forceinline__ void sum_groups(const NormGradArgs &p, float *sums, const V8 (&dw)[C]) {
+    const int tr = threadIdx.x % p.tpr, groups = blockDim.x / p.tpr, g = threadIdx.x / p.tpr;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        const int64_t col = 8 * (static_cast<int64_t>(j) * p.tpr + tr);
+        const uint32_t col = 8 * (j * p.tpr + tr);
         if (col >= p.K) continue;
-        float4 *d = reinterpret_cast<float4 *>(p.parts + group * p.K + col);
-        d[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-        d[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+        float v[8];
+        floats_of(dw[j], v);
+        float4 *d = reinterpret_cast<float4 *>(sums + g * p.K + col);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __syncthreads();
+    for (uint32_t col = 8 * threadIdx.x; col < p.K; col += 8 * blockDim.x) {
+        V8 v = zero_v8();
+        for (int k = 0; k < groups; ++k) {
+            Raw8<F32> r;
+            load8_again(r, reinterpret_cast<const uint8_t *>(sums + k * p.K + col));
+            const V8 b = to_v8(r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v.v[i] = add2(v.v[i], b.v[i]);
+        }
+        part_out(p, blockIdx.x, col, v);
     }
 }
 
-// dw[col] = sum of the partial sums, in a fixed order: 32 columns a block,
-// the partials split over its 8 warps.
-__global__ void __launch_bounds__(256) mx_rmsnorm_dw_kernel(const float *parts, int64_t n, int64_t K,
-                                                            Out dw, int *status) {
-    __shared__ float sums[8][32];
+// First look at a chunk: dw += dy * xhat and along += dy * w * xhat, with
+// xhat = h * rstd; leaves dy * w in a.
+__device__ __forceinline__ void look(V8 &a, const V8 &h, const V8 &w, float rstd, V8 &dw,
+                                     uint64_t &along) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t x = mul2(h.v[i], same2(rstd));
+        dw.v[i] = fma2(a.v[i], x, dw.v[i]);
+        a.v[i] = mul2(a.v[i], w.v[i]);
+        along = fma2(a.v[i], x, along);
+    }
+}
+// dx = rstd * (a - xhat * along) + dres, into g (which holds dres).
+__device__ __forceinline__ void finish(const V8 &a, const V8 &h, float rstd, float along, V8 &g) {
+    const uint64_t r = same2(rstd), m = same2(-along);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g.v[i] = fma2(r, fma2(mul2(h.v[i], r), m, a.v[i]), g.v[i]);
+}
+
+// Each group of tpr threads takes rows in turn and keeps its columns' sums of
+// dy * h * rstd in registers; they are added up over the block's groups at the
+// end: one partial per block.  AGAIN: rows too wide for the registers are
+// loaded twice (the second time from L1 or L2), once for mean(dy * w * h), once
+// for dx.
+template <typename D, typename S, int C, int THREADS, bool AGAIN>
+__global__ void __launch_bounds__(THREADS)
+    mx_rmsnorm_backward_kernel(const __grid_constant__ NormGradArgs p) {
+    __shared__ float part[2][32];
+    extern __shared__ __align__(128) uint8_t smem[];  // [groups][K] fp32 where groups > 1
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tr = threadIdx.x % p.tpr, groups = blockDim.x / p.tpr, g = threadIdx.x / p.tpr;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
+    V8 dw[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) dw[j] = zero_v8();
+    // Every group of a block makes the same number of turns (they share barriers).
+    int turn = 0;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < p.T; base += stride, turn ^= 1) {
+        const int64_t row = base + g;
+        const bool live = row < p.T;
+        const uint8_t *dy = p.dy + row * p.dy_pitch, *hp = p.h + row * p.h_pitch;
+        const uint8_t *gp = p.dres + row * p.dres_pitch;
+        Raw8<D> dr[C];
+        Raw8<S> hr[C], gr[C];
+        const float rstd = live ? p.rstd[row] : 0.0f;
+        uint64_t sums = 0;
+        if (!AGAIN) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                const uint32_t col = 8 * (j * p.tpr + tr);
+                zero8(dr[j]);
+                zero8(hr[j]);
+                zero8(gr[j]);
+                if (live && col < p.K) {
+                    load8(dr[j], dy + col * D::kBytes, p.aligned32);
+                    load8(hr[j], hp + col * S::kBytes, p.aligned32);
+                    if (p.dres != nullptr) load8(gr[j], gp + col * S::kBytes, p.aligned32);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const uint32_t col = 8 * (j * p.tpr + tr);
+            if (!live || col >= p.K) continue;
+            if (AGAIN) {
+                load8_again(dr[j], dy + col * D::kBytes);
+                load8_again(hr[j], hp + col * S::kBytes);
+            }
+            V8 a = to_v8(dr[j]);
+            look(a, to_v8(hr[j]), load_weight8(p.w, p.w_f32 != 0, col), rstd, dw[j], sums);
+        }
+        const float along = sum_row(sum2(sums), p.tpr, part[turn]) / static_cast<float>(p.K);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const uint32_t col = 8 * (j * p.tpr + tr);
+            if (!live || col >= p.K) continue;
+            if (AGAIN) {
+                load8_again(dr[j], dy + col * D::kBytes);
+                load8_again(hr[j], hp + col * S::kBytes);
+                zero8(gr[j]);
+                if (p.dres != nullptr) load8(gr[j], gp + col * S::kBytes, p.aligned32);
+            }
+            V8 a = to_v8(dr[j]), v = to_v8(gr[j]);
+            const V8 w = load_weight8(p.w, p.w_f32 != 0, col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], w.v[i]);
+            finish(a, to_v8(hr[j]), rstd, along, v);
+            store8<S>(p.dx, p.dx.p + row * p.dx_pitch + col * S::kBytes, v, p.aligned32, p.status);
+        }
+    }
+    if (p.parts.p == nullptr) return;
+    if (groups == 1) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const uint32_t col = 8 * (j * p.tpr + tr);
+            if (col < p.K) part_out(p, blockIdx.x, col, dw[j]);
+        }
+        return;
+    }
+    sum_groups<C>(p, reinterpret_cast<float *>(smem), dw);
+}
+
+// Many rows, through the ring.  The groups' weight gradients are summed in shared memory at the end: one partial
+// per block.
+template <typename D, typename S, int C, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    mx_rmsnorm_backward_ring_kernel(const __grid_constant__ NormGradArgs p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t db = p.K * D::kBytes, sb = p.K * S::kBytes;
+    const bool res = p.dres != nullptr;
+    const uint32_t bytes = db + sb + (res ? sb : 0);
+    Ring ring = ring_of(smem, p.tpr, p.stages, bytes);
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tr = threadIdx.x % p.tpr, groups = blockDim.x / p.tpr, g = threadIdx.x / p.tpr;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
+    int64_t row = static_cast<int64_t>(g) * gridDim.x + blockIdx.x;
+    const uint64_t once = l2_evict_first_policy();
+    auto fill = [&](int64_t r, int s) {
+        uint8_t *d = ring.slots + s * ring.slot_bytes;
+        mbar_arrive_expect_tx(&ring.full[s], bytes);
+        bulk_load_hint(d, p.dy + r * p.dy_pitch, db, &ring.full[s], once);
+        bulk_load_hint(d + db, p.h + r * p.h_pitch, sb, &ring.full[s], once);
+        if (res) bulk_load_hint(d + db + sb, p.dres + r * p.dres_pitch, sb, &ring.full[s], once);
+    };
+    if (tr == 0)
+        for (int s = 0; s < p.stages; ++s)
+            if (row + s * stride < p.T) fill(row + s * stride, s);
+    V8 w[C], dw[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        const uint32_t col = 8 * (j * p.tpr + tr);
+        w[j] = col < p.K ? load_weight8(p.w, p.w_f32 != 0, col) : zero_v8();
+        dw[j] = zero_v8();
+    }
+    for (int turn = 0; row < p.T; row += stride, ++turn) {
+        const float rstd = p.rstd[row];
+        bool ok = mbar_wait_inl(&ring.full[ring.s], ring.parity, p.status, nullptr);
+        const uint8_t *slot = ring.slot();
+        V8 a[C];
+        Raw8<S> hr[C], gr[C];
+        uint64_t sums = 0;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const uint32_t col = 8 * (j * p.tpr + tr);
+            Raw8<D> dr;
+            zero8(dr);
+            zero8(hr[j]);
+            zero8(gr[j]);
+            if (col < p.K) {
+                load8_again(dr, slot + col * D::kBytes);
+                load8_again(hr[j], slot + db + col * S::kBytes);
+                if (res) load8_again(gr[j], slot + db + sb + col * S::kBytes);
+            }
+            a[j] = to_v8(dr);
+            look(a[j], to_v8(hr[j]), w[j], rstd, dw[j], sums);
+        }
+        float along = sum2(sums);
+        ok = ring.sum(along, ok, turn);
+        if (!ok) {
+            if (tr == 0) ring.drain((p.T - row + stride - 1) / stride);
+            break;
+        }
+        if (tr == 0 && row + p.stages * stride < p.T) fill(row + p.stages * stride, ring.s);
+        ring.next();
+        along /= static_cast<float>(p.K);
+        uint8_t *dx = p.dx.p + row * p.dx_pitch;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const uint32_t col = 8 * (j * p.tpr + tr);
+            if (col >= p.K) continue;
+            V8 v = to_v8(gr[j]);
+            finish(a[j], to_v8(hr[j]), rstd, along, v);
+            store8<S>(p.dx, dx + col * S::kBytes, v, p.aligned32, p.status);
+        }
+    }
+    if (p.parts.p == nullptr) return;
+    // All slots are consumed (or drained): the ring's memory holds the groups' sums.
+    __syncthreads();
+    sum_groups<C>(p, reinterpret_cast<float *>(smem), dw);
+}
+
+// dw[col] = sum of the n partial sums, in a fixed order: 32 columns a block,
+// the partials split over its 32 warps.
+__global__ void __launch_bounds__(1024) mx_rmsnorm_dw_kernel(const float *parts, int64_t n, int64_t K,
+                                                             Out dw, int *status) {
+    __shared__ float sums[32][32];
     griddep_wait();
     griddep_launch_dependents();
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
     float s = 0.0f;
-    if (col < K)
-        for (int64_t i = threadIdx.x >> 5; i < n; i += 8) s += parts[i * K + col];
+    if (col < K) {
+#pragma unroll 8
+        for (int64_t i = threadIdx.x >> 5; i < n; i += 32) s += parts[i * K + col];
+    }
     sums[threadIdx.x >> 5][threadIdx.x & 31] = s;
     __syncthreads();
     if (threadIdx.x < 32 && col < K) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
+        for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x];
         float *d = reinterpret_cast<float *>(dw.p) + col;
         if (MX_STORE_OK(d, 4, dw.p, dw.bytes, status)) *d = s;
     }
 }
 
-// Chunks of 8 columns a row's threads cover: the padded width of the scale layout.
-int64_t padded_chunks(int64_t K) { return (K + 255) / 256 * 32; }
-
+// ---------------------------------------------------------------- shapes
+// Threads of a row and its chunks of 8 columns per thread; `n` chunks is the
+// padded width of the scale layout (a multiple of 32).
 struct RowShape {
-    int chunks_per_thread, tpr, groups;
+    int c, tpr, groups, stages;
+    size_t smem;
 };
-// Few chunks a thread keep the registers few and the loads of a row in flight
-// at once; a block has at least 256 threads.
-RowShape row_shape(int64_t K, int most) {
+int64_t padded_chunks(int64_t K) { return (K + 255) / 256 * 32; }
+RowShape row_shape(int64_t n, int c) {
+    const int tpr = static_cast<int>((n + 32 * c - 1) / (32 * c)) * 32;
+    return {c, tpr, tpr >= 256 ? 1 : 256 / tpr, 0, 0};
+}
+
+// One warp a row (no barrier) for rows of up to 160 chunks, once the rows
+// fill the SMs; two chunks a thread otherwise, four where a row needs more than
+// 1024 threads.
+RowShape norm_shape(int64_t T, int64_t K, const DeviceInfo &dev) {
     const int64_t n = padded_chunks(K);
-    const int c = n <= 32 ? 1 : n <= 2 * most ? 2 : n <= 4 * most ? 4 : 8;
-    const int tpr = static_cast<int>(((n + c - 1) / c + 31) / 32 * 32);
-    return {c, tpr, tpr >= 256 ? 1 : 256 / tpr};
+    if (n <= 32 || (n <= 160 && T >= 16ll * dev.sm_count)) return row_shape(n, static_cast<int>(n / 32));
+    return row_shape(n, n <= 1024 ? 2 : 4);
 }
 
 template <typename X, typename S, bool RES>
-cudaError_t launch_norm(const NormArgs &p, const RowShape &s, cudaStream_t stream) {
-    const int64_t grid = (p.rows + s.groups - 1) / s.groups;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+cudaError_t launch_norm(NormArgs &p, const DeviceInfo &dev, cudaStream_t stream) {
+    const RowShape s = norm_shape(p.T, p.K, dev);
+    p.tpr = s.tpr;
     const int threads = s.tpr * s.groups;
-    switch (s.chunks_per_thread) {
-        case 1: return launch_dependent(mx_rmsnorm_kernel<X, S, RES, 1>, grid, threads, stream, p);
-        case 2: return launch_dependent(mx_rmsnorm_kernel<X, S, RES, 2>, grid, threads, stream, p);
-        case 4: return launch_dependent(mx_rmsnorm_kernel<X, S, RES, 4>, grid, threads, stream, p);
-        default: return launch_dependent(mx_rmsnorm_kernel<X, S, RES, 8>, grid, threads, stream, p);
+    const int64_t tiles = (p.T + s.groups - 1) / s.groups;
+    const int64_t grid = tiles + (padding_words(p.enc, p.T) + threads - 1) / threads;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.tiles = static_cast<uint32_t>(tiles);
+#define MX_NORM_CASE(C, THREADS) \
+    launch_dependent(mx_rmsnorm_kernel<X, S, RES, C, THREADS>, grid, threads, 0, stream, p)
+    switch (s.c) {
+        case 1: return MX_NORM_CASE(1, 256);
+        case 2: return MX_NORM_CASE(2, 512);
+        case 3: return MX_NORM_CASE(3, 256);
+        case 5: return MX_NORM_CASE(5, 256);
+        default: return threads <= 512 ? MX_NORM_CASE(4, 512) : MX_NORM_CASE(4, 1024);
     }
+#undef MX_NORM_CASE
+}
+
+constexpr int kGradBlocks = 304;  // of the direct gradient kernel, at most
+constexpr int kRingThreads = 512;
+constexpr int kRingTurns = 4;  // rows a group must have for the ring to pay
+constexpr size_t kRingSmem = 220 * 1024;
+
+RowShape grad_shape(int64_t T, int64_t K) {
+    const int64_t n = padded_chunks(K);
+    RowShape s = n <= 160 ? row_shape(n, static_cast<int>(n / 32)) : row_shape(n, n <= 512 ? 2 : 4);
+    if (T < s.groups) s.groups = static_cast<int>(T);
+    s.smem = s.groups > 1 ? s.groups * static_cast<size_t>(K) * 4 : 0;
+    return s;
+}
+int64_t grad_grid(int64_t T, const RowShape &s) {
+    const int64_t want = (T + s.groups - 1) / s.groups;
+    return want < kGradBlocks ? want : kGradBlocks;
+}
+
+// The ring's shape for rows of `bytes`, or stages = 0 where it does not apply.
+RowShape ring_shape(int64_t T, int64_t K, size_t bytes, const DeviceInfo &dev) {
+    const int64_t n = padded_chunks(K);
+    RowShape s = row_shape(n, 2);
+    s.groups = kRingThreads / s.tpr;
+    if (n <= 160 || s.groups < 1 || T < static_cast<int64_t>(kRingTurns) * s.groups * dev.sm_count) return s;
+    s.stages = static_cast<int>((kRingSmem - 256 * s.groups) / (s.groups * (bytes + 8)));
+    if (s.stages > 8) s.stages = 8;
+    if (s.stages < 2) s.stages = 0;
+    s.smem = s.groups * (s.stages * (bytes + 8) + 256);
+    return s;
+}
+
+template <typename Kern>
+cudaError_t with_smem(Kern kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(bytes));
 }
 
 template <typename D, typename S>
-cudaError_t launch_norm_grad(const NormGradArgs &p, const RowShape &s, int grid, cudaStream_t stream) {
+cudaError_t launch_norm_grad(NormGradArgs &p, int64_t *n_parts, const DeviceInfo &dev,
+                             cudaStream_t stream) {
+    RowShape s = ring_shape(
+        p.T, p.K, static_cast<size_t>(p.K) * (D::kBytes + (p.dres != nullptr ? 2 : 1) * S::kBytes), dev);
+    const bool ring = s.stages > 0;
+    if (!ring) s = grad_shape(p.T, p.K);
+    p.tpr = s.tpr;
+    p.stages = s.stages;
+    const int64_t grid = ring ? dev.sm_count : grad_grid(p.T, s);
+    *n_parts = grid;
+    p.parts.bytes = static_cast<size_t>(grid) * p.K * 4;
     const int threads = s.tpr * s.groups;
-    switch (s.chunks_per_thread) {
-        case 1: return launch_dependent(mx_rmsnorm_backward_kernel<D, S, 1>, grid, threads, stream, p);
-        case 2: return launch_dependent(mx_rmsnorm_backward_kernel<D, S, 2>, grid, threads, stream, p);
-        case 4: return launch_dependent(mx_rmsnorm_backward_kernel<D, S, 4>, grid, threads, stream, p);
-        default: return launch_dependent(mx_rmsnorm_backward_kernel<D, S, 8>, grid, threads, stream, p);
+    auto go = [&](auto kernel) {
+        const cudaError_t e = with_smem(kernel, s.smem);
+        return e != cudaSuccess ? e : launch_dependent(kernel, grid, threads, s.smem, stream, p);
+    };
+    if (ring) return go(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads>);
+    switch (s.c) {
+        case 1: return go(mx_rmsnorm_backward_kernel<D, S, 1, 256, false>);
+        case 2: return go(mx_rmsnorm_backward_kernel<D, S, 2, 256, false>);
+        case 3: return go(mx_rmsnorm_backward_kernel<D, S, 3, 256, false>);
+        case 5: return go(mx_rmsnorm_backward_kernel<D, S, 5, 256, false>);
+        default:
+            return threads <= 256   ? go(mx_rmsnorm_backward_kernel<D, S, 4, 256, false>)
+                   : threads <= 512 ? go(mx_rmsnorm_backward_kernel<D, S, 4, 512, true>)
+                                    : go(mx_rmsnorm_backward_kernel<D, S, 4, 1024, true>);
     }
-}
-
-constexpr int kGradGrid = 304;  // blocks of the gradient at most: two for each of 152 SMs
-
-int grad_grid(int64_t T, const RowShape &s) {
-    const int64_t want = (T + s.groups - 1) / s.groups;
-    return static_cast<int>(want < kGradGrid ? want : kGradGrid);
 }
 
 }  // namespace
@@ -270,33 +569,31 @@ cudaError_t launch_rmsnorm(const RowIn &x, const RowIn &res, const void *w, int 
     p.x = static_cast<const uint8_t *>(x.p);
     p.res = static_cast<const uint8_t *>(res.p);
     p.w = static_cast<const uint8_t *>(w);
-    p.x_pitch = x.pitch;
-    p.res_pitch = res.pitch;
-    p.h_pitch = h_pitch;
+    p.x_pitch = x.pitch * (x.f32 ? 4 : 2);
+    p.res_pitch = res.pitch * (res.f32 ? 4 : 2);
+    p.h_pitch = h_pitch * (res.f32 ? 4 : 2);
+    p.aligned32 = aligned32(x.p) && aligned32(res.p) && aligned32(h);
     const size_t sb = res.f32 ? 4 : 2;
     p.h = {static_cast<uint8_t *>(h), (static_cast<size_t>(T - 1) * h_pitch + K) * sb};
     p.y = {static_cast<uint8_t *>(y), static_cast<size_t>(T) * K * 2};
     p.rstd = {reinterpret_cast<uint8_t *>(rstd), static_cast<size_t>(T) * 4};
     p.enc = row_encoded(e, T, K);
     p.T = T;
-    p.K = K;
-    p.rows = e.fmt != kEncNone ? 128 * scale_groups(T) : T;
+    p.K = static_cast<uint32_t>(K);
     p.eps = eps;
     p.w_f32 = w_f32;
     p.status = dev.status;
-    const RowShape s = row_shape(K, 1024);
-    p.tpr = s.tpr;
-    if (res.p == nullptr) return x.f32 ? launch_norm<F32, F32, false>(p, s, stream)
-                                       : launch_norm<BF16, BF16, false>(p, s, stream);
-    if (x.f32) return res.f32 ? launch_norm<F32, F32, true>(p, s, stream)
-                              : launch_norm<F32, BF16, true>(p, s, stream);
-    return res.f32 ? launch_norm<BF16, F32, true>(p, s, stream)
-                   : launch_norm<BF16, BF16, true>(p, s, stream);
+    if (res.p == nullptr) return x.f32 ? launch_norm<F32, F32, false>(p, dev, stream)
+                                       : launch_norm<BF16, BF16, false>(p, dev, stream);
+    if (x.f32) return res.f32 ? launch_norm<F32, F32, true>(p, dev, stream)
+                              : launch_norm<F32, BF16, true>(p, dev, stream);
+    return res.f32 ? launch_norm<BF16, F32, true>(p, dev, stream)
+                   : launch_norm<BF16, BF16, true>(p, dev, stream);
 }
 
 size_t rmsnorm_backward_ws(int64_t T, int64_t K) {
-    const RowShape s = row_shape(K, 512);
-    return static_cast<size_t>(grad_grid(T, s)) * s.groups * static_cast<size_t>(K) * 4;
+    // The direct kernel's partials; the ring's (one per SM) are fewer.
+    return static_cast<size_t>(grad_grid(T, grad_shape(T, K))) * static_cast<size_t>(K) * 4;
 }
 
 cudaError_t launch_rmsnorm_backward(const RowIn &dy, const RowIn &h, const void *w, int w_f32,
@@ -309,27 +606,26 @@ cudaError_t launch_rmsnorm_backward(const RowIn &dy, const RowIn &h, const void 
     p.w = static_cast<const uint8_t *>(w);
     p.dres = static_cast<const uint8_t *>(dres.p);
     p.rstd = rstd;
-    p.dy_pitch = dy.pitch;
-    p.h_pitch = h.pitch;
-    p.dres_pitch = dres.pitch;
-    p.dx_pitch = dx_pitch;
+    p.dy_pitch = dy.pitch * (dy.f32 ? 4 : 2);
+    p.h_pitch = h.pitch * (h.f32 ? 4 : 2);
+    p.dres_pitch = dres.pitch * (h.f32 ? 4 : 2);
+    p.dx_pitch = dx_pitch * (h.f32 ? 4 : 2);
+    p.aligned32 = aligned32(dy.p) && aligned32(h.p) && aligned32(dres.p) && aligned32(dx);
     p.dx = {static_cast<uint8_t *>(dx),
             (static_cast<size_t>(T - 1) * dx_pitch + K) * static_cast<size_t>(h.f32 ? 4 : 2)};
-    p.parts = dw != nullptr ? static_cast<float *>(ws) : nullptr;
+    p.parts.p = dw != nullptr ? static_cast<uint8_t *>(ws) : nullptr;
     p.T = T;
-    p.K = K;
+    p.K = static_cast<uint32_t>(K);
     p.w_f32 = w_f32;
     p.status = dev.status;
-    const RowShape s = row_shape(K, 512);
-    p.tpr = s.tpr;
-    const int grid = grad_grid(T, s);
-    cudaError_t e = dy.f32 ? (h.f32 ? launch_norm_grad<F32, F32>(p, s, grid, stream)
-                                    : launch_norm_grad<F32, BF16>(p, s, grid, stream))
-                           : (h.f32 ? launch_norm_grad<BF16, F32>(p, s, grid, stream)
-                                    : launch_norm_grad<BF16, BF16>(p, s, grid, stream));
+    int64_t n = 0;
+    const cudaError_t e = dy.f32 ? (h.f32 ? launch_norm_grad<F32, F32>(p, &n, dev, stream)
+                                          : launch_norm_grad<F32, BF16>(p, &n, dev, stream))
+                                 : (h.f32 ? launch_norm_grad<BF16, F32>(p, &n, dev, stream)
+                                          : launch_norm_grad<BF16, BF16>(p, &n, dev, stream));
     if (e != cudaSuccess || dw == nullptr) return e;
-    return launch_dependent(mx_rmsnorm_dw_kernel, (K + 31) / 32, 256, stream,
-                            static_cast<const float *>(ws), static_cast<int64_t>(grid) * s.groups, K,
+    return launch_dependent(mx_rmsnorm_dw_kernel, (K + 31) / 32, 1024, 0, stream,
+                            static_cast<const float *>(ws), n, K,
                             Out{reinterpret_cast<uint8_t *>(dw), static_cast<size_t>(K) * 4},
                             dev.status);
 }

@@ -26,41 +26,90 @@ struct F32 {
     static constexpr int kBytes = 4;
 };
 
-// Eight columns as loaded (kept packed until they are used, so that several
-// loads can be in flight without their converted values taking registers).
+// ---------------------------------------------------------------- pairs
+// Eight columns as four packed fp32 pairs {even column (low), odd (high)}: the
+// f32x2 instructions round each half like the scalar ones, at half the issue
+// slots, which is what these kernels run short of first.
+struct V8 {
+    uint64_t v[4];
+};
+using enc::add2;
+using enc::mul2;
+using enc::pack2;
+using enc::sub2;
+using enc::unpack2;
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t same2(float v) { return pack2(v, v); }
+__device__ __forceinline__ float sum2(uint64_t a) {
+    float lo, hi;
+    unpack2(a, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ V8 zero_v8() { return V8{{0, 0, 0, 0}}; }
+__device__ __forceinline__ void floats_of(const V8 &a, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2(a.v[i], f[2 * i], f[2 * i + 1]);
+}
+
+// ---------------------------------------------------------------- loads and stores
+// Eight columns as loaded: kept packed until they are used, so that several
+// loads can be in flight without their converted values taking registers.
 template <typename T>
-struct Raw8;
-template <>
-struct Raw8<BF16> {
-    uint4 a;
-};
-template <>
-struct Raw8<F32> {
-    uint4 a, b;
+struct Raw8 {
+    uint32_t w[2 * T::kBytes];
 };
 
-__device__ __forceinline__ void load8(Raw8<BF16> &r, const uint8_t *p) {
-    r.a = __ldcs(reinterpret_cast<const uint4 *>(p));
+__device__ __forceinline__ void load16(uint32_t *w, const uint8_t *p) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
 }
-__device__ __forceinline__ void load8(Raw8<F32> &r, const uint8_t *p) {
-    r.a = __ldcs(reinterpret_cast<const uint4 *>(p));
-    r.b = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+template <typename T>
+__device__ __forceinline__ void zero8(Raw8<T> &r) {
+#pragma unroll
+    for (int i = 0; i < 2 * T::kBytes; ++i) r.w[i] = 0;
 }
-__device__ __forceinline__ void zero8(Raw8<BF16> &r) { r.a = make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void zero8(Raw8<F32> &r) { r.a = r.b = make_uint4(0, 0, 0, 0); }
+// From shared memory, or from global memory that is read again shortly.
+template <typename T>
+__device__ __forceinline__ void load8_again(Raw8<T> &r, const uint8_t *p) {
+    load16(r.w, p);
+    if constexpr (T::kBytes == 4) load16(r.w + 4, p + 16);
+}
+// From global memory, read once (not kept in L1, first to leave L2).  A lane's
+// 32 bytes of fp32 are one instruction where the matrix is 32-byte aligned:
+// two of 16 bytes touch every sector twice, and once their first touch has left
+// L1 the second goes to L2 again (SwiGLU's gradient, fp32 8192 x 14336: 403 us
+// against 260 us, decided by how the compiler spaced the two).
+__device__ __forceinline__ void load8(Raw8<BF16> &r, const uint8_t *p, bool) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+}
+__device__ __forceinline__ void load8(Raw8<F32> &r, const uint8_t *p, bool aligned32) {
+    if (aligned32)
+        asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
+                       "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+                     : "l"(p));
+    else
+        load8_again(r, p);
+}
 
-__device__ __forceinline__ void to_f32(const Raw8<BF16> &r, float (&v)[8]) {
-    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+__device__ __forceinline__ V8 to_v8(const Raw8<BF16> &r) {
+    V8 a;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+        a.v[i] = pack2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+    return a;
 }
-__device__ __forceinline__ void to_f32(const Raw8<F32> &r, float (&v)[8]) {
-    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+__device__ __forceinline__ V8 to_v8(const Raw8<F32> &r) {
+    V8 a;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 4; ++i)
+        a.v[i] = pack2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    return a;
 }
 
 // Two bf16 in a word, lo in the low half (round to nearest even).
@@ -69,15 +118,21 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ void from_f32(Raw8<BF16> &r, const float (&v)[8]) {
-    r.a = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                     bf16x2(v[6], v[7]));
+__device__ __forceinline__ void from_v8(Raw8<BF16> &r, const V8 &a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack2(a.v[i], lo, hi);
+        r.w[i] = bf16x2(lo, hi);
+    }
 }
-__device__ __forceinline__ void from_f32(Raw8<F32> &r, const float (&v)[8]) {
-    r.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                     __float_as_uint(v[3]));
-    r.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                     __float_as_uint(v[7]));
+__device__ __forceinline__ void from_v8(Raw8<F32> &r, const V8 &a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack2(a.v[i], lo, hi);
+        r.w[2 * i] = __float_as_uint(lo), r.w[2 * i + 1] = __float_as_uint(hi);
+    }
 }
 
 // A written buffer: its base and extent (the bounds-checked build tests every
@@ -87,71 +142,93 @@ struct Out {
     size_t bytes;
 };
 
+// Eight columns at d, inside o.
 template <typename T>
-__device__ __forceinline__ void store8(const Out &o, int64_t at, const float (&v)[8], int *status) {
+__device__ __forceinline__ void store8(const Out &o, uint8_t *d, const V8 &a, bool aligned32,
+                                       int *status) {
     Raw8<T> r;
-    from_f32(r, v);
-    uint8_t *d = o.p + at * T::kBytes;
+    from_v8(r, a);
     if (!MX_STORE_OK(d, 8 * T::kBytes, o.p, o.bytes, status)) return;
-    reinterpret_cast<uint4 *>(d)[0] = r.a;
-    if constexpr (T::kBytes == 4) reinterpret_cast<uint4 *>(d)[1] = r.b;
+    if constexpr (T::kBytes == 4) {
+        if (aligned32) {
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(d), "r"(r.w[0]),
+                         "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]),
+                         "r"(r.w[6]), "r"(r.w[7])
+                         : "memory");
+            return;
+        }
+        reinterpret_cast<uint4 *>(d)[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    }
+    reinterpret_cast<uint4 *>(d)[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
 }
 
-// A weight vector's 8 columns, of either type (uniform branch).
-__device__ __forceinline__ void load_weight8(const uint8_t *w, bool w_f32, int64_t col,
-                                             float (&v)[8]) {
+// Eight columns of a weight vector of either type (uniform branch).
+__device__ __forceinline__ V8 load_weight8(const uint8_t *w, bool w_f32, uint32_t col) {
     if (w_f32) {
         Raw8<F32> r;
-        r.a = __ldg(reinterpret_cast<const uint4 *>(w + col * 4));
-        r.b = __ldg(reinterpret_cast<const uint4 *>(w + col * 4) + 1);
-        to_f32(r, v);
-    } else {
-        Raw8<BF16> r;
-        r.a = __ldg(reinterpret_cast<const uint4 *>(w + col * 2));
-        to_f32(r, v);
+        load8_again(r, w + 4 * static_cast<size_t>(col));
+        return to_v8(r);
     }
+    Raw8<BF16> r;
+    load8_again(r, w + 2 * static_cast<size_t>(col));
+    return to_v8(r);
 }
 
 // ---------------------------------------------------------------- encode
 struct Encoded {
     Out codes, scales;
     int64_t katoms;  // scale atoms (4 blocks) per 128-line group
+    int64_t pitch;   // bytes of a row of codes
     int fmt;
 };
 
+// A row's codes and scales: where its chunk 0 and its block 0 go.
+struct EncodedRow {
+    uint8_t *codes, *scales;
+};
+__device__ __forceinline__ EncodedRow encoded_row(const Encoded &e, int64_t row) {
+    const uint32_t r = static_cast<uint32_t>(row) & 127u;
+    return {e.codes.p + row * e.pitch,
+            e.scales.p + (static_cast<uint64_t>(row) >> 7) * static_cast<uint64_t>(e.katoms) * 512u +
+                (r & 31u) * 16u + (r >> 5) * 4u};
+}
+
 // Encodes columns 8c .. 8c+7 of a row (c: the lane's chunk, lanes holding
-// consecutive chunks with c % 16 == lane % 16; v = 0 past the row's end) and
-// stores codes and scales.  Called by whole groups of 16 lanes.  The rules are those
-// of mx_quantize and mx_quantize_mxfp8: the exponent of the block's largest
-// magnitude less the format's largest exponent, codes to nearest even and
-// saturating, a block with Inf or NaN: scale 0xFF and zero codes.  Chunks
-// past the row's end give the zero bytes of the scales' padding.
-__device__ __forceinline__ void encode8(const Encoded &e, int64_t row, int64_t cols, int64_t c,
-                                        const float (&v)[8], int *status) {
+// consecutive chunks with c % 16 == lane % 16; `in`: the chunk lies in the row,
+// a is 0 where it does not) and stores codes and scales.  Called by whole
+// groups of 16 lanes.  The rules are those of mx_quantize and
+// mx_quantize_mxfp8: the exponent of the block's largest magnitude less the
+// format's largest exponent, codes to nearest even and saturating, a block
+// with Inf or NaN: scale 0xFF and zero codes.  Chunks past the row's end give
+// the zero bytes of the scales' padding.
+__device__ __forceinline__ void encode8(const Encoded &e, const EncodedRow &at, uint32_t c, bool in,
+                                        const V8 &a, int *status) {
     const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
-    float m = enc::absmax2_nan(enc::absmax3_nan(v[0], v[1], v[2]), enc::absmax3_nan(v[3], v[4], v[5]));
-    m = enc::absmax3_nan(m, v[6], v[7]);
+    float f[8];
+    floats_of(a, f);
+    float m = enc::absmax2_nan(enc::absmax3_nan(f[0], f[1], f[2]), enc::absmax3_nan(f[3], f[4], f[5]));
+    m = enc::absmax3_nan(m, f[6], f[7]);
     m = enc::absmax2_nan(m, __shfl_xor_sync(mask, m, 1));
     m = enc::absmax2_nan(m, __shfl_xor_sync(mask, m, 2));
     float inv;
-    const uint32_t s = e.fmt == kEncMX8 ? enc::scale_of_e4m3(m, inv) : enc::scale_of(m, inv);
-    float q[8];
+    const bool fp8 = e.fmt == kEncMX8;
+    const uint32_t s = fp8 ? enc::scale_of_e4m3(m, inv) : enc::scale_of(m, inv);
+    V8 q;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(v[i], inv);
-    if (8 * c < cols) {
-        if (e.fmt == kEncMX8) {
-            uint2 w = make_uint2(enc::cvt_e4m3x4(q[0], q[1], q[2], q[3]),
-                                 enc::cvt_e4m3x4(q[4], q[5], q[6], q[7]));
+    for (int i = 0; i < 4; ++i) q.v[i] = mul2(a.v[i], same2(inv));
+    floats_of(q, f);
+    if (in) {
+        if (fp8) {
+            uint2 w = make_uint2(enc::cvt_e4m3x4(f[0], f[1], f[2], f[3]),
+                                 enc::cvt_e4m3x4(f[4], f[5], f[6], f[7]));
             if (s == 0xFFu) w = make_uint2(0, 0);
-            uint8_t *d = e.codes.p + row * cols + 8 * c;
-            if (MX_STORE_OK(d, 8, e.codes.p, e.codes.bytes, status))
-                *reinterpret_cast<uint2 *>(d) = w;
+            uint8_t *d = at.codes + 8u * c;
+            if (MX_STORE_OK(d, 8, e.codes.p, e.codes.bytes, status)) *reinterpret_cast<uint2 *>(d) = w;
         } else {
-            uint32_t w = enc::cvt_e2m1x8(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
+            uint32_t w = enc::cvt_e2m1x8(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]);
             if (s == 0xFFu) w = 0;
-            uint8_t *d = e.codes.p + row * (cols / 2) + 4 * c;
-            if (MX_STORE_OK(d, 4, e.codes.p, e.codes.bytes, status))
-                *reinterpret_cast<uint32_t *>(d) = w;
+            uint8_t *d = at.codes + 4u * c;
+            if (MX_STORE_OK(d, 4, e.codes.p, e.codes.bytes, status)) *reinterpret_cast<uint32_t *>(d) = w;
         }
     }
     // The bytes of four blocks to the lane of the first: one word.
@@ -159,9 +236,25 @@ __device__ __forceinline__ void encode8(const Encoded &e, int64_t row, int64_t c
     w |= __shfl_xor_sync(mask, w, 4);
     w |= __shfl_xor_sync(mask, w, 8);
     if ((threadIdx.x & 15) == 0) {
-        uint8_t *d = e.scales.p + enc::scale_offset(row, c / 4, e.katoms);
-        if (MX_STORE_OK(d, 4, e.scales.p, e.scales.bytes, status))
-            *reinterpret_cast<uint32_t *>(d) = w;
+        uint8_t *d = at.scales + (c >> 4) * 512u;
+        if (MX_STORE_OK(d, 4, e.scales.p, e.scales.bytes, status)) *reinterpret_cast<uint32_t *>(d) = w;
+    }
+}
+
+// Words (4 blocks of a line) of the scales' padding lines T .. 128 * ceil(T / 128) - 1.
+__host__ __device__ __forceinline__ int64_t padding_words(const Encoded &e, int64_t T) {
+    return e.fmt == kEncNone ? 0 : (128 - T % 128) % 128 * e.katoms;
+}
+// Zeroes them: the n-th of `threads` threads.
+__device__ __forceinline__ void zero_padding(const Encoded &e, int64_t T, int64_t n, int64_t threads,
+                                             int *status) {
+    const int64_t words = padding_words(e, T);
+    const uint32_t katoms = static_cast<uint32_t>(e.katoms);  // words fit 32 bits: columns are below 2^30
+    for (int64_t i = n; i < words; i += threads) {
+        const uint32_t line = static_cast<uint32_t>(i) / katoms;
+        const uint32_t atom = static_cast<uint32_t>(i) - line * katoms;
+        uint8_t *d = encoded_row(e, T + line).scales + static_cast<size_t>(atom) * 512;
+        if (MX_STORE_OK(d, 4, e.scales.p, e.scales.bytes, status)) *reinterpret_cast<uint32_t *>(d) = 0;
     }
 }
 
@@ -177,19 +270,23 @@ inline Encoded row_encoded(const RowEncode &e, int64_t T, int64_t K) {
     Encoded r{};
     r.fmt = e.fmt;
     r.katoms = scale_katoms(K);
+    r.pitch = e.fmt == kEncMX8 ? K : K / 2;
     r.codes = {static_cast<uint8_t *>(e.codes),
-               static_cast<size_t>(T) * static_cast<size_t>(e.fmt == kEncMX8 ? K : K / 2)};
+               static_cast<size_t>(T) * static_cast<size_t>(r.pitch)};
     r.scales = {static_cast<uint8_t *>(e.scales),
                 static_cast<size_t>(scale_groups(T)) * static_cast<size_t>(r.katoms) * 512};
     return r;
 }
 
+inline bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 // Launch under the library's programmatic-dependent-launch rule (the kernel
 // waits in griddep_wait before it touches global memory).
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int threads,
+cudaError_t launch_dependent(void (*kernel)(Params...), int64_t grid, int threads, size_t smem,
                              cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg{};
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.stream = stream;
