@@ -54,37 +54,40 @@ def _type(t: torch.Tensor, name: str) -> int:
 
 def _rows(t: torch.Tensor, name: str, shape=None):
     """(pointer, mx_type, pitch) of a matrix whose rows are contiguous."""
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        _type(t, name)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be 2-D" + (f" {shape}" if shape else "") + f", got {tuple(t.shape)}")
-    rows, cols = t.shape
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be 2-D" + (f" {tuple(shape)}" if shape else "") + f", got {tuple(t.shape)}")
     pitch, step = t.stride()
+    rows, cols = t.shape
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), _type(t, name), pitch if rows > 1 else cols
+    return t.data_ptr(), kind, pitch if rows > 1 else cols
 
 
-def _vector(t: torch.Tensor, name: str, n: int) -> int:
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-    return _b._dev_ptr(t, name)
+def _vector(t: torch.Tensor, name: str, n: int):
+    """(pointer, mx_type) of a contiguous vector of n elements."""
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        _type(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and [{n}], got {tuple(t.shape)}")
+    return t.data_ptr(), kind
 
 
 def _encoded(fmt, T: int, K: int, device):
     """Empty (codes, scales) of a row-direction encoding."""
-    if fmt is None:
-        return None, None
-    if fmt not in (FMT_MXFP4, FMT_MXFP8):
+    if fmt != FMT_MXFP8 and fmt != FMT_MXFP4:
         raise ValueError("fmt must be None, FMT_MXFP4 or FMT_MXFP8")
-    codes = torch.empty((T, K if fmt == FMT_MXFP8 else K // 2), dtype=torch.uint8, device=device)
     # mx_scales_bytes(T, K), or one byte of an empty operand
     n = -(-T // 128) * 128 * (8 * -(-K // 256))
-    return codes, torch.empty((n or 1,), dtype=torch.uint8, device=device)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return (torch.empty((T, K if fmt == FMT_MXFP8 else K // 2), dtype=torch.uint8, device=device),
+            torch.empty(n or 1, dtype=torch.uint8, device=device))
 
 
 def rmsnorm(x, weight, residual=None, eps: float = 1e-5, fmt=None, want_y: bool = True,
@@ -97,27 +100,30 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-5, fmt=None, want_y: bool 
         with torch.cuda.stream(stream):
             return rmsnorm(x, weight, residual, eps, fmt, want_y, out_h)
     xp, xt, xs = _rows(x, "x")
-    T, K = x.shape
+    shape = x.shape
+    T, K = shape
     d = x.device
-    w = _vector(weight, "weight", K)
+    w, wt = _vector(weight, "weight", K)
     h, rp, rt, rs, hs = out_h, None, 0, 0, 0
     if residual is not None:
-        rp, rt, rs = _rows(residual, "residual", (T, K))
+        rp, rt, rs = _rows(residual, "residual", shape)
         if h is None:
-            h, hs = torch.empty((T, K), dtype=residual.dtype, device=d), K
+            h, hs = torch.empty(shape, dtype=residual.dtype, device=d), K
         else:
-            _, ht, hs = _rows(h, "out_h", (T, K))
+            _, ht, hs = _rows(h, "out_h", shape)
             if ht != rt:
                 raise ValueError("out_h must have the residual's type")
     elif h is not None:
         raise ValueError("out_h needs a residual")
-    y = torch.empty((T, K), dtype=torch.bfloat16, device=d) if want_y else None
-    codes, scales = _encoded(fmt, T, K, d)
-    rstd = torch.empty((T,), dtype=torch.float32, device=d)
-    st = _b.lib().mx_rmsnorm(xp, xt, xs, rp, rt, rs, w, _type(weight, "weight"), eps, T, K, _ptr(h),
-                             hs, _ptr(y), fmt or 0, _ptr(codes), _ptr(scales), rstd.data_ptr(),
-                             _stream(x))
-    _b._check(st, "mx_rmsnorm")
+    y = torch.empty(shape, dtype=torch.bfloat16, device=d) if want_y else None
+    codes, scales = _encoded(fmt, T, K, d) if fmt is not None else (None, None)
+    rstd = torch.empty(T, dtype=torch.float32, device=d)
+    st = (_b._lib or _b.lib()).mx_rmsnorm(
+        xp, xt, xs, rp, rt, rs, w, wt, eps, T, K, None if h is None else h.data_ptr(), hs,
+        None if y is None else y.data_ptr(), fmt or 0, None if codes is None else codes.data_ptr(),
+        None if scales is None else scales.data_ptr(), rstd.data_ptr(), _stream(x))
+    if st:
+        _b._check(st, "mx_rmsnorm")
     return RMSNormOut(h, y, codes, scales, rstd)
 
 
@@ -134,31 +140,40 @@ def rmsnorm_backward(dy, h, weight, rstd, dres=None, want_dw: bool = True, ws=No
         with torch.cuda.stream(stream):
             return rmsnorm_backward(dy, h, weight, rstd, dres, want_dw, ws, out_dx)
     dp, dt, ds = _rows(dy, "dy")
-    T, K = dy.shape
-    hp, ht, hs = _rows(h, "h", (T, K))
-    w = _vector(weight, "weight", K)
-    r = _vector(rstd, "rstd", T)
-    if rstd.dtype != torch.float32:
+    shape = dy.shape
+    T, K = shape
+    d = dy.device
+    hp, ht, hs = _rows(h, "h", shape)
+    w, wt = _vector(weight, "weight", K)
+    r, kind = _vector(rstd, "rstd", T)
+    if kind != _F32:
         raise ValueError("rstd must be float32")
     gp, gs = None, 0
     if dres is not None:
-        gp, gt, gs = _rows(dres, "dres", (T, K))
+        gp, gt, gs = _rows(dres, "dres", shape)
         if gt != ht:
             raise ValueError("dres must have h's type")
     if out_dx is None:
-        out_dx = torch.empty((T, K), dtype=h.dtype, device=dy.device)
-    op, ot, os_ = _rows(out_dx, "out_dx", (T, K))
-    if ot != ht:
-        raise ValueError("out_dx must have h's type")
-    dw = torch.empty((K,), dtype=torch.float32, device=dy.device) if want_dw else None
-    if ws is None and want_dw:
-        ws = torch.empty((max(rmsnorm_backward_workspace_bytes(T, K), 256),), dtype=torch.uint8,
-                         device=dy.device)
-    st = _b.lib().mx_rmsnorm_backward(dp, dt, ds, hp, ht, hs, w, _type(weight, "weight"), r, gp, gs,
-                                      T, K, op, os_, _ptr(dw), _ptr(ws),
-                                      0 if ws is None else ws.numel() * ws.element_size(),
-                                      _stream(dy))
-    _b._check(st, "mx_rmsnorm_backward")
+        out_dx = torch.empty(shape, dtype=h.dtype, device=d)
+        op, os_ = out_dx.data_ptr(), K
+    else:
+        op, ot, os_ = _rows(out_dx, "out_dx", shape)
+        if ot != ht:
+            raise ValueError("out_dx must have h's type")
+    L = _b._lib or _b.lib()
+    dw, wp, n = None, None, 0
+    if want_dw:
+        dw = torch.empty(K, dtype=torch.float32, device=d)
+        if ws is None:
+            n = L.mx_rmsnorm_backward_workspace_bytes(T, K)
+            ws = torch.empty(n or 1, dtype=torch.uint8, device=d)
+        else:
+            n = ws.numel() * ws.element_size()
+        wp = _b._dev_ptr(ws, "workspace")
+    st = L.mx_rmsnorm_backward(dp, dt, ds, hp, ht, hs, w, wt, r, gp, gs, T, K, op, os_,
+                               None if dw is None else dw.data_ptr(), wp, n, _stream(dy))
+    if st:
+        _b._check(st, "mx_rmsnorm_backward")
     return out_dx, dw
 
 
@@ -169,15 +184,19 @@ def swiglu(gu, fmt=None, want_y: bool = True, stream=None) -> SwiGLUOut:
         with torch.cuda.stream(stream):
             return swiglu(gu, fmt, want_y)
     p, t, s = _rows(gu, "gu")
-    T, F2 = gu.shape
-    if F2 % 2:
+    T, F = gu.shape
+    if F % 2:
         raise ValueError("gu must have an even number of columns")
-    F = F2 // 2
-    y = torch.empty((T, F), dtype=torch.bfloat16, device=gu.device) if want_y else None
-    codes, scales = _encoded(fmt, T, F, gu.device)
-    st = _b.lib().mx_swiglu(p, t, s, T, F, _ptr(y), fmt or 0, _ptr(codes), _ptr(scales),
-                            _stream(gu))
-    _b._check(st, "mx_swiglu")
+    F //= 2
+    d = gu.device
+    y = torch.empty((T, F), dtype=torch.bfloat16, device=d) if want_y else None
+    codes, scales = _encoded(fmt, T, F, d) if fmt is not None else (None, None)
+    st = (_b._lib or _b.lib()).mx_swiglu(
+        p, t, s, T, F, None if y is None else y.data_ptr(), fmt or 0,
+        None if codes is None else codes.data_ptr(), None if scales is None else scales.data_ptr(),
+        _stream(gu))
+    if st:
+        _b._check(st, "mx_swiglu")
     return SwiGLUOut(y, codes, scales)
 
 
@@ -193,9 +212,10 @@ def swiglu_backward(dy, gu, out=None, stream=None) -> torch.Tensor:
         out = torch.empty((T, 2 * F), dtype=torch.bfloat16, device=dy.device)
     elif tuple(out.shape) != (T, 2 * F) or _type(out, "out") != _BF16:
         raise ValueError(f"out must be bf16 [{T}, {2 * F}]")
-    st = _b.lib().mx_swiglu_backward(dp, dt, ds, gp, gt, gs, T, F, _b._dev_ptr(out, "out"),
-                                     _stream(dy))
-    _b._check(st, "mx_swiglu_backward")
+    st = (_b._lib or _b.lib()).mx_swiglu_backward(dp, dt, ds, gp, gt, gs, T, F, _b._dev_ptr(out, "out"),
+                                                  _stream(dy))
+    if st:
+        _b._check(st, "mx_swiglu_backward")
     return out
 
 
@@ -227,9 +247,9 @@ def _at(a):
 
 def _grad_buffers(tensors, ws):
     d = tensors[0].device if tensors else "cuda"
-    norm = torch.empty((1,), dtype=torch.float32, device=d)
+    norm = torch.empty(1, dtype=torch.float32, device=d)
     if ws is None:
-        ws = torch.empty((max(grad_workspace_bytes(len(tensors)), 256),), dtype=torch.uint8, device=d)
+        ws = torch.empty(grad_workspace_bytes(len(tensors)) or 1, dtype=torch.uint8, device=d)
     return norm, ws
 
 

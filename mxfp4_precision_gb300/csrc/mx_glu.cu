@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(256) mx_swiglu_kernel(const __grid_constant__ 
     const Place at = place(p);
     const uint32_t col = 8 * at.c;
     const bool in = col < p.F;
+    // Only a warp that the row ends in has lanes to clear.
+    const bool full = col - 8 * (at.c & 31) + 256 <= p.F;
     const uint8_t *src = p.gu + static_cast<size_t>(col) * G::kBytes;
     const size_t up = static_cast<size_t>(p.F) * G::kBytes;
     // Whole warps share a row, so that its blocks are encoded together.
@@ -80,8 +82,10 @@ __global__ void __launch_bounds__(256) mx_swiglu_kernel(const __grid_constant__ 
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int64_t r = row + k * at.deep;
-            zero8(gr[k]);
-            zero8(ur[k]);
+            if (!full) {
+                zero8(gr[k]);
+                zero8(ur[k]);
+            }
             if (in && r < at.end) {
                 load8(gr[k], src + r * p.gu_pitch, p.aligned32);
                 load8(ur[k], src + r * p.gu_pitch + up, p.aligned32);

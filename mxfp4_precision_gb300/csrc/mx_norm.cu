@@ -29,21 +29,21 @@ struct NormArgs {
     float eps;
     bool aligned32;
     int w_f32;
-    int tpr;         // threads per row, a multiple of 32
+    int tpr, groups;  // threads per row (a multiple of 32), rows per block
     uint32_t tiles;  // blocks that hold rows; those after them zero the scales' padding lines
     int *status;
 };
 
 // Sum over the tpr threads of a row (the whole block takes part: rows of one
 // block reduce in step).  `part` holds one float per warp.
-__device__ __forceinline__ float sum_row(float v, int tpr, float *part) {
+__device__ __forceinline__ float sum_row(float v, int g, int tpr, float *part) {
     v = sum_lanes(v, 32);
     if (tpr == 32) return v;
-    const int warp = threadIdx.x >> 5, n = tpr >> 5, first = warp / n * n;
-    if ((threadIdx.x & 31) == 0) part[warp] = v;
+    const int n = tpr >> 5;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.0f;
-    for (int i = 0; i < n; ++i) v += part[first + i];
+    for (int i = 0; i < n; ++i) v += part[g * n + i];
     return v;
 }
 
@@ -94,9 +94,16 @@ __device__ __forceinline__ void rstd_out(const NormArgs &p, int64_t row, float r
 }
 
 // One row per tpr threads and no turn after it, C chunks of 8 columns per
-// thread, the row in registers between its sum and its output.
+// thread, the row in registers between its sum and its output.  Blocks per SM that the registers must allow: the loads in flight are what
+// counts, and the compiler left alone takes C = 4 to one block of 512 threads
+// (bf16, 2048 x 16384: 67 us against 51 us).
+template <typename X, typename S, int C, int THREADS>
+constexpr int norm_blocks() {
+    if (THREADS > 256) return THREADS > 512 ? 1 : 2;
+    return C == 1 ? 6 : C == 2 ? 5 : C <= 4 ? 4 : X::kBytes + S::kBytes == 8 ? 2 : 3;
+}
 template <typename X, typename S, bool RES, int C, int THREADS>
-__global__ void __launch_bounds__(THREADS) mx_rmsnorm_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(THREADS, norm_blocks<X, S, C, THREADS>()) mx_rmsnorm_kernel(const __grid_constant__ NormArgs p) {
     __shared__ float part[32];
     griddep_wait();
     griddep_launch_dependents();
@@ -105,26 +112,33 @@ __global__ void __launch_bounds__(THREADS) mx_rmsnorm_kernel(const __grid_consta
                      static_cast<int64_t>(gridDim.x - p.tiles) * blockDim.x, p.status);
         return;
     }
-    const int tr = threadIdx.x % p.tpr;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.tpr) + threadIdx.x / p.tpr;
+    int g = 0, tr = threadIdx.x;
+    if (p.groups > 1) {
+        g = p.tpr == 32 ? tr >> 5 : tr / p.tpr;
+        tr -= g * p.tpr;
+    }
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * p.groups + g;
     const bool live = row < p.T;
+    const uint8_t *x = p.x + row * p.x_pitch, *res = p.res + row * p.res_pitch;
     Raw8<X> xr[C];
     Raw8<S> rr[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
         const uint32_t col = 8 * (j * p.tpr + tr);
-        zero8(xr[j]);
-        zero8(rr[j]);
-        if (live && col < p.K) {
-            load8(xr[j], p.x + row * p.x_pitch + col * X::kBytes, p.aligned32);
-            if (RES) load8(rr[j], p.res + row * p.res_pitch + col * S::kBytes, p.aligned32);
+        // Only a warp that the row ends in has lanes to clear.
+        if (!live || col - 8 * (tr & 31) + 256 > p.K) {
+            zero8(xr[j]);
+            zero8(rr[j]);
+            if (!live || col >= p.K) continue;
         }
+        load8(xr[j], x + col * X::kBytes, p.aligned32);
+        if (RES) load8(rr[j], res + col * S::kBytes, p.aligned32);
     }
     V8 h[C];
     uint64_t ss = 0;
 #pragma unroll
     for (int j = 0; j < C; ++j) h[j] = join<X, S, RES>(xr[j], rr[j], ss);
-    const float rstd = rstd_of(sum_row(sum2(ss), p.tpr, part), p.K, p.eps);
+    const float rstd = rstd_of(sum_row(sum2(ss), g, p.tpr, part), p.K, p.eps);
     if (!live) return;
     if (tr == 0) rstd_out(p, row, rstd);
     const NormRow at = norm_row(p, row);
@@ -158,6 +172,7 @@ struct Ring {
     // Sum over the group, and whether every thread's wait ended well.
     __device__ __forceinline__ bool sum(float &v, bool ok, int turn) {
         v = sum_lanes(v, 32);
+        if (tpr == 32) return __all_sync(0xFFFFFFFFu, ok);
         float *at = part + (turn & 1) * 32;
         const int tr = threadIdx.x % tpr;
         if ((tr & 31) == 0) at[tr >> 5] = v;
@@ -165,6 +180,11 @@ struct Ring {
         v = 0.0f;
         for (int i = 0; i < tpr >> 5; ++i) v += at[i];
         return ok;
+    }
+    // Every thread of the group is done with the slot.
+    __device__ __forceinline__ void done() {
+        if (tpr == 32) __syncwarp();
+        else bar_and(id, tpr, true);
     }
     // After a wait that ran out: the slots still being filled, before the block ends.
     __device__ __forceinline__ void drain(int64_t left) {
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(THREADS)
             V8 a = to_v8(dr[j]);
             look(a, to_v8(hr[j]), load_weight8(p.w, p.w_f32 != 0, col), rstd, dw[j], sums);
         }
-        const float along = sum_row(sum2(sums), p.tpr, part[turn]) / static_cast<float>(p.K);
+        const float along = sum_row(sum2(sums), g, p.tpr, part[turn]) / static_cast<float>(p.K);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const uint32_t col = 8 * (j * p.tpr + tr);
@@ -345,9 +365,11 @@ __global__ void __launch_bounds__(THREADS)
     sum_groups<C>(p, reinterpret_cast<float *>(smem), dw);
 }
 
-// Many rows, through the ring.  The groups' weight gradients are summed in shared memory at the end: one partial
-// per block.
-template <typename D, typename S, int C, int THREADS>
+// Many rows, through the ring.  LOOK2: a row is read from its slot twice, once
+// for mean(dy * w * h) and once for dx, instead of staying in registers between
+// them; the slot is then free only after the second.  The groups' weight
+// gradients are summed in shared memory at the end: one partial per block.
+template <typename D, typename S, int C, int THREADS, bool LOOK2>
 __global__ void __launch_bounds__(THREADS)
     mx_rmsnorm_backward_ring_kernel(const __grid_constant__ NormGradArgs p) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -359,6 +381,7 @@ __global__ void __launch_bounds__(THREADS)
     griddep_launch_dependents();
     const int tr = threadIdx.x % p.tpr, groups = blockDim.x / p.tpr, g = threadIdx.x / p.tpr;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
+    // Neighbouring blocks take neighbouring rows.
     int64_t row = static_cast<int64_t>(g) * gridDim.x + blockIdx.x;
     const uint64_t once = l2_evict_first_policy();
     auto fill = [&](int64_t r, int s) {
@@ -395,7 +418,7 @@ __global__ void __launch_bounds__(THREADS)
             if (col < p.K) {
                 load8_again(dr, slot + col * D::kBytes);
                 load8_again(hr[j], slot + db + col * S::kBytes);
-                if (res) load8_again(gr[j], slot + db + sb + col * S::kBytes);
+                if (!LOOK2 && res) load8_again(gr[j], slot + db + sb + col * S::kBytes);
             }
             a[j] = to_v8(dr);
             look(a[j], to_v8(hr[j]), w[j], rstd, dw[j], sums);
@@ -406,18 +429,32 @@ __global__ void __launch_bounds__(THREADS)
             if (tr == 0) ring.drain((p.T - row + stride - 1) / stride);
             break;
         }
-        if (tr == 0 && row + p.stages * stride < p.T) fill(row + p.stages * stride, ring.s);
-        ring.next();
+        const int64_t next = row + p.stages * stride;
+        if (!LOOK2 && tr == 0 && next < p.T) fill(next, ring.s);
         along /= static_cast<float>(p.K);
         uint8_t *dx = p.dx.p + row * p.dx_pitch;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const uint32_t col = 8 * (j * p.tpr + tr);
             if (col >= p.K) continue;
+            if (LOOK2) {
+                Raw8<D> dr;
+                load8_again(dr, slot + col * D::kBytes);
+                load8_again(hr[j], slot + db + col * S::kBytes);
+                if (res) load8_again(gr[j], slot + db + sb + col * S::kBytes);
+                a[j] = to_v8(dr);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[j].v[i] = mul2(a[j].v[i], w[j].v[i]);
+            }
             V8 v = to_v8(gr[j]);
             finish(a[j], to_v8(hr[j]), rstd, along, v);
             store8<S>(p.dx, dx + col * S::kBytes, v, p.aligned32, p.status);
         }
+        if (LOOK2) {
+            ring.done();
+            if (tr == 0 && next < p.T) fill(next, ring.s);
+        }
+        ring.next();
     }
     if (p.parts.p == nullptr) return;
     // All slots are consumed (or drained): the ring's memory holds the groups' sums.
@@ -463,11 +500,13 @@ RowShape row_shape(int64_t n, int c) {
 }
 
 // One warp a row (no barrier) for rows of up to 160 chunks, once the rows
-// fill the SMs; two chunks a thread otherwise, four where a row needs more than
-// 1024 threads.
+// fill the SMs; otherwise two or three chunks a thread, whichever leaves fewer
+// threads without one, and four where a row needs more than 1024 threads.
 RowShape norm_shape(int64_t T, int64_t K, const DeviceInfo &dev) {
     const int64_t n = padded_chunks(K);
     if (n <= 32 || (n <= 160 && T >= 16ll * dev.sm_count)) return row_shape(n, static_cast<int>(n / 32));
+    const RowShape two = row_shape(n, 2), three = row_shape(n, 3);
+    if (n <= 1024 && three.tpr * 3 < two.tpr * 2) return three;
     return row_shape(n, n <= 1024 ? 2 : 4);
 }
 
@@ -475,6 +514,7 @@ template <typename X, typename S, bool RES>
 cudaError_t launch_norm(NormArgs &p, const DeviceInfo &dev, cudaStream_t stream) {
     const RowShape s = norm_shape(p.T, p.K, dev);
     p.tpr = s.tpr;
+    p.groups = s.groups;
     const int threads = s.tpr * s.groups;
     const int64_t tiles = (p.T + s.groups - 1) / s.groups;
     const int64_t grid = tiles + (padding_words(p.enc, p.T) + threads - 1) / threads;
@@ -484,17 +524,20 @@ cudaError_t launch_norm(NormArgs &p, const DeviceInfo &dev, cudaStream_t stream)
     launch_dependent(mx_rmsnorm_kernel<X, S, RES, C, THREADS>, grid, threads, 0, stream, p)
     switch (s.c) {
         case 1: return MX_NORM_CASE(1, 256);
-        case 2: return MX_NORM_CASE(2, 512);
-        case 3: return MX_NORM_CASE(3, 256);
+        case 2: return threads <= 256 ? MX_NORM_CASE(2, 256) : MX_NORM_CASE(2, 512);
+        case 3: return threads <= 256 ? MX_NORM_CASE(3, 256) : MX_NORM_CASE(3, 512);
         case 5: return MX_NORM_CASE(5, 256);
-        default: return threads <= 512 ? MX_NORM_CASE(4, 512) : MX_NORM_CASE(4, 1024);
+        default:
+            return threads <= 256   ? MX_NORM_CASE(4, 256)
+                   : threads <= 512 ? MX_NORM_CASE(4, 512)
+                                    : MX_NORM_CASE(4, 1024);
     }
 #undef MX_NORM_CASE
 }
 
 constexpr int kGradBlocks = 304;  // of the direct gradient kernel, at most
 constexpr int kRingThreads = 512;
-constexpr int kRingTurns = 4;  // rows a group must have for the ring to pay
+constexpr int kRingTurns = 2;  // rows a group must have for the ring to pay
 constexpr size_t kRingSmem = 220 * 1024;
 
 RowShape grad_shape(int64_t T, int64_t K) {
@@ -509,12 +552,13 @@ int64_t grad_grid(int64_t T, const RowShape &s) {
     return want < kGradBlocks ? want : kGradBlocks;
 }
 
-// The ring's shape for rows of `bytes`, or stages = 0 where it does not apply.
+// The ring's shape for rows of `bytes`, or stages = 0 where it does not apply:
+// one warp a row up to 160 chunks, then two chunks a thread, four above 1024.
 RowShape ring_shape(int64_t T, int64_t K, size_t bytes, const DeviceInfo &dev) {
     const int64_t n = padded_chunks(K);
-    RowShape s = row_shape(n, 2);
+    RowShape s = row_shape(n, n <= 160 ? static_cast<int>(n / 32) : n <= 1024 ? 2 : 4);
     s.groups = kRingThreads / s.tpr;
-    if (n <= 160 || s.groups < 1 || T < static_cast<int64_t>(kRingTurns) * s.groups * dev.sm_count) return s;
+    if (s.groups < 1 || T < static_cast<int64_t>(kRingTurns) * s.groups * dev.sm_count) return s;
     s.stages = static_cast<int>((kRingSmem - 256 * s.groups) / (s.groups * (bytes + 8)));
     if (s.stages > 8) s.stages = 8;
     if (s.stages < 2) s.stages = 0;
@@ -546,7 +590,16 @@ cudaError_t launch_norm_grad(NormGradArgs &p, int64_t *n_parts, const DeviceInfo
         const cudaError_t e = with_smem(kernel, s.smem);
         return e != cudaSuccess ? e : launch_dependent(kernel, grid, threads, s.smem, stream, p);
     };
-    if (ring) return go(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads>);
+    if (ring) {
+        if (s.tpr > 32 && s.c == 2) return go(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads, false>);
+        switch (s.c) {
+            case 1: return go(mx_rmsnorm_backward_ring_kernel<D, S, 1, kRingThreads, true>);
+            case 2: return go(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads, true>);
+            case 3: return go(mx_rmsnorm_backward_ring_kernel<D, S, 3, kRingThreads, true>);
+            case 4: return go(mx_rmsnorm_backward_ring_kernel<D, S, 4, kRingThreads, true>);
+            default: return go(mx_rmsnorm_backward_ring_kernel<D, S, 5, kRingThreads, true>);
+        }
+    }
     switch (s.c) {
         case 1: return go(mx_rmsnorm_backward_kernel<D, S, 1, 256, false>);
         case 2: return go(mx_rmsnorm_backward_kernel<D, S, 2, 256, false>);

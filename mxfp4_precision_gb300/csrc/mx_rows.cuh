@@ -4,8 +4,7 @@
 // rows whose columns lie across lanes.
 //
 // Every kernel here gives each thread chunks of 8 consecutive columns: 16
-// bytes of bf16, 32 of fp32.  Four lanes hold one 32-column block, 16 lanes
-// the four blocks whose scale bytes are one word of the tiled layout.
+// bytes of bf16, 32 of fp32.  Four lanes hold one 32-column block.
 #pragma once
 
 #include <cstdint>
@@ -194,22 +193,21 @@ __device__ __forceinline__ EncodedRow encoded_row(const Encoded &e, int64_t row)
 }
 
 // Encodes columns 8c .. 8c+7 of a row (c: the lane's chunk, lanes holding
-// consecutive chunks with c % 16 == lane % 16; `in`: the chunk lies in the row,
+// consecutive chunks with c % 32 == lane; `in`: the chunk lies in the row,
 // a is 0 where it does not) and stores codes and scales.  Called by whole
-// groups of 16 lanes.  The rules are those of mx_quantize and
+// warps.  The rules are those of mx_quantize and
 // mx_quantize_mxfp8: the exponent of the block's largest magnitude less the
 // format's largest exponent, codes to nearest even and saturating, a block
 // with Inf or NaN: scale 0xFF and zero codes.  Chunks past the row's end give
 // the zero bytes of the scales' padding.
 __device__ __forceinline__ void encode8(const Encoded &e, const EncodedRow &at, uint32_t c, bool in,
                                         const V8 &a, int *status) {
-    const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
     float f[8];
     floats_of(a, f);
     float m = enc::absmax2_nan(enc::absmax3_nan(f[0], f[1], f[2]), enc::absmax3_nan(f[3], f[4], f[5]));
     m = enc::absmax3_nan(m, f[6], f[7]);
-    m = enc::absmax2_nan(m, __shfl_xor_sync(mask, m, 1));
-    m = enc::absmax2_nan(m, __shfl_xor_sync(mask, m, 2));
+    m = enc::absmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = enc::absmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     float inv;
     const bool fp8 = e.fmt == kEncMX8;
     const uint32_t s = fp8 ? enc::scale_of_e4m3(m, inv) : enc::scale_of(m, inv);
@@ -231,13 +229,10 @@ __device__ __forceinline__ void encode8(const Encoded &e, const EncodedRow &at, 
             if (MX_STORE_OK(d, 4, e.codes.p, e.codes.bytes, status)) *reinterpret_cast<uint32_t *>(d) = w;
         }
     }
-    // The bytes of four blocks to the lane of the first: one word.
-    uint32_t w = s << (2 * (threadIdx.x & 12));
-    w |= __shfl_xor_sync(mask, w, 4);
-    w |= __shfl_xor_sync(mask, w, 8);
-    if ((threadIdx.x & 15) == 0) {
-        uint8_t *d = at.scales + (c >> 4) * 512u;
-        if (MX_STORE_OK(d, 4, e.scales.p, e.scales.bytes, status)) *reinterpret_cast<uint32_t *>(d) = w;
+    // One byte a block: the eight of a warp lie in two sectors, as two gathered words would.
+    if ((threadIdx.x & 3) == 0) {
+        uint8_t *d = at.scales + (c >> 4) * 512u + ((c >> 2) & 3u);
+        if (MX_STORE_OK(d, 1, e.scales.p, e.scales.bytes, status)) *d = static_cast<uint8_t>(s);
     }
 }
 
