@@ -38,27 +38,36 @@ struct Table {
     int chunk;
 };
 
-struct Piece {
-    int tensor;
-    int64_t begin;
-    int len;
-};
-
+// A block's chunks are a contiguous share of all; it walks them with the tensor
+// it is in, which one search finds (the table lies in constant memory, a
+// search costs as long as a chunk's loads).
 template <int N>
-__device__ __forceinline__ Piece piece_of(const Table<N> &t, uint32_t chunk) {
-    int lo = 0, hi = t.count;  // first[lo] <= chunk < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (t.first[mid] <= chunk) lo = mid;
-        else hi = mid;
+struct Walk {
+    uint32_t begin, end;  // chunks
+    int tensor;
+
+    __device__ __forceinline__ Walk(const Table<N> &t, bool backwards) {
+        const uint64_t all = t.first[t.count];
+        begin = static_cast<uint32_t>(all * blockIdx.x / gridDim.x);
+        end = static_cast<uint32_t>(all * (blockIdx.x + 1) / gridDim.x);
+        const uint32_t at = backwards ? end - 1 : begin;
+        int lo = 0, hi = t.count;  // first[lo] <= at < first[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (t.first[mid] <= at) lo = mid;
+            else hi = mid;
+        }
+        tensor = lo;
     }
-    Piece r;
-    r.tensor = lo;
-    r.begin = static_cast<int64_t>(chunk - t.first[lo]) * t.chunk;
-    const int64_t left = t.n[lo] - r.begin;
-    r.len = static_cast<int>(left < t.chunk ? left : t.chunk);
-    return r;
-}
+    // Elements [first, first + len) of the tensor that chunk c lies in.
+    __device__ __forceinline__ int piece(const Table<N> &t, uint32_t c, int64_t &first) {
+        while (t.first[tensor + 1] <= c) ++tensor;
+        while (t.first[tensor] > c) --tensor;
+        first = static_cast<int64_t>(c - t.first[tensor]) * t.chunk;
+        const int64_t left = t.n[tensor] - first;
+        return static_cast<int>(left < t.chunk ? left : t.chunk);
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ float load1(const uint8_t *p, int i) {
@@ -128,24 +137,29 @@ __device__ __forceinline__ float sum_squares(const uint8_t *p, int len) {
         ends = fmaf(v, v, ends);
     }
     const uint8_t *body = p + q.head * T::kBytes;
-    uint64_t body2[kUnroll] = {};
-    for (int i = t; i < q.whole; i += kUnroll * kThreads) {
+    uint64_t sums[kUnroll] = {};
+    auto take = [&](const Raw8<T> &r, uint64_t &sum) {
+        const V8 v = to_v8(r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum = fma2(v.v[j], v.v[j], sum);
+    };
+    auto at = [&](int i) { return body + static_cast<int64_t>(i) * 8 * T::kBytes; };
+    int i = t;
+    // Groups of loads without a condition between them, so that they are in flight
+    // together (a condition each: one at a time, 136 us against 124 us for 218M fp32).
+    for (; i + (kUnroll - 1) * kThreads < q.whole; i += kUnroll * kThreads) {
         Raw8<T> r[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            zero8(r[k]);
-            // default cache policy: the scaling pass reads the last of this again
-            if (i + k * kThreads < q.whole)
-                load8_again(r[k], body + static_cast<int64_t>(i + k * kThreads) * 8 * T::kBytes);
-        }
+        for (int k = 0; k < kUnroll; ++k) load8(r[k], at(i + k * kThreads));
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const V8 v = to_v8(r[k]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) body2[k] = fma2(v.v[j], v.v[j], body2[k]);
-        }
+        for (int k = 0; k < kUnroll; ++k) take(r[k], sums[k]);
     }
-    return ends + sum2(add2(add2(body2[0], body2[1]), add2(body2[2], body2[3])));
+    for (; i < q.whole; i += kThreads) {
+        Raw8<T> r;
+        load8(r, at(i));
+        take(r, sums[0]);
+    }
+    return ends + sum2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
 }
 
 template <int N>
@@ -155,11 +169,13 @@ __global__ void __launch_bounds__(kThreads) mx_grad_sums_kernel(const __grid_con
     griddep_wait();
     griddep_launch_dependents();
     float s = 0.0f;
-    for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-        const Piece q = piece_of(t, c);
-        const bool f32 = t.f32[q.tensor] != 0;
-        const uint8_t *p = t.p[q.tensor] + q.begin * (f32 ? 4 : 2);
-        s += f32 ? sum_squares<F32>(p, q.len) : sum_squares<BF16>(p, q.len);
+    Walk<N> walk(t, false);
+    for (uint32_t c = walk.begin; c < walk.end; ++c) {
+        int64_t first;
+        const int len = walk.piece(t, c, first);
+        const bool f32 = t.f32[walk.tensor] != 0;
+        const uint8_t *p = t.p[walk.tensor] + first * (f32 ? 4 : 2);
+        s += f32 ? sum_squares<F32>(p, len) : sum_squares<BF16>(p, len);
     }
     const Sum all = sum_block({s, 0.0f}, part);
     if (threadIdx.x == 0) sums[blockIdx.x] = all;
@@ -192,30 +208,33 @@ __device__ __forceinline__ void scale_piece(const Out &whole, const uint8_t *p, 
     const uint8_t *body = p + q.head * T::kBytes;
     uint8_t *dst = out + q.head * O::kBytes;
     const bool aligned32 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
-    for (int i = t; i < q.whole; i += kUnroll * kThreads) {
+    auto at = [&](int i) { return body + static_cast<int64_t>(i) * 8 * T::kBytes; };
+    auto put = [&](const Raw8<T> &r, int i) {
+        V8 v = to_v8(r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v.v[j] = mul2(v.v[j], same2(coef));
+        store8<O>(whole, dst + static_cast<int64_t>(i) * 8 * O::kBytes, v, aligned32, status);
+    };
+    int n = t;
+    for (; n + (kUnroll - 1) * kThreads < q.whole; n += kUnroll * kThreads) {
         Raw8<T> r[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            zero8(r[k]);
-            if (i + k * kThreads < q.whole)
-                load8(r[k], body + static_cast<int64_t>(i + k * kThreads) * 8 * T::kBytes, true);
-        }
+        for (int k = 0; k < kUnroll; ++k) load8(r[k], at(n + k * kThreads));
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            if (i + k * kThreads >= q.whole) continue;
-            V8 v = to_v8(r[k]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v.v[j] = mul2(v.v[j], same2(coef));
-            store8<O>(whole, dst + static_cast<int64_t>(i + k * kThreads) * 8 * O::kBytes, v, aligned32, status);
-        }
+        for (int k = 0; k < kUnroll; ++k) put(r[k], n + k * kThreads);
     }
-    for (int i = tail + t; i < len; i += 2 * kUnroll * kThreads) {
-        float v[2 * kUnroll];
+    for (; n < q.whole; n += kThreads) {
+        Raw8<T> r;
+        load8(r, at(n));
+        put(r, n);
+    }
+    for (int i = tail + t; i < len; i += 4 * kUnroll * kThreads) {
+        float v[4 * kUnroll];
 #pragma unroll
-        for (int k = 0; k < 2 * kUnroll; ++k)
+        for (int k = 0; k < 4 * kUnroll; ++k)
             v[k] = i + k * kThreads < len ? load1<T>(p, i + k * kThreads) : 0.0f;
 #pragma unroll
-        for (int k = 0; k < 2 * kUnroll; ++k)
+        for (int k = 0; k < 4 * kUnroll; ++k)
             if (i + k * kThreads < len) store1<O>(whole, out, i + k * kThreads, v[k] * coef, status);
     }
 }
@@ -233,20 +252,21 @@ __global__ void __launch_bounds__(kThreads) mx_grad_scale_kernel(const __grid_co
     float coef = max_norm / (total + eps);
     if (coef > 1.0f) coef = 1.0f;  // a NaN stays
     // Backwards: what the sums read last is still in L2.
-    const uint32_t chunks = t.first[t.count];
-    for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-        const Piece q = piece_of(t, chunks - 1 - i);
-        const bool f32 = t.f32[q.tensor] != 0, out_f32 = t.out_f32[q.tensor] != 0;
-        const uint8_t *p = t.p[q.tensor] + q.begin * (f32 ? 4 : 2);
-        uint8_t *out = t.out[q.tensor] + q.begin * (out_f32 ? 4 : 2);
-        const Out whole{t.out[q.tensor], static_cast<size_t>(t.n[q.tensor]) * (out_f32 ? 4 : 2)};
+    Walk<N> walk(t, true);
+    for (uint32_t c = walk.end; c-- > walk.begin;) {
+        int64_t first;
+        const int len = walk.piece(t, c, first), k = walk.tensor;
+        const bool f32 = t.f32[k] != 0, out_f32 = t.out_f32[k] != 0;
+        const uint8_t *p = t.p[k] + first * (f32 ? 4 : 2);
+        uint8_t *out = t.out[k] + first * (out_f32 ? 4 : 2);
+        const Out whole{t.out[k], static_cast<size_t>(t.n[k]) * (out_f32 ? 4 : 2)};
         if (p == out && coef == 1.0f) continue;  // in place and nothing to change
         if (f32) {
-            if (out_f32) scale_piece<F32, F32>(whole, p, out, q.len, coef, status);
-            else scale_piece<F32, BF16>(whole, p, out, q.len, coef, status);
+            if (out_f32) scale_piece<F32, F32>(whole, p, out, len, coef, status);
+            else scale_piece<F32, BF16>(whole, p, out, len, coef, status);
         } else {
-            if (out_f32) scale_piece<BF16, F32>(whole, p, out, q.len, coef, status);
-            else scale_piece<BF16, BF16>(whole, p, out, q.len, coef, status);
+            if (out_f32) scale_piece<BF16, F32>(whole, p, out, len, coef, status);
+            else scale_piece<BF16, BF16>(whole, p, out, len, coef, status);
         }
     }
 }

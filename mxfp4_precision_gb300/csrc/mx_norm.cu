@@ -383,13 +383,12 @@ __global__ void __launch_bounds__(THREADS)
     const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
     // Neighbouring blocks take neighbouring rows.
     int64_t row = static_cast<int64_t>(g) * gridDim.x + blockIdx.x;
-    const uint64_t once = l2_evict_first_policy();
     auto fill = [&](int64_t r, int s) {
         uint8_t *d = ring.slots + s * ring.slot_bytes;
         mbar_arrive_expect_tx(&ring.full[s], bytes);
-        bulk_load_hint(d, p.dy + r * p.dy_pitch, db, &ring.full[s], once);
-        bulk_load_hint(d + db, p.h + r * p.h_pitch, sb, &ring.full[s], once);
-        if (res) bulk_load_hint(d + db + sb, p.dres + r * p.dres_pitch, sb, &ring.full[s], once);
+        bulk_load(d, p.dy + r * p.dy_pitch, db, &ring.full[s]);
+        bulk_load(d + db, p.h + r * p.h_pitch, sb, &ring.full[s]);
+        if (res) bulk_load(d + db + sb, p.dres + r * p.dres_pitch, sb, &ring.full[s]);
     };
     if (tr == 0)
         for (int s = 0; s < p.stages; ++s)

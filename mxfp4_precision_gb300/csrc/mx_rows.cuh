@@ -77,18 +77,22 @@ __device__ __forceinline__ void load8_again(Raw8<T> &r, const uint8_t *p) {
     load16(r.w, p);
     if constexpr (T::kBytes == 4) load16(r.w + 4, p + 16);
 }
-// From global memory, read once (not kept in L1, first to leave L2).  A lane's
-// 32 bytes of fp32 are one instruction where the matrix is 32-byte aligned:
-// two of 16 bytes touch every sector twice, and once their first touch has left
-// L1 the second goes to L2 again (SwiGLU's gradient, fp32 8192 x 14336: 403 us
-// against 260 us, decided by how the compiler spaced the two).
-__device__ __forceinline__ void load8(Raw8<BF16> &r, const uint8_t *p, bool) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+// From global memory, without a copy in L1.  A lane's 32 bytes of fp32 are one
+// instruction where they are 32-byte aligned: two of 16 bytes touch every sector
+// twice, and once its first touch has left L1 the second goes to L2 again
+// (SwiGLU's gradient, fp32 8192 x 14336: 403 us against 254 us, decided by how
+// the compiler spaced the two).  Volatile, because the compiler otherwise spaces
+// a group of loads out to save registers and fewer are in flight.  L2 keeps its
+// default policy: marking these lines to leave first costs 3 to 5% of the
+// bandwidth (SwiGLU, the same matrix: 187 us against 178 us).
+__device__ __forceinline__ void load8(Raw8<BF16> &r, const uint8_t *p, bool = true) {
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(p));
 }
-__device__ __forceinline__ void load8(Raw8<F32> &r, const uint8_t *p, bool aligned32) {
+__device__ __forceinline__ void load8(Raw8<F32> &r, const uint8_t *p, bool aligned32 = true) {
     if (aligned32)
-        asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
                        "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
                      : "l"(p));
