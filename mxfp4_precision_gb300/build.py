@@ -2,14 +2,18 @@
 
 Each CUDA translation unit compiles in parallel to an object file, then they
 are linked into one shared library (static CUDA runtime, no libcuda link: the
-driver entry point for tensor-map encoding is fetched at run time).
+driver entry point for tensor-map encoding is fetched at run time).  Beside it,
+``_build/mx_torch.so``: the Python entry points of the operators between the
+GEMMs (csrc/mx_torch.cpp, host code only, against the installed torch).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD_DIR, "libmx.so")
+TORCH_SOURCE = "mx_torch.cpp"
+TORCH_LIB = os.path.join(BUILD_DIR, "mx_torch.so")
 # Bounds-checked variant (every kernel store guarded; see MX_ERR_BOUNDS in mx.h),
 # used by the tests only.
 CHECKED_DIR = os.path.join(HERE, "_build_checked")
@@ -49,10 +55,38 @@ def _stale(lib: str | None = None) -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        raise RuntimeError("torch not found: the Python entry points need it to build")
+    return os.path.dirname(spec.origin)
+
+
+def _compile_torch(verbose: bool) -> str:
+    """Object file of the Python entry points (host code)."""
+    torch, obj = _torch_dir(), os.path.join(BUILD_DIR, "mx_torch.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c",
+           os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
+    _run(cmd, verbose)
+    return obj
+
+
+def _run(cmd: list[str], verbose: bool = False) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{' '.join(cmd[-3:])} failed:\n{res.stdout}\n{res.stderr}")
+    if verbose and (res.stdout or res.stderr):
+        print(res.stdout + res.stderr, flush=True)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
           checked: bool = False) -> str:
     out_dir, lib = (CHECKED_DIR, CHECKED_LIB) if checked else (BUILD_DIR, LIB)
-    if not force and not _stale(lib):
+    if not force and not _stale(lib) and (checked or not _stale(TORCH_LIB)):
         return lib
     os.makedirs(out_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -60,24 +94,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
     def compile_one(src: str) -> str:
         obj = os.path.join(out_dir, os.path.splitext(src)[0] + ".o")
-        cmd = [nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{res.stdout}\n{res.stderr}")
-        if verbose and (res.stdout or res.stderr):
-            print(res.stdout + res.stderr, flush=True)
+        _run([nvcc, *ARCH, *flags, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        torch_obj = None if checked else ex.submit(_compile_torch, verbose)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, lib)
+    if torch_obj is not None:
+        tmp = TORCH_LIB + f".tmp{os.getpid()}"
+        _run(["g++", "-shared", "-o", tmp, torch_obj.result(), "-L", out_dir, "-l:libmx.so", "-Wl,-rpath,$ORIGIN",
+              "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+        os.replace(tmp, TORCH_LIB)
     return lib
 
 
