@@ -29,6 +29,56 @@ __device__ __forceinline__ float sigmoid(float g) {
     return r * 0x1p-10f;  // the reciprocal itself stays normal
 }
 
+// The same within 2 u where the kernel has the time for it (fp32 in, bound by
+// memory), so that codes fall on a rounding boundary's other side no more often
+// than with expf and a division: exp(-g) = 2^n 2^f with n = round(-g log2 e)
+// from adding 1.5 * 2^23 (the sum's low bits then hold n), f by a two-part log2 e
+// and 2^f on [-1/2, 1/2] a degree-6 polynomial whose coefficients were fitted
+// here for the least relative error (0.03 u before their rounding to fp32, 0.27 u
+// after); a Newton step on the reciprocal.  For |g| <= 87: the
+// form above outside.
+__device__ __forceinline__ float sigmoid_fine(float g) {
+    const float z = fmaf(g, -0x1.715476p+0f, 12582912.0f);
+    float f = fmaf(g, -0x1.715476p+0f, 12582912.0f - z);
+    f = fmaf(g, -0x1.4ae0cp-26f, f);
+    float p = fmaf(0x1.41fbbcp-13f, f, 0x1.5f3e54p-10f);
+    p = fmaf(p, f, 0x1.3b2d4cp-7f);
+    p = fmaf(p, f, 0x1.c6aee8p-5f);
+    p = fmaf(p, f, 0x1.ebfbdcp-3f);
+    p = fmaf(p, f, 0x1.62e430p-1f);
+    p = fmaf(p, f, 1.0f);
+    // n, in -127 .. 127, moves p's exponent (p lies in [0.70, 1.42], and above 1 where n = -127).
+    const float d = 1.0f + __uint_as_float(__float_as_uint(p) + (__float_as_uint(z) << 23));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return fmaf(r, fmaf(-d, r, 1.0f), r);
+}
+
+// y = g * s * u of eight columns, by either form.
+template <bool FINE>
+__device__ __forceinline__ V8 gated(const float (&g)[8], const float (&u)[8]) {
+    V8 y;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float s0 = FINE ? sigmoid_fine(g[i]) : sigmoid(g[i]);
+        const float s1 = FINE ? sigmoid_fine(g[i + 1]) : sigmoid(g[i + 1]);
+        y.v[i / 2] = pack2(g[i] * s0 * u[i], g[i + 1] * s1 * u[i + 1]);
+    }
+    return y;
+}
+template <typename G>
+__device__ __forceinline__ V8 gated(const V8 &gate, const V8 &up) {
+    float g[8], u[8];
+    floats_of(gate, g);
+    floats_of(up, u);
+    if constexpr (G::kBytes == 4) {
+        float top = enc::absmax2_nan(enc::absmax3_nan(g[0], g[1], g[2]), enc::absmax3_nan(g[3], g[4], g[5]));
+        top = enc::absmax3_nan(top, g[6], g[7]);
+        if (top <= 87.0f) return gated<true>(g, u);
+    }
+    return gated<false>(g, u);
+}
+
 // Both kernels: a block is `deep` rows by `wide` chunks of 8 columns (a
 // multiple of 32 threads), `segments` blocks side by side make a row; each
 // thread keeps its columns and takes `turns` rows, two at a time.
@@ -61,7 +111,7 @@ __device__ __forceinline__ Place place(const GluArgs &p) {
 }
 
 template <typename G>
-__global__ void __launch_bounds__(256) mx_swiglu_kernel(const __grid_constant__ GluArgs p) {
+__global__ void __launch_bounds__(256, G::kBytes == 4 ? 4 : 6) mx_swiglu_kernel(const __grid_constant__ GluArgs p) {
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x >= p.tiles) {
@@ -95,14 +145,7 @@ __global__ void __launch_bounds__(256) mx_swiglu_kernel(const __grid_constant__ 
         for (int k = 0; k < 2; ++k) {
             const int64_t r = row + k * at.deep;
             if (r >= at.end) break;
-            float g[8], u[8];
-            floats_of(to_v8(gr[k]), g);
-            floats_of(to_v8(ur[k]), u);
-            V8 y;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y.v[i] = pack2(g[2 * i] * sigmoid(g[2 * i]) * u[2 * i],
-                               g[2 * i + 1] * sigmoid(g[2 * i + 1]) * u[2 * i + 1]);
+            const V8 y = gated<G>(to_v8(gr[k]), to_v8(ur[k]));
             if (in && p.y.p != nullptr)
                 store8<BF16>(p.y, p.y.p + (r * p.F + col) * 2, y, p.aligned32, p.status);
             if (p.enc.fmt != kEncNone && at.c < p.enc.katoms * 16)
