@@ -498,20 +498,31 @@ RowShape row_shape(int64_t n, int c) {
     return {c, tpr, tpr >= 256 ? 1 : 256 / tpr, 0, 0};
 }
 
-// One warp a row (no barrier) for rows of up to 160 chunks, once the rows
-// fill the SMs; otherwise two or three chunks a thread, whichever leaves fewer
-// threads without one, and four where a row needs more than 1024 threads.
-RowShape norm_shape(int64_t T, int64_t K, const DeviceInfo &dev) {
+// How a row is cut, by what keeps the most loads in flight:
+//   up to 32 chunks (K <= 256): one warp;
+//   up to 160, once the rows fill the SMs with warps: one warp a row, no barrier
+//     (bf16 16383 x 1056: 29.7 us, 34.4 us at two chunks a thread);
+//   two chunks a thread, or three where that leaves fewer threads without one
+//     (bf16 16383 x 2080: 52 us, 63 us at two);
+//   beyond 256 threads at two chunks: three or four, since several blocks of up
+//     to 256 threads overlap their barriers (bf16 4096 x 8192: 41 us, 52 us at
+//     two; fp32 x and bf16 stream: 57.9 us, 60.5 us), but not for rows of 8 bytes
+//     a column (fp32 both: 82 us, 76 us at two), whose threads then hold too much;
+//   above 1024 chunks: four.
+RowShape norm_shape(int64_t T, int64_t K, int bytes, const DeviceInfo &dev) {
     const int64_t n = padded_chunks(K);
-    if (n <= 32 || (n <= 160 && T >= 16ll * dev.sm_count)) return row_shape(n, static_cast<int>(n / 32));
-    const RowShape two = row_shape(n, 2), three = row_shape(n, 3);
-    if (n <= 1024 && three.tpr * 3 < two.tpr * 2) return three;
-    return row_shape(n, n <= 1024 ? 2 : 4);
+    const bool many = T >= 16ll * dev.sm_count;
+    if (n <= 32 || (n <= 160 && many)) return row_shape(n, static_cast<int>(n / 32));
+    if (n > 1024) return row_shape(n, 4);
+    const RowShape two = row_shape(n, 2), three = row_shape(n, 3), four = row_shape(n, 4);
+    if (many && bytes <= 6 && two.tpr > 256)
+        return three.tpr <= 256 && three.tpr * 3 <= four.tpr * 4 ? three : four;
+    return three.tpr * 3 < two.tpr * 2 ? three : two;
 }
 
 template <typename X, typename S, bool RES>
 cudaError_t launch_norm(NormArgs &p, const DeviceInfo &dev, cudaStream_t stream) {
-    const RowShape s = norm_shape(p.T, p.K, dev);
+    const RowShape s = norm_shape(p.T, p.K, X::kBytes + (RES ? S::kBytes : 0), dev);
     p.tpr = s.tpr;
     p.groups = s.groups;
     const int threads = s.tpr * s.groups;
