@@ -331,7 +331,8 @@ mx_status mx_linear_dgrad(const void *d_dY, const void *d_W, float *d_dX, int64_
  *                    rows; mx_scales_bytes
  * each from y in fp32 (rounded once).  Encoding needs columns % 32 == 0.  Outputs
  * may be NULL where noted; d_codes and d_scales must be NULL for MX_FORMAT_NONE.
- * Columns above MX_ROW_COLUMNS_MAX (norm) get MX_ERR_UNSUPPORTED.  T == 0 or no
+ * An output may overlap an input only where a call says so.  Columns above
+ * MX_ROW_COLUMNS_MAX (norm) get MX_ERR_UNSUPPORTED.  T == 0 or no
  * columns: MX_OK, nothing launched (the weight gradient is zero-filled).
  */
 typedef enum { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 } mx_type;

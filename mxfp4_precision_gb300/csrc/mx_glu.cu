@@ -79,6 +79,11 @@ __device__ __forceinline__ V8 gated(const V8 &gate, const V8 &up) {
     return gated<false>(g, u);
 }
 
+// One read, one write, bound by memory with fp32 input: 8192 x 14336 with bf16 y
+// and MXFP8 codes 179 us, 1.30 GB = 7.2 TB/s (106% of a plain copy's rate: it
+// writes less than it reads); the gradient 254 us, 1.88 GB = 7.4 TB/s (109%).  With
+// bf16 input and codes alone the instructions bound it, 25 an element: 96 us, 591 MB
+// = 6.2 TB/s (91%).
 // Both kernels: a block is `deep` rows by `wide` chunks of 8 columns (a
 // multiple of 32 threads), `segments` blocks side by side make a row; each
 // thread keeps its columns and takes `turns` rows, two at a time.

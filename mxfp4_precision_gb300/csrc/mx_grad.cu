@@ -7,6 +7,12 @@
 // needs no table in device memory and can be captured in a graph.  Sums run
 // in fp32 per thread and in pairs of fp32 across threads and blocks, in an order
 // that the sizes alone fix (no atomics): the same inputs give the same bits.
+//
+// Bound by memory, and by the second read: the factor is known only after the
+// whole norm.  218M fp32 gradients into bf16: 126 us for the norm (6.9 TB/s) and
+// 195 us for the scaling (6.7 TB/s), 320 us in all, where one read and one write
+// would take 192 us and two reads and one write 320 us at a plain copy's rate.  Going
+// backwards finds some 40 MB in L2.  64 small tensors: 5 us, two launches.
 #include <cstdint>
 #include <cuda_runtime.h>
 

@@ -94,9 +94,15 @@ __device__ __forceinline__ void rstd_out(const NormArgs &p, int64_t row, float r
 }
 
 // One row per tpr threads and no turn after it, C chunks of 8 columns per
-// thread, the row in registers between its sum and its output.  Blocks per SM that the registers must allow: the loads in flight are what
-// counts, and the compiler left alone takes C = 4 to one block of 512 threads
-// (bf16, 2048 x 16384: 67 us against 51 us).
+// thread, the row in registers between its sum and its output: one read, one
+// write.  Bound by memory; what it needs is loads in flight, and several short
+// blocks per SM have more of them than one long-lived block that feeds itself
+// through a ring of shared-memory slots (8192 x 4096: 62 to 66 us so).  fp32 x,
+// bf16 stream and bf16 y, MXFP8 codes, 8192 x 4096: 56.8 us, 370 MB = 6.5 TB/s (96%
+// of a plain copy's rate); 16384 x 4096 without y: 89.5 us, 6.8 TB/s (99.6%).
+// norm_blocks: blocks per SM that the registers must allow; the compiler left
+// alone takes C = 4 to one block of 512 threads (bf16, 2048 x 16384: 67 us against
+// 51 us).
 template <typename X, typename S, int C, int THREADS>
 constexpr int norm_blocks() {
     if (THREADS > 256) return THREADS > 512 ? 1 : 2;
@@ -281,7 +287,8 @@ __device__ __forceinline__ void finish(const V8 &a, const V8 &h, float rstd, flo
     for (int i = 0; i < 4; ++i) g.v[i] = fma2(r, fma2(mul2(h.v[i], r), m, a.v[i]), g.v[i]);
 }
 
-// Each group of tpr threads takes rows in turn and keeps its columns' sums of
+// Few rows, or rows too wide for the ring below (fp32 beyond 8192 columns or
+// so): each group of tpr threads takes rows in turn and keeps its columns' sums of
 // dy * h * rstd in registers; they are added up over the block's groups at the
 // end: one partial per block.  AGAIN: rows too wide for the registers are
 // loaded twice (the second time from L1 or L2), once for mean(dy * w * h), once
@@ -365,7 +372,11 @@ __global__ void __launch_bounds__(THREADS)
     sum_groups<C>(p, reinterpret_cast<float *>(smem), dw);
 }
 
-// Many rows, through the ring.  LOOK2: a row is read from its slot twice, once
+// Many rows, through the ring: from two rows a group on (bf16 stream 1024 x 4096:
+// 13.0 us, 14.2 us directly; 8192 x 4096: 54.8 us, 81 us directly).  Bound by
+// memory: with fp32 dy 336 MB = 6.1 TB/s (90% of a plain copy's rate) there, of
+// which the sum of the partial weight gradients takes 3 us and the ring's filling
+// and emptying 4 us.  LOOK2 (one warp a row, or four chunks a thread): a row is read from its slot twice, once
 // for mean(dy * w * h) and once for dx, instead of staying in registers between
 // them; the slot is then free only after the second.  The groups' weight
 // gradients are summed in shared memory at the end: one partial per block.
@@ -462,7 +473,8 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // dw[col] = sum of the n partial sums, in a fixed order: 32 columns a block,
-// the partials split over its 32 warps.
+// the partials split over its 32 warps.  Bound by its launch and two rounds of
+// loads from L2 (3 us behind the ring's 152 partials of 4096 columns).
 __global__ void __launch_bounds__(1024) mx_rmsnorm_dw_kernel(const float *parts, int64_t n, int64_t K,
                                                              Out dw, int *status) {
     __shared__ float sums[32][32];
