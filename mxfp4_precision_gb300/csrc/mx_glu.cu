@@ -82,11 +82,14 @@ __device__ __forceinline__ V8 gated(const V8 &gate, const V8 &up) {
 // One read, one write, bound by memory with fp32 input: 8192 x 14336 with bf16 y
 // and MXFP8 codes 179 us, 1.30 GB = 7.2 TB/s (106% of a plain copy's rate: it
 // writes less than it reads); the gradient 254 us, 1.88 GB = 7.4 TB/s (109%).  With
-// bf16 input and codes alone the instructions bound it, 25 an element: 96 us, 591 MB
-// = 6.2 TB/s (91%).
+// bf16 input and codes alone the instructions bound it, 25 an element: 95 us, 591 MB
+// = 6.2 TB/s (92%).
 // Both kernels: a block is `deep` rows by `wide` chunks of 8 columns (a
 // multiple of 32 threads), `segments` blocks side by side make a row; each
 // thread keeps its columns and takes `turns` rows, two at a time.
+// Small blocks: a finished one makes room for the next sooner (128 threads against
+// 256: bf16 8192 x 4096 to codes alone 90% of a plain copy's rate, 81%).
+constexpr int kBlock = 128;
 struct GluArgs {
     const uint8_t *gu, *dy;
     int64_t gu_pitch, dy_pitch;  // bytes
@@ -116,7 +119,7 @@ __device__ __forceinline__ Place place(const GluArgs &p) {
 }
 
 template <typename G>
-__global__ void __launch_bounds__(256, G::kBytes == 4 ? 4 : 6) mx_swiglu_kernel(const __grid_constant__ GluArgs p) {
+__global__ void __launch_bounds__(kBlock, G::kBytes == 4 ? 8 : 11) mx_swiglu_kernel(const __grid_constant__ GluArgs p) {
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x >= p.tiles) {
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(256, G::kBytes == 4 ? 4 : 6) mx_swiglu_kernel(
 }
 
 template <typename D, typename G>
-__global__ void __launch_bounds__(256) mx_swiglu_backward_kernel(const __grid_constant__ GluArgs p) {
+__global__ void __launch_bounds__(kBlock) mx_swiglu_backward_kernel(const __grid_constant__ GluArgs p) {
     griddep_wait();
     griddep_launch_dependents();
     const Place at = place(p);
@@ -197,18 +200,19 @@ __global__ void __launch_bounds__(256) mx_swiglu_backward_kernel(const __grid_co
     }
 }
 
-// Tiles of rows whose `chunks` are cut into equal segments of at most 256; several
-// rows a thread once there are blocks enough for every SM to hold `kWaves` full turns.
-constexpr int64_t kWaves = 4;
+// Tiles of rows whose `chunks` are cut into equal segments of at most a block;
+// several rows a thread once there are blocks enough for every SM to be filled
+// kWaves times.
+constexpr int64_t kWaves = 2;
 bool shape(GluArgs &p, int64_t chunks, int64_t pad_words, int most, const DeviceInfo &dev,
            int64_t *grid, int *threads) {
-    p.segments = static_cast<int>((chunks + 255) / 256);
+    p.segments = static_cast<int>((chunks + kBlock - 1) / kBlock);
     p.wide = static_cast<int>(((chunks + p.segments - 1) / p.segments + 31) / 32 * 32);
-    const int deep = 256 / p.wide;
+    const int deep = kBlock / p.wide;
     *threads = p.wide * deep;
     p.turns = most;
     auto tiles = [&] { return (p.T + deep * p.turns - 1) / (deep * p.turns) * p.segments; };
-    while (p.turns > 1 && tiles() < kWaves * 8 * dev.sm_count) p.turns /= 2;
+    while (p.turns > 1 && tiles() < kWaves * (2048 / kBlock) * dev.sm_count) p.turns /= 2;
     *grid = tiles() + (pad_words + *threads - 1) / *threads;
     p.tiles = static_cast<uint32_t>(tiles());
     return *grid <= 0x7FFFFFFF;

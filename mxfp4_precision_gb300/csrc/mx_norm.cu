@@ -287,14 +287,14 @@ __device__ __forceinline__ void finish(const V8 &a, const V8 &h, float rstd, flo
     for (int i = 0; i < 4; ++i) g.v[i] = fma2(r, fma2(mul2(h.v[i], r), m, a.v[i]), g.v[i]);
 }
 
-// Few rows, or rows too wide for the ring below (fp32 beyond 8192 columns or
-// so): each group of tpr threads takes rows in turn and keeps its columns' sums of
+// Few rows, or rows too wide for two in the ring below (fp32 beyond 9000 columns or
+// so: 10240 to 16384 columns 61 to 74% of a plain copy's rate, beyond that 45 to 67%): each group of tpr threads takes rows in turn and keeps its columns' sums of
 // dy * h * rstd in registers; they are added up over the block's groups at the
 // end: one partial per block.  AGAIN: rows too wide for the registers are
 // loaded twice (the second time from L1 or L2), once for mean(dy * w * h), once
 // for dx.
 template <typename D, typename S, int C, int THREADS, bool AGAIN>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1)
     mx_rmsnorm_backward_kernel(const __grid_constant__ NormGradArgs p) {
     __shared__ float part[2][32];
     extern __shared__ __align__(128) uint8_t smem[];  // [groups][K] fp32 where groups > 1
@@ -372,10 +372,9 @@ __global__ void __launch_bounds__(THREADS)
     sum_groups<C>(p, reinterpret_cast<float *>(smem), dw);
 }
 
-// Many rows, through the ring: from two rows a group on (bf16 stream 1024 x 4096:
-// 13.0 us, 14.2 us directly; 8192 x 4096: 54.8 us, 81 us directly).  Bound by
-// memory: with fp32 dy 336 MB = 6.1 TB/s (90% of a plain copy's rate) there, of
-// which the sum of the partial weight gradients takes 3 us and the ring's filling
+// Many rows, through the ring (bf16 stream 8192 x 4096: 53.5 us, 81 us directly).
+// Bound by memory: with fp32 dy 336 MB = 6.3 TB/s (92% of a plain copy's rate)
+// there; the sum of the partial weight gradients takes 2 us and the ring's filling
 // and emptying 4 us.  LOOK2 (one warp a row, or four chunks a thread): a row is read from its slot twice, once
 // for mean(dy * w * h) and once for dx, instead of staying in registers between
 // them; the slot is then free only after the second.  The groups' weight
@@ -472,28 +471,43 @@ __global__ void __launch_bounds__(THREADS)
     sum_groups<C>(p, reinterpret_cast<float *>(smem), dw);
 }
 
-// dw[col] = sum of the n partial sums, in a fixed order: 32 columns a block,
-// the partials split over its 32 warps.  Bound by its launch and two rounds of
-// loads from L2 (3 us behind the ring's 152 partials of 4096 columns).
-__global__ void __launch_bounds__(1024) mx_rmsnorm_dw_kernel(const float *parts, int64_t n, int64_t K,
-                                                             Out dw, int *status) {
+// dw[col] = sum of the n partial sums, in a fixed order: 32 columns a block, four
+// a lane, the partials split over the block's other threads, four of them in
+// flight (the last again, unused, beyond the end): one round of loads from L2
+// up to 512 partials, which with the launch is what bounds it.
+__global__ void __launch_bounds__(1024) mx_rmsnorm_dw_kernel(const float *parts, int n, uint32_t K, Out dw,
+                                                             int *status) {
     __shared__ float sums[32][32];
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
-    float s = 0.0f;
+    const uint32_t col = blockIdx.x * 32 + 4 * (threadIdx.x & 7);
+    float s[4] = {0, 0, 0, 0};
     if (col < K) {
-#pragma unroll 8
-        for (int64_t i = threadIdx.x >> 5; i < n; i += 32) s += parts[i * K + col];
-    }
-    sums[threadIdx.x >> 5][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (threadIdx.x < 32 && col < K) {
-        s = 0.0f;
+        for (int i = threadIdx.x >> 3; i < n; i += 4 * 128) {
+            float4 v[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x];
-        float *d = reinterpret_cast<float *>(dw.p) + col;
-        if (MX_STORE_OK(d, 4, dw.p, dw.bytes, status)) *d = s;
+            for (int k = 0; k < 4; ++k)
+                v[k] = *reinterpret_cast<const float4 *>(parts + static_cast<int64_t>(min(i + 128 * k, n - 1)) * K + col);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + 128 * k < n) s[0] += v[k].x, s[1] += v[k].y, s[2] += v[k].z, s[3] += v[k].w;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], 8);
+        s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], 16);
+    }
+    if ((threadIdx.x & 31) < 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sums[threadIdx.x >> 5][4 * (threadIdx.x & 7) + k] = s[k];
+    __syncthreads();
+    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < K) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t += sums[i][threadIdx.x];
+        float *d = reinterpret_cast<float *>(dw.p) + blockIdx.x * 32 + threadIdx.x;
+        if (MX_STORE_OK(d, 4, dw.p, dw.bytes, status)) *d = t;
     }
 }
 
@@ -559,7 +573,6 @@ cudaError_t launch_norm(NormArgs &p, const DeviceInfo &dev, cudaStream_t stream)
 
 constexpr int kGradBlocks = 304;  // of the direct gradient kernel, at most
 constexpr int kRingThreads = 512;
-constexpr int kRingTurns = 2;  // rows a group must have for the ring to pay
 constexpr size_t kRingSmem = 220 * 1024;
 
 RowShape grad_shape(int64_t T, int64_t K) {
@@ -574,16 +587,26 @@ int64_t grad_grid(int64_t T, const RowShape &s) {
     return want < kGradBlocks ? want : kGradBlocks;
 }
 
-// The ring's shape for rows of `bytes`, or stages = 0 where it does not apply:
-// one warp a row up to 160 chunks, then two chunks a thread, four above 1024.
+// The ring's shape for rows of `bytes`, or stages = 0 where it does not apply: one
+// warp a row up to 160 chunks; then two chunks a thread, or three or four where
+// that gives an SM two rows at a time (bf16 8192 columns: 85% of a plain copy's
+// rate, 76% with one row at a time; fp32 dy 5120 columns: 90%, 75%).
 RowShape ring_shape(int64_t T, int64_t K, size_t bytes, const DeviceInfo &dev) {
     const int64_t n = padded_chunks(K);
-    RowShape s = row_shape(n, n <= 160 ? static_cast<int>(n / 32) : n <= 1024 ? 2 : 4);
-    s.groups = kRingThreads / s.tpr;
-    if (s.groups < 1 || T < static_cast<int64_t>(kRingTurns) * s.groups * dev.sm_count) return s;
-    s.stages = static_cast<int>((kRingSmem - 256 * s.groups) / (s.groups * (bytes + 8)));
-    if (s.stages > 8) s.stages = 8;
-    if (s.stages < 2) s.stages = 0;
+    const int slots = static_cast<int>((kRingSmem - 4096) / (bytes + 8));
+    RowShape s{};
+    for (int c = n <= 160 ? static_cast<int>(n / 32) : n <= 1024 ? 2 : 4; c <= 5; ++c) {
+        RowShape t = row_shape(n, c);
+        t.groups = kRingThreads / t.tpr < slots / 2 ? kRingThreads / t.tpr : slots / 2;
+        if (t.groups < 1) continue;
+        if (s.groups == 0) s = t;
+        if (t.groups >= 2) s = t;
+        if (n <= 160 || s.groups >= 2 || c == 4) break;
+    }
+    // It pays from one row a group on (1024 rows of 2048 columns, bf16 stream: 7.4 us,
+    // 7.9 us directly), two for one-warp rows (4096 of 512: 6.9 us directly, 7.4 us).
+    if (s.groups < 1 || T < (s.tpr == 32 ? 2ll : 1ll) * s.groups * dev.sm_count) return s;
+    s.stages = slots / s.groups < 8 ? slots / s.groups : 8;
     s.smem = s.groups * (s.stages * (bytes + 8) + 256);
     return s;
 }
@@ -700,7 +723,7 @@ cudaError_t launch_rmsnorm_backward(const RowIn &dy, const RowIn &h, const void 
                                           : launch_norm_grad<BF16, BF16>(p, &n, dev, stream));
     if (e != cudaSuccess || dw == nullptr) return e;
     return launch_dependent(mx_rmsnorm_dw_kernel, (K + 31) / 32, 1024, 0, stream,
-                            static_cast<const float *>(ws), n, K,
+                            static_cast<const float *>(ws), static_cast<int>(n), static_cast<uint32_t>(K),
                             Out{reinterpret_cast<uint8_t *>(dw), static_cast<size_t>(K) * 4},
                             dev.status);
 }
