@@ -512,37 +512,42 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_dw_kernel(const float *parts,
 }
 
 // ---------------------------------------------------------------- shapes
-// Threads of a row and its chunks of 8 columns per thread; `n` chunks is the
-// padded width of the scale layout (a multiple of 32).
+// Threads of a row and its chunks of 8 columns per thread, and the rows of a block
+// of `block` threads or one row; `n` chunks is the padded width of the scale
+// layout (a multiple of 32).
 struct RowShape {
     int c, tpr, groups, stages;
     size_t smem;
 };
 int64_t padded_chunks(int64_t K) { return (K + 255) / 256 * 32; }
-RowShape row_shape(int64_t n, int c) {
+RowShape row_shape(int64_t n, int c, int block) {
     const int tpr = static_cast<int>((n + 32 * c - 1) / (32 * c)) * 32;
-    return {c, tpr, tpr >= 256 ? 1 : 256 / tpr, 0, 0};
+    return {c, tpr, tpr >= block ? 1 : block / tpr, 0, 0};
 }
 
-// How a row is cut, by what keeps the most loads in flight:
-//   up to 32 chunks (K <= 256): one warp;
+// How a row is cut, by what keeps the most loads in flight (rates of a plain
+// copy's, at 2^25 elements unless said):
+//   blocks of 128 threads where a row needs no more, since a finished one makes room
+//     sooner (bf16 2048 columns, codes alone: 86%, 78% in blocks of 256);
+//   up to 32 chunks (K <= 256): one warp a row;
 //   up to 160, once the rows fill the SMs with warps: one warp a row, no barrier
 //     (bf16 16383 x 1056: 29.7 us, 34.4 us at two chunks a thread);
 //   two chunks a thread, or three where that leaves fewer threads without one
 //     (bf16 16383 x 2080: 52 us, 63 us at two);
-//   beyond 256 threads at two chunks: three or four, since several blocks of up
-//     to 256 threads overlap their barriers (bf16 4096 x 8192: 41 us, 52 us at
-//     two; fp32 x and bf16 stream: 57.9 us, 60.5 us), but not for rows of 8 bytes
-//     a column (fp32 both: 82 us, 76 us at two), whose threads then hold too much;
+//   three or four beyond 128 threads at two, for rows of up to 4 bytes a column, whose
+//     threads hold little (bf16 4096 columns, codes alone: 90%, 82% at two), and
+//     beyond 256 for rows of 6 (fp32 x and bf16 stream, 4096 x 8192: 57.9 us, 60.5 us;
+//     at 4096 columns 96%, 97% at two), but not for rows of 8 (fp32 both, 4096 x 8192:
+//     82 us, 76 us at two);
 //   above 1024 chunks: four.
 RowShape norm_shape(int64_t T, int64_t K, int bytes, const DeviceInfo &dev) {
     const int64_t n = padded_chunks(K);
     const bool many = T >= 16ll * dev.sm_count;
-    if (n <= 32 || (n <= 160 && many)) return row_shape(n, static_cast<int>(n / 32));
-    if (n > 1024) return row_shape(n, 4);
-    const RowShape two = row_shape(n, 2), three = row_shape(n, 3), four = row_shape(n, 4);
-    if (many && bytes <= 6 && two.tpr > 256)
-        return three.tpr <= 256 && three.tpr * 3 <= four.tpr * 4 ? three : four;
+    if (n <= 32 || (n <= 160 && many)) return row_shape(n, static_cast<int>(n / 32), 128);
+    if (n > 1024) return row_shape(n, 4, 128);
+    const RowShape two = row_shape(n, 2, 128), three = row_shape(n, 3, 128), four = row_shape(n, 4, 128);
+    const int most = bytes <= 4 ? 128 : bytes <= 6 ? 256 : 1024;
+    if (many && two.tpr > most) return three.tpr <= most && three.tpr * 3 <= four.tpr * 4 ? three : four;
     return three.tpr * 3 < two.tpr * 2 ? three : two;
 }
 
@@ -577,7 +582,7 @@ constexpr size_t kRingSmem = 220 * 1024;
 
 RowShape grad_shape(int64_t T, int64_t K) {
     const int64_t n = padded_chunks(K);
-    RowShape s = n <= 160 ? row_shape(n, static_cast<int>(n / 32)) : row_shape(n, n <= 512 ? 2 : 4);
+    RowShape s = n <= 160 ? row_shape(n, static_cast<int>(n / 32), 256) : row_shape(n, n <= 512 ? 2 : 4, 256);
     if (T < s.groups) s.groups = static_cast<int>(T);
     s.smem = s.groups > 1 ? s.groups * static_cast<size_t>(K) * 4 : 0;
     return s;
@@ -596,7 +601,7 @@ RowShape ring_shape(int64_t T, int64_t K, size_t bytes, const DeviceInfo &dev) {
     const int slots = static_cast<int>((kRingSmem - 4096) / (bytes + 8));
     RowShape s{};
     for (int c = n <= 160 ? static_cast<int>(n / 32) : n <= 1024 ? 2 : 4; c <= 5; ++c) {
-        RowShape t = row_shape(n, c);
+        RowShape t = row_shape(n, c, 256);
         t.groups = kRingThreads / t.tpr < slots / 2 ? kRingThreads / t.tpr : slots / 2;
         if (t.groups < 1) continue;
         if (s.groups == 0) s = t;
