@@ -15,80 +15,90 @@ namespace {
 
 using namespace rows;
 
-// 1 / (1 + exp(-g)) from the hardware's 2^x and reciprocal.  Their errors (2 and
-// 1 units in the last place) and the rounded product g log2 e leave the
-// sigmoid within (5 + |g|) u, u = 2^-24: far inside both outputs' roundings,
-// and the limits come out by themselves (0 for an exponential that overflows, 1
-// for one that vanishes, NaN for NaN).  expf and a division instead take 54
-// instructions an element, which bounds the kernel (bf16 in, 8192 x 14336: 171
-// us against 87 us for the memory).
+// Three forms of s = 1 / (1 + exp(-g)), u = 2^-24.
+//
+// kFast, |g| <= 80: the hardware's 2^x and reciprocal.  Their errors (2 and 1
+// units in the last place) and the rounded product g log2 e leave it within
+// (5 + |g|) u: far inside the outputs' roundings.  expf and a division instead
+// take 54 instructions an element, which bounds the kernel (bf16 in, 8192 x 14336:
+// 171 us against 87 us for the memory).
+//
+// kFine, |g| <= 80: within 2 u, where the kernel has the time for it (fp32 in, bound
+// by memory), so that codes fall on a rounding boundary's other side no more often
+// than with expf and a division: exp(-g) = 2^n 2^f with n = round(-g log2 e) from
+// adding 1.5 * 2^23 (the sum's low bits then hold n), f by a two-part log2 e and
+// 2^f on [-1/2, 1/2] a degree-6 polynomial whose coefficients were fitted here for
+// the least relative error (0.03 u before their rounding to fp32, 0.27 u after); a
+// Newton step on the reciprocal.
+//
+// kFar, any g: beyond 80, where the exponential of the forms above leaves fp32's
+// range, s is exp(g) down to the smallest subnormal below and 1 above; NaN for NaN.
+enum : int { kFast, kFine, kFar };
+template <int FORM>
 __device__ __forceinline__ float sigmoid(float g) {
     float e, r;
+    if constexpr (FORM == kFine) {
+        const float z = fmaf(g, -0x1.715476p+0f, 12582912.0f);
+        float f = fmaf(g, -0x1.715476p+0f, 12582912.0f - z);
+        f = fmaf(g, -0x1.4ae0cp-26f, f);
+        float p = fmaf(0x1.41fbbcp-13f, f, 0x1.5f3e54p-10f);
+        p = fmaf(p, f, 0x1.3b2d4cp-7f);
+        p = fmaf(p, f, 0x1.c6aee8p-5f);
+        p = fmaf(p, f, 0x1.ebfbdcp-3f);
+        p = fmaf(p, f, 0x1.62e430p-1f);
+        p = fmaf(p, f, 1.0f);
+        // n, in -116 .. 116, moves p's exponent (p lies in [0.70, 1.42]).
+        const float d = 1.0f + __uint_as_float(__float_as_uint(p) + (__float_as_uint(z) << 23));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+        return fmaf(r, fmaf(-d, r, 1.0f), r);
+    }
+    if (FORM == kFar && g < -80.0f) {
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * 0x1.715476p+0f));
+        return e;
+    }
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -0x1.715476p+0f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0x1p-10f, 0x1p-10f)));
-    return r * 0x1p-10f;  // the reciprocal itself stays normal
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
 }
 
-// The same within 2 u where the kernel has the time for it (fp32 in, bound by
-// memory), so that codes fall on a rounding boundary's other side no more often
-// than with expf and a division: exp(-g) = 2^n 2^f with n = round(-g log2 e)
-// from adding 1.5 * 2^23 (the sum's low bits then hold n), f by a two-part log2 e
-// and 2^f on [-1/2, 1/2] a degree-6 polynomial whose coefficients were fitted
-// here for the least relative error (0.03 u before their rounding to fp32, 0.27 u
-// after); a Newton step on the reciprocal.  For |g| <= 87: the
-// form above outside.
-__device__ __forceinline__ float sigmoid_fine(float g) {
-    const float z = fmaf(g, -0x1.715476p+0f, 12582912.0f);
-    float f = fmaf(g, -0x1.715476p+0f, 12582912.0f - z);
-    f = fmaf(g, -0x1.4ae0cp-26f, f);
-    float p = fmaf(0x1.41fbbcp-13f, f, 0x1.5f3e54p-10f);
-    p = fmaf(p, f, 0x1.3b2d4cp-7f);
-    p = fmaf(p, f, 0x1.c6aee8p-5f);
-    p = fmaf(p, f, 0x1.ebfbdcp-3f);
-    p = fmaf(p, f, 0x1.62e430p-1f);
-    p = fmaf(p, f, 1.0f);
-    // n, in -127 .. 127, moves p's exponent (p lies in [0.70, 1.42], and above 1 where n = -127).
-    const float d = 1.0f + __uint_as_float(__float_as_uint(p) + (__float_as_uint(z) << 23));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-    return fmaf(r, fmaf(-d, r, 1.0f), r);
+// Whether one of eight values lies beyond 80 or is NaN.
+__device__ __forceinline__ bool any_far(const float (&g)[8]) {
+    float top = enc::absmax2_nan(enc::absmax3_nan(g[0], g[1], g[2]), enc::absmax3_nan(g[3], g[4], g[5]));
+    top = enc::absmax3_nan(top, g[6], g[7]);
+    return !(top <= 80.0f);
 }
 
-// y = g * s * u of eight columns, by either form.
-template <bool FINE>
+// y = g * s * u of eight columns.
+template <int FORM>
 __device__ __forceinline__ V8 gated(const float (&g)[8], const float (&u)[8]) {
     V8 y;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float s0 = FINE ? sigmoid_fine(g[i]) : sigmoid(g[i]);
-        const float s1 = FINE ? sigmoid_fine(g[i + 1]) : sigmoid(g[i + 1]);
-        y.v[i / 2] = pack2(g[i] * s0 * u[i], g[i + 1] * s1 * u[i + 1]);
-    }
+    for (int i = 0; i < 8; i += 2)
+        y.v[i / 2] = pack2(g[i] * sigmoid<FORM>(g[i]) * u[i], g[i + 1] * sigmoid<FORM>(g[i + 1]) * u[i + 1]);
     return y;
 }
-template <typename G>
-__device__ __forceinline__ V8 gated(const V8 &gate, const V8 &up) {
-    float g[8], u[8];
-    floats_of(gate, g);
-    floats_of(up, u);
-    if constexpr (G::kBytes == 4) {
-        float top = enc::absmax2_nan(enc::absmax3_nan(g[0], g[1], g[2]), enc::absmax3_nan(g[3], g[4], g[5]));
-        top = enc::absmax3_nan(top, g[6], g[7]);
-        if (top <= 87.0f) return gated<true>(g, u);
+
+// dg into u, du into d (which hold u and dy).
+template <int FORM>
+__device__ __forceinline__ void ungated(const float (&g)[8], float (&u)[8], float (&d)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float s = sigmoid<FORM>(g[i]), ds = d[i] * s;
+        u[i] = ds * u[i] * fmaf(g[i], 1.0f - s, 1.0f);
+        d[i] = ds * g[i];
     }
-    return gated<false>(g, u);
 }
 
 // One read, one write, bound by memory with fp32 input: 8192 x 14336 with bf16 y
-// and MXFP8 codes 179 us, 1.30 GB = 7.2 TB/s (106% of a plain copy's rate: it
+// and MXFP8 codes 178 us, 1.30 GB = 7.3 TB/s (107% of a plain copy's rate: it
 // writes less than it reads); the gradient 254 us, 1.88 GB = 7.4 TB/s (109%).  With
-// bf16 input and codes alone the instructions bound it, 25 an element: 95 us, 591 MB
-// = 6.2 TB/s (92%).
+// bf16 input and codes alone the instructions bound it: 98.8 us, 591 MB = 6.0 TB/s
+// (88%).
 // Both kernels: a block is `deep` rows by `wide` chunks of 8 columns (a
 // multiple of 32 threads), `segments` blocks side by side make a row; each
 // thread keeps its columns and takes `turns` rows, two at a time.
 // Small blocks: a finished one makes room for the next sooner (128 threads against
-// 256: bf16 8192 x 4096 to codes alone 90% of a plain copy's rate, 81%).
+// 256: bf16 8192 x 4096 to codes alone 87% of a plain copy's rate, 81%).
 constexpr int kBlock = 128;
 struct GluArgs {
     const uint8_t *gu, *dy;
@@ -119,7 +129,7 @@ __device__ __forceinline__ Place place(const GluArgs &p) {
 }
 
 template <typename G>
-__global__ void __launch_bounds__(kBlock, G::kBytes == 4 ? 8 : 11) mx_swiglu_kernel(const __grid_constant__ GluArgs p) {
+__global__ void __launch_bounds__(kBlock, G::kBytes == 4 ? 8 : 10) mx_swiglu_kernel(const __grid_constant__ GluArgs p) {
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x >= p.tiles) {
@@ -153,7 +163,10 @@ __global__ void __launch_bounds__(kBlock, G::kBytes == 4 ? 8 : 11) mx_swiglu_ker
         for (int k = 0; k < 2; ++k) {
             const int64_t r = row + k * at.deep;
             if (r >= at.end) break;
-            const V8 y = gated<G>(to_v8(gr[k]), to_v8(ur[k]));
+            float g[8], u[8];
+            floats_of(to_v8(gr[k]), g);
+            floats_of(to_v8(ur[k]), u);
+            const V8 y = any_far(g) ? gated<kFar>(g, u) : gated<G::kBytes == 4 ? kFine : kFast>(g, u);
             if (in && p.y.p != nullptr)
                 store8<BF16>(p.y, p.y.p + (r * p.F + col) * 2, y, p.aligned32, p.status);
             if (p.enc.fmt != kEncNone && at.c < p.enc.katoms * 16)
@@ -182,12 +195,8 @@ __global__ void __launch_bounds__(kBlock) mx_swiglu_backward_kernel(const __grid
         floats_of(to_v8(gr), g);
         floats_of(to_v8(ur), u);
         floats_of(to_v8(dr), d);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float s = sigmoid(g[i]), ds = d[i] * s;
-            u[i] = ds * u[i] * fmaf(g[i], 1.0f - s, 1.0f);
-            d[i] = ds * g[i];
-        }
+        if (any_far(g)) ungated<kFar>(g, u, d);
+        else ungated<kFast>(g, u, d);
         V8 dg, du;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -37,7 +37,7 @@ struct NormArgs {
 // Sum over the tpr threads of a row (the whole block takes part: rows of one
 // block reduce in step).  `part` holds one float per warp.
 __device__ __forceinline__ float sum_row(float v, int g, int tpr, float *part) {
-    v = sum_lanes(v, 32);
+    v = sum_lanes(v);
     if (tpr == 32) return v;
     const int n = tpr >> 5;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
@@ -177,7 +177,7 @@ struct Ring {
     }
     // Sum over the group, and whether every thread's wait ended well.
     __device__ __forceinline__ bool sum(float &v, bool ok, int turn) {
-        v = sum_lanes(v, 32);
+        v = sum_lanes(v);
         if (tpr == 32) return __all_sync(0xFFFFFFFFu, ok);
         float *at = part + (turn & 1) * 32;
         const int tr = threadIdx.x % tpr;
@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 1)
     sum_groups<C>(p, reinterpret_cast<float *>(smem), dw);
 }
 
-// Many rows, through the ring (bf16 stream 8192 x 4096: 53.5 us, 81 us directly).
-// Bound by memory: with fp32 dy 336 MB = 6.3 TB/s (92% of a plain copy's rate)
+// Many rows, through the ring (bf16 stream 8192 x 4096: 54 us, 81 us directly).
+// Bound by memory: with fp32 dy 336 MB = 6.2 TB/s (91% of a plain copy's rate)
 // there; the sum of the partial weight gradients takes 2 us and the ring's filling
 // and emptying 4 us.  LOOK2 (one warp a row, or four chunks a thread): a row is read from its slot twice, once
 // for mean(dy * w * h) and once for dx, instead of staying in registers between
@@ -577,6 +577,7 @@ cudaError_t launch_norm(NormArgs &p, const DeviceInfo &dev, cudaStream_t stream)
 }
 
 constexpr int kGradBlocks = 304;  // of the direct gradient kernel, at most
+constexpr int kRingBlocks = 160;  // one per SM; devices with more SMs take the direct kernel
 constexpr int kRingThreads = 512;
 constexpr size_t kRingSmem = 220 * 1024;
 
@@ -600,6 +601,7 @@ RowShape ring_shape(int64_t T, int64_t K, size_t bytes, const DeviceInfo &dev) {
     const int64_t n = padded_chunks(K);
     const int slots = static_cast<int>((kRingSmem - 4096) / (bytes + 8));
     RowShape s{};
+    if (dev.sm_count > kRingBlocks) return s;
     for (int c = n <= 160 ? static_cast<int>(n / 32) : n <= 1024 ? 2 : 4; c <= 5; ++c) {
         RowShape t = row_shape(n, c, 256);
         t.groups = kRingThreads / t.tpr < slots / 2 ? kRingThreads / t.tpr : slots / 2;
@@ -616,13 +618,6 @@ RowShape ring_shape(int64_t T, int64_t K, size_t bytes, const DeviceInfo &dev) {
     return s;
 }
 
-template <typename Kern>
-cudaError_t with_smem(Kern kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(bytes));
-}
-
 template <typename D, typename S>
 cudaError_t launch_norm_grad(NormGradArgs &p, int64_t *n_parts, const DeviceInfo &dev,
                              cudaStream_t stream) {
@@ -636,18 +631,21 @@ cudaError_t launch_norm_grad(NormGradArgs &p, int64_t *n_parts, const DeviceInfo
     *n_parts = grid;
     p.parts.bytes = static_cast<size_t>(grid) * p.K * 4;
     const int threads = s.tpr * s.groups;
-    auto go = [&](auto kernel) {
-        const cudaError_t e = with_smem(kernel, s.smem);
-        return e != cudaSuccess ? e : launch_dependent(kernel, grid, threads, s.smem, stream, p);
-    };
+    auto go = [&](auto kernel) { return launch_dependent(kernel, grid, threads, s.smem, stream, p); };
     if (ring) {
-        if (s.tpr > 32 && s.c == 2) return go(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads, false>);
+        // The limit is the kernel's, not the call's: always the same one.
+        auto large = [&](auto kernel) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(kRingSmem));
+            return e != cudaSuccess ? e : go(kernel);
+        };
+        if (s.tpr > 32 && s.c == 2) return large(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads, false>);
         switch (s.c) {
-            case 1: return go(mx_rmsnorm_backward_ring_kernel<D, S, 1, kRingThreads, true>);
-            case 2: return go(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads, true>);
-            case 3: return go(mx_rmsnorm_backward_ring_kernel<D, S, 3, kRingThreads, true>);
-            case 4: return go(mx_rmsnorm_backward_ring_kernel<D, S, 4, kRingThreads, true>);
-            default: return go(mx_rmsnorm_backward_ring_kernel<D, S, 5, kRingThreads, true>);
+            case 1: return large(mx_rmsnorm_backward_ring_kernel<D, S, 1, kRingThreads, true>);
+            case 2: return large(mx_rmsnorm_backward_ring_kernel<D, S, 2, kRingThreads, true>);
+            case 3: return large(mx_rmsnorm_backward_ring_kernel<D, S, 3, kRingThreads, true>);
+            case 4: return large(mx_rmsnorm_backward_ring_kernel<D, S, 4, kRingThreads, true>);
+            default: return large(mx_rmsnorm_backward_ring_kernel<D, S, 5, kRingThreads, true>);
         }
     }
     switch (s.c) {
@@ -695,8 +693,9 @@ cudaError_t launch_rmsnorm(const RowIn &x, const RowIn &res, const void *w, int 
 }
 
 size_t rmsnorm_backward_ws(int64_t T, int64_t K) {
-    // The direct kernel's partials; the ring's (one per SM) are fewer.
-    return static_cast<size_t>(grad_grid(T, grad_shape(T, K))) * static_cast<size_t>(K) * 4;
+    // One partial for each block of either kernel.
+    const int64_t direct = grad_grid(T, grad_shape(T, K)), ring = T < kRingBlocks ? T : kRingBlocks;
+    return static_cast<size_t>(direct > ring ? direct : ring) * static_cast<size_t>(K) * 4;
 }
 
 cudaError_t launch_rmsnorm_backward(const RowIn &dy, const RowIn &h, const void *w, int w_f32,

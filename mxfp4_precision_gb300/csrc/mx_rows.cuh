@@ -258,9 +258,10 @@ __device__ __forceinline__ void zero_padding(const Encoded &e, int64_t T, int64_
 }
 
 // ---------------------------------------------------------------- sums
-// Sum over the `width` lanes (a power of two) that share a row.
-__device__ __forceinline__ float sum_lanes(float v, int width) {
-    for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+// Sum over the warp.
+__device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 

@@ -72,6 +72,13 @@ def test_norm_with_residual(T, K, xt, st, wt, fmt, pad):
     assert_encoded(o.codes, o.scales, y32 * rstd[:, None] * f64(w), f, fmt == "mx8", f"{T}x{K}")
 
 
+@pytest.mark.parametrize("T,K", [(2433, 768), (2440, 1024), (2432, 1280), (2435, 2080), (2432, 4128), (2432, 8192)])
+@pytest.mark.parametrize("xt,st,fmt", [(F32, BF16, "mx8"), (BF16, BF16, "mx4"), (F32, F32, "mx8")])
+def test_norm_many_rows(T, K, xt, st, fmt):
+    """Rows enough to fill the SMs: the ways of cutting a row that only then are taken."""
+    test_norm_with_residual(T, K, xt, st, BF16, fmt, 0)
+
+
 @pytest.mark.parametrize("T,K", [(1, 8), (4, 40), (3, 1000), (129, 72), (2, 24), (5, 32760)])
 @pytest.mark.parametrize("xt", [F32, BF16])
 def test_norm_without_residual_any_multiple_of_8(T, K, xt):
@@ -175,6 +182,32 @@ def test_norm_backward(T, K, dt, st, wt, pad, res):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
+# Rows enough for the ring, at every way of cutting a row there.
+RING_SIZES = [(4900, 256), (4901, 512), (4900, 760), (4864, 1024), (4865, 1280), (800, 2048), (700, 4096), (620, 5120),
+              (320, 6144), (311, 8192), (170, 16384)]
+
+
+@pytest.mark.parametrize("T,K", RING_SIZES)
+@pytest.mark.parametrize("dt,st,pad,res", [(F32, BF16, 0, True), (BF16, BF16, 8, False), (F32, F32, 0, True)])
+def test_norm_backward_many_rows(T, K, dt, st, pad, res):
+    test_norm_backward(T, K, dt, st, BF16, pad, res)
+
+
+def test_norm_backward_in_place_many_rows():
+    T, K = 700, 4096
+    dy, h, w = _matrix(T, K, BF16, 35), _matrix(T, K, BF16, 36), _weight(K, F32, 37)
+    dres = _matrix(T, K, BF16, 38, 32)
+    rstd = mx.rmsnorm(h, w).rstd
+    a, dw = mx.rmsnorm_backward(dy, h, w, rstd, dres=dres)
+    b, dw2 = mx.rmsnorm_backward(dy, h, w, rstd, dres=dres, out_dx=dres)
+    mx.check_status()
+    assert torch.equal(a, b) and torch.equal(dw, dw2)
+    a, _ = mx.rmsnorm_backward(dy, h, w, rstd)
+    b, none = mx.rmsnorm_backward(dy, h, w, rstd, want_dw=False, out_dx=dy)
+    mx.check_status()
+    assert none is None and torch.equal(a, b)
+
+
 def test_norm_backward_in_place_and_without_dw():
     dy, h, w = _matrix(70, 1056, F32, 25), _matrix(70, 1056, BF16, 26), _weight(1056, BF16, 27)
     dres = _matrix(70, 1056, BF16, 28, 32)
@@ -225,6 +258,13 @@ def test_swiglu(T, F, gt, fmt, pad):
     y = swiglu64(f64(gu))
     assert_near(o.y, y, np.abs(y) * (UB + DELTA) + TINY, "y")
     assert_encoded(o.codes, o.scales, y, f, fmt == "mx8", f"{T}x{F}")
+
+
+@pytest.mark.parametrize("T,F", [(20003, 288), (10001, 1056)])
+def test_swiglu_many_rows(T, F):
+    """Rows enough for several to a thread."""
+    test_swiglu(T, F, F32, "mx8", 0)
+    test_swiglu(T, F, BF16, "mx4", 8)
 
 
 @pytest.mark.parametrize("T,F", [(1, 8), (5, 24), (3, 1000)])

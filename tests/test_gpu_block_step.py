@@ -94,6 +94,22 @@ def test_checked_norm_stays_in_bounds(libs, T, K, xf, sf, fmt):
     _same(outs)
 
 
+@pytest.mark.parametrize("T,K,sf", [(4901, 512, 0), (4865, 1280, 1), (700, 4096, 0), (320, 6144, 0), (170, 16384, 0)])
+def test_checked_norm_gradient_of_many_rows_stays_in_bounds(libs, T, K, sf):
+    dy, h, w = _x(T, K, 1 - sf, 11), _x(T, K, sf, 12), _x(1, K, 0, 13)
+    rstd, outs = torch.rand(T, device="cuda"), []
+    for L in libs:
+        dx, dw = _buf(T * K * (4 if sf else 2)), _buf(4 * K)
+        n = mx.rmsnorm_backward_workspace_bytes(T, K)
+        ws = _buf(n)
+        assert L.mx_rmsnorm_backward(dy.data_ptr(), 1 - sf, K, h.data_ptr(), sf, K, w.data_ptr(), 0, rstd.data_ptr(),
+                                     h.data_ptr(), K, T, K, dx.data_ptr(), K, dw.data_ptr(), ws.data_ptr(), n,
+                                     None) == 0
+        assert L.mx_check_status(None) == 0
+        outs.append((dx, dw))
+    _same(outs)
+
+
 @pytest.mark.parametrize("T,F", [(1, 32), (5, 1056), (130, 288), (3, 4128), (700, 2080)])
 @pytest.mark.parametrize("gf,fmt", [(1, 2), (0, 1)])
 def test_checked_swiglu_stays_in_bounds(libs, T, F, gf, fmt):
