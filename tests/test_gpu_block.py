@@ -193,6 +193,34 @@ def test_norm_backward_many_rows(T, K, dt, st, pad, res):
     test_norm_backward(T, K, dt, st, BF16, pad, res)
 
 
+@pytest.mark.parametrize("T", [3, 170])
+def test_norm_backward_just_beyond_16384_columns(T):
+    test_norm_backward(T, 17024, BF16, BF16, BF16, 0, True)
+
+
+def _skewed(t):
+    """The same matrix at 16 bytes off a 32-byte boundary."""
+    wide = torch.zeros(t.shape[0], t.shape[1] + 16, dtype=t.dtype, device="cuda")
+    skew = 16 // t.element_size()
+    wide[:, skew:skew + t.shape[1]] = t
+    return wide[:, skew:skew + t.shape[1]]
+
+
+@pytest.mark.parametrize("T,K", [(5, 4096), (700, 2080)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_off_a_32_byte_boundary_give_the_same_bits(T, K, dtype):
+    x, r, w, dres = (_matrix(T, K, dtype, 91), _matrix(T, K, dtype, 92), _weight(K, F32, 93), _matrix(T, K, dtype, 94))
+    gu, dy = _matrix(T, 2 * K, dtype, 95), _matrix(T, K, dtype, 96)
+    runs = []
+    for f in (lambda t: t, _skewed):
+        o = mx.rmsnorm(f(x), w, residual=f(r), fmt=mx.FMT_MXFP8, out_h=f(torch.zeros_like(r)))
+        dx, dw = mx.rmsnorm_backward(f(dy), f(x), w, o.rstd, dres=f(dres), out_dx=f(torch.zeros_like(r)))
+        g = mx.swiglu(f(gu), fmt=mx.FMT_MXFP8)
+        runs.append([*o, dx, dw, *g, mx.swiglu_backward(f(dy), f(gu))])
+    mx.check_status()
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
 def test_norm_backward_in_place_many_rows():
     T, K = 700, 4096
     dy, h, w = _matrix(T, K, BF16, 35), _matrix(T, K, BF16, 36), _weight(K, F32, 37)
