@@ -405,6 +405,19 @@ def test_clip_into_a_flat_bucket(sizes, dt, ot, std):
     assert (flat[gaps] == 7.0).all()
 
 
+@pytest.mark.parametrize("count", [63, 64, 65, 255, 256, 257, 1023, 1024, 1025, 2049])
+def test_clip_at_the_edges_of_the_table(count):
+    """As many tensors as one table holds, one fewer and one more; 1 to 40 elements each."""
+    gs = _grads([1 + (7 * i) % 40 for i in range(count)], F32, 67)
+    n64 = _norm64(gs)
+    refs = [f64(g) * (0.01 / (n64 + 1e-6)) for g in gs]
+    norm = mx.clip_grads(gs, 0.01)
+    mx.check_status()
+    assert_near(f64(norm), np.array([n64]), n64 * 2.0 ** -22, "norm")
+    for g, ref in zip(gs, refs):
+        assert_near(g, ref, np.abs(ref) * (_rounding(F32) + DELTA) + TINY, "clipped")
+
+
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_clip_in_place_and_unaligned(dt):
     base = _grads([50000], dt, 62)[0]
