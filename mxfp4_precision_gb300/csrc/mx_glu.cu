@@ -15,7 +15,7 @@ namespace {
 
 using namespace rows;
 
-// Three forms of s = 1 / (1 + exp(-g)), u = 2^-24.
+// Three forms of the sigmoid s = 1 / (1 + exp(-g)) and of silu(g) = g s, u = 2^-24.
 //
 // kFast, |g| <= 80: the hardware's 2^x and reciprocal.  Their errors (2 and 1
 // units in the last place) and the rounded product g log2 e leave it within
@@ -23,13 +23,11 @@ using namespace rows;
 // take 54 instructions an element, which bounds the kernel (bf16 in, 8192 x 14336:
 // 171 us against 87 us for the memory).
 //
-// kFine, |g| <= 80: within 2 u, where the kernel has the time for it (fp32 in, bound
-// by memory), so that codes fall on a rounding boundary's other side no more often
-// than with expf and a division: exp(-g) = 2^n 2^f with n = round(-g log2 e) from
-// adding 1.5 * 2^23 (the sum's low bits then hold n), f by a two-part log2 e and
-// 2^f on [-1/2, 1/2] a degree-6 polynomial whose coefficients were fitted here for
-// the least relative error (0.03 u before their rounding to fp32, 0.27 u after); a
-// Newton step on the reciprocal.
+// kFine, |g| <= 80: silu(g) = g / (1 + expf(-g)), each step rounded as fp32 rounds
+// it, where the kernel has the time for it (fp32 in, bound by memory).  y, its codes
+// and its scales then have the bits of the formula in fp32; a sigmoid that was
+// multiplied by g put 6 in a million bf16 y on a rounding boundary's other side, at
+// the same time.
 //
 // kFar, any g: beyond 80, where the exponential of the forms above leaves fp32's
 // range, s is exp(g) down to the smallest subnormal below and 1 above; NaN for NaN.
@@ -37,21 +35,6 @@ enum : int { kFast, kFine, kFar };
 template <int FORM>
 __device__ __forceinline__ float sigmoid(float g) {
     float e, r;
-    if constexpr (FORM == kFine) {
-        const float z = fmaf(g, -0x1.715476p+0f, 12582912.0f);
-        float f = fmaf(g, -0x1.715476p+0f, 12582912.0f - z);
-        f = fmaf(g, -0x1.4ae0cp-26f, f);
-        float p = fmaf(0x1.41fbbcp-13f, f, 0x1.5f3e54p-10f);
-        p = fmaf(p, f, 0x1.3b2d4cp-7f);
-        p = fmaf(p, f, 0x1.c6aee8p-5f);
-        p = fmaf(p, f, 0x1.ebfbdcp-3f);
-        p = fmaf(p, f, 0x1.62e430p-1f);
-        p = fmaf(p, f, 1.0f);
-        // n, in -116 .. 116, moves p's exponent (p lies in [0.70, 1.42]).
-        const float d = 1.0f + __uint_as_float(__float_as_uint(p) + (__float_as_uint(z) << 23));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-        return fmaf(r, fmaf(-d, r, 1.0f), r);
-    }
     if (FORM == kFar && g < -80.0f) {
         asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * 0x1.715476p+0f));
         return e;
@@ -59,6 +42,25 @@ __device__ __forceinline__ float sigmoid(float g) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -0x1.715476p+0f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
+}
+
+// g / d to nearest for |g| <= 80 and d = 1 + exp(-g): a reciprocal with one Newton
+// step, and a quotient with one correction from its remainder (Markstein, IBM J. Res.
+// Dev. 34(1), 1990).  On the host it is the division's value for 4 10^8 such pairs, with
+// the reciprocal one unit off either way.  The division itself takes the kernel from
+// 178 to 182 us (fp32 in, 8192 x 14336).
+__device__ __forceinline__ float quotient(float g, float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    r = fmaf(r, fmaf(-d, r, 1.0f), r);
+    const float q = g * r;
+    return fmaf(-fmaf(d, q, -g), r, q);  // the remainder's sign so that -0 stays -0
+}
+
+template <int FORM>
+__device__ __forceinline__ float silu(float g) {
+    if constexpr (FORM == kFine) return quotient(g, __fadd_rn(1.0f, expf(-g)));
+    else return g * sigmoid<FORM>(g);
 }
 
 // Whether one of eight values lies beyond 80 or is NaN.
@@ -74,7 +76,7 @@ __device__ __forceinline__ V8 gated(const float (&g)[8], const float (&u)[8]) {
     V8 y;
 #pragma unroll
     for (int i = 0; i < 8; i += 2)
-        y.v[i / 2] = pack2(g[i] * sigmoid<FORM>(g[i]) * u[i], g[i + 1] * sigmoid<FORM>(g[i + 1]) * u[i + 1]);
+        y.v[i / 2] = pack2(silu<FORM>(g[i]) * u[i], silu<FORM>(g[i + 1]) * u[i + 1]);
     return y;
 }
 

@@ -1,0 +1,68 @@
+"""The operators between the GEMMs where their values are easily lost: the bits of
+SwiGLU's fp32 formula."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp4_precision_gb300 as mx
+import oracle
+from tests.block_testutil import canonical_scales
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from mxfp4_precision_gb300 import build
+    build.build()
+    mx.lib()
+
+
+def _normal(rows, cols, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(rows, cols, generator=g, device="cuda") * std
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16 if t.dtype == BF16 else torch.int32)
+
+
+# --------------------------------------------------------------------------- SwiGLU
+def _gates(T, F, seed):
+    """Rows of normal gates, then rows whose magnitudes spread over all of fp32 up to 80 (zeros of both
+    signs and subnormals among them)."""
+    g = _normal(T, F, seed, 3.0)
+    r = torch.Generator(device="cuda").manual_seed(seed + 1)
+    top = int(np.float32(80.0).view(np.int32))
+    wide = torch.randint(0, top + 1, (T // 4, F), generator=r, device="cuda", dtype=torch.int32)
+    wide[0, :8] = 0
+    wide = wide.view(F32) * torch.where(torch.rand(T // 4, F, generator=r, device="cuda") < 0.5, -1.0, 1.0)
+    g[-(T // 4):] = wide
+    return g
+
+
+@pytest.mark.parametrize("fmt", [mx.FMT_MXFP8, mx.FMT_MXFP4])
+def test_swiglu_of_fp32_has_the_bits_of_the_formula(fmt):
+    """y = g / (1 + exp(-g)) * u with every step rounded to fp32, then once to bf16 and once to the codes:
+    no value, code or scale differs.  4M elements: a form that is off by an fp32 bit here and there
+    moves some 6 in a million bf16 y across a rounding boundary."""
+    T, F = 2048, 2048
+    g, u = _gates(T, F, 1), _normal(T, F, 3)
+    o = mx.swiglu(torch.cat([g, u], 1), fmt=fmt)
+    mx.check_status()
+    y = g / (1 + torch.exp(-g)) * u
+    assert torch.equal(_bits(o.y), _bits(y.to(BF16)))
+    fp8 = fmt == mx.FMT_MXFP8
+    blocks = y.cpu().numpy().reshape(T, F // 32, 32)
+    want = (oracle.scale_bytes_e4m3 if fp8 else oracle.scale_bytes)(np.abs(blocks).max(-1))
+    scales, clean = canonical_scales(o.scales.cpu().numpy(), T, F)
+    assert clean and np.array_equal(scales, want)
+    # a power of two within fp32's range times a value: exact, or a zero of its sign in either format
+    v = blocks * np.exp2(127.0 - want.astype(np.float64)).astype(np.float32)[..., None]
+    c = (oracle.e4m3_rne if fp8 else oracle.e2m1_rne)(v).reshape(T, F)
+    got = o.codes.cpu().numpy()
+    if not fp8:
+        got = np.stack([got & 15, got >> 4], -1).reshape(T, F)
+    assert np.array_equal(got, c)
