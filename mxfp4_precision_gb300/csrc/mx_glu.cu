@@ -57,10 +57,13 @@ __device__ __forceinline__ float quotient(float g, float d) {
     return fmaf(-fmaf(d, q, -g), r, q);  // the remainder's sign so that -0 stays -0
 }
 
-template <int FORM>
+// silu(g) in form NEAR up to 80; beyond, where FAR allows for such gates, in kFar: an
+// element's form does not depend on its neighbours.
+template <int NEAR, bool FAR>
 __device__ __forceinline__ float silu(float g) {
-    if constexpr (FORM == kFine) return quotient(g, __fadd_rn(1.0f, expf(-g)));
-    else return g * sigmoid<FORM>(g);
+    if (FAR && !(fabsf(g) <= 80.0f)) return g * sigmoid<kFar>(g);
+    if constexpr (NEAR == kFine) return quotient(g, __fadd_rn(1.0f, expf(-g)));
+    else return g * sigmoid<kFast>(g);
 }
 
 // Whether one of eight values lies beyond 80 or is NaN.
@@ -71,12 +74,12 @@ __device__ __forceinline__ bool any_far(const float (&g)[8]) {
 }
 
 // y = g * s * u of eight columns.
-template <int FORM>
+template <int NEAR, bool FAR>
 __device__ __forceinline__ V8 gated(const float (&g)[8], const float (&u)[8]) {
     V8 y;
 #pragma unroll
     for (int i = 0; i < 8; i += 2)
-        y.v[i / 2] = pack2(silu<FORM>(g[i]) * u[i], silu<FORM>(g[i + 1]) * u[i + 1]);
+        y.v[i / 2] = pack2(silu<NEAR, FAR>(g[i]) * u[i], silu<NEAR, FAR>(g[i + 1]) * u[i + 1]);
     return y;
 }
 
@@ -168,7 +171,8 @@ __global__ void __launch_bounds__(kBlock, G::kBytes == 4 ? 8 : 10) mx_swiglu_ker
             float g[8], u[8];
             floats_of(to_v8(gr[k]), g);
             floats_of(to_v8(ur[k]), u);
-            const V8 y = any_far(g) ? gated<kFar>(g, u) : gated<G::kBytes == 4 ? kFine : kFast>(g, u);
+            constexpr int kNear = G::kBytes == 4 ? kFine : kFast;
+            const V8 y = any_far(g) ? gated<kNear, true>(g, u) : gated<kNear, false>(g, u);
             if (in && p.y.p != nullptr)
                 store8<BF16>(p.y, p.y.p + (r * p.F + col) * 2, y, p.aligned32, p.status);
             if (p.enc.fmt != kEncNone && at.c < p.enc.katoms * 16)

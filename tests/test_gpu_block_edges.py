@@ -1,5 +1,5 @@
 """The operators between the GEMMs where their values are easily lost: the bits of
-SwiGLU's fp32 formula."""
+SwiGLU's fp32 formula, elements beside gates beyond 80."""
 import numpy as np
 import pytest
 import torch
@@ -66,3 +66,26 @@ def test_swiglu_of_fp32_has_the_bits_of_the_formula(fmt):
     if not fp8:
         got = np.stack([got & 15, got >> 4], -1).reshape(T, F)
     assert np.array_equal(got, c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("far", [-80.5, 81.0, -300.0, 1e30])
+def test_swiglu_beside_far_gates_keeps_its_bits(dtype, far):
+    """One gate in eight replaced by one beyond 80, where its u is 0: no other element, code or scale
+    changes, forward or backward."""
+    T, F = 1024, 2048
+    gu, dy = _normal(T, 2 * F, 11, 3.0), _normal(T, F, 12)
+    at = torch.zeros(F, dtype=torch.bool, device="cuda")
+    at[5::8] = True
+    gu[:, F:][:, at] = 0
+    runs = []
+    for value in (0.5, far):
+        gu[:, :F][:, at] = value
+        x = gu.to(dtype)
+        o = mx.swiglu(x, fmt=mx.FMT_MXFP8)
+        d = mx.swiglu_backward(dy.to(dtype), x)
+        # the far elements' own results: zeros whose sign is the gate's, and du of the gate itself
+        runs.append([o.y[:, ~at], o.codes[:, ~at], o.scales, d[:, :F][:, ~at], d[:, F:][:, ~at]])
+    mx.check_status()
+    for a, b in zip(*runs):
+        assert torch.equal(_bits(a) if a.dtype == BF16 else a, _bits(b) if b.dtype == BF16 else b)
