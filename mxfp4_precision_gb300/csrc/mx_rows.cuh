@@ -197,13 +197,14 @@ __device__ __forceinline__ EncodedRow encoded_row(const Encoded &e, int64_t row)
 }
 
 // Encodes columns 8c .. 8c+7 of a row (c: the lane's chunk, lanes holding
-// consecutive chunks with c % 32 == lane; `in`: the chunk lies in the row,
-// a is 0 where it does not) and stores codes and scales.  Called by whole
+// consecutive chunks with c % 32 == lane; `in`: the chunk lies in the row)
+// and stores codes and scales.  Called by whole
 // warps.  The rules are those of mx_quantize and
 // mx_quantize_mxfp8: the exponent of the block's largest magnitude less the
 // format's largest exponent, codes to nearest even and saturating, a block
 // with Inf or NaN: scale 0xFF and zero codes.  Chunks past the row's end give
-// the zero bytes of the scales' padding.
+// the zero bytes of the scales' padding whatever a holds (0 times a row's Inf or
+// NaN rstd is NaN).
 __device__ __forceinline__ void encode8(const Encoded &e, const EncodedRow &at, uint32_t c, bool in,
                                         const V8 &a, int *status) {
     float f[8];
@@ -236,7 +237,7 @@ __device__ __forceinline__ void encode8(const Encoded &e, const EncodedRow &at, 
     // One byte a block: the eight of a warp lie in two sectors, as two gathered words would.
     if ((threadIdx.x & 3) == 0) {
         uint8_t *d = at.scales + (c >> 4) * 512u + ((c >> 2) & 3u);
-        if (MX_STORE_OK(d, 1, e.scales.p, e.scales.bytes, status)) *d = static_cast<uint8_t>(s);
+        if (MX_STORE_OK(d, 1, e.scales.p, e.scales.bytes, status)) *d = static_cast<uint8_t>(in ? s : 0u);
     }
 }
 

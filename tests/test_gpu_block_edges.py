@@ -1,5 +1,6 @@
 """The operators between the GEMMs where their values are easily lost: the bits of
-SwiGLU's fp32 formula, elements beside gates beyond 80."""
+SwiGLU's fp32 formula, elements beside gates beyond 80, the scales' padding of rows
+that hold no numbers."""
 import numpy as np
 import pytest
 import torch
@@ -27,6 +28,30 @@ def _normal(rows, cols, seed, std=1.0):
 
 def _bits(t):
     return t.contiguous().view(torch.int16 if t.dtype == BF16 else torch.int32)
+
+
+# --------------------------------------------------------------------------- norm
+@pytest.mark.parametrize("K", [32, 288, 1056, 4128])
+@pytest.mark.parametrize("fmt", [mx.FMT_MXFP8, mx.FMT_MXFP4])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_scale_padding_is_zero_beside_rows_without_numbers(K, fmt, residual):
+    """Rows whose rstd is NaN (a NaN in them), 0 (an Inf) or Inf (all zeros, eps = 0): their blocks are
+    marked as the formula has them, the padding beyond K stays zero, and so do the rows between."""
+    x = _normal(7, K, 21)
+    x[1, 3] = float("nan")
+    x[2, K - 1] = float("inf")
+    x[4] = 0
+    r = torch.zeros(7, K, dtype=BF16, device="cuda") if residual else None
+    o = mx.rmsnorm(x, torch.ones(K, device="cuda"), residual=r, eps=0.0, fmt=fmt)
+    mx.check_status()
+    scales, clean = canonical_scales(o.scales.cpu().numpy(), 7, K)
+    codes = o.codes.cpu().numpy()
+    assert clean
+    for row in (1, 4):
+        assert (scales[row] == 0xFF).all() and not codes[row].any()
+    assert scales[2, -1] == 0xFF and not scales[2, :-1].any()
+    for row in (0, 3, 5, 6):
+        assert codes[row].any() and (scales[row] != 0xFF).all()
 
 
 # --------------------------------------------------------------------------- SwiGLU
