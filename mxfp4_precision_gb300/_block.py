@@ -3,10 +3,10 @@ residual's addition, SwiGLU, their gradients, gradient norm and clipping).
 
 Matrices are 2-D CUDA tensors of torch.bfloat16 (or raw 16-bit patterns) or
 torch.float32 whose rows are contiguous; a row pitch (a slice of columns) is
-passed on.  Outputs and workspaces are allocated with torch unless given.  A
-`stream` other than the current one becomes the current one for the call, so
-that what is allocated belongs to it.  None of them records an autograd node:
-the gradients are calls of their own.
+passed on.  All tensors of a call are on one device.  Outputs and workspaces are
+allocated with torch unless given.  A `stream` other than the current one becomes
+the current one for the call, so that what is allocated belongs to it.  None of
+them records an autograd node: the gradients are calls of their own.
 
 The tensors are checked and unpacked in ``_build/mx_torch.so``
 (csrc/mx_torch.cpp), which calls the C ABI in include/mx.h; ValueError for

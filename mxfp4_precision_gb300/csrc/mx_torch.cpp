@@ -8,6 +8,7 @@
 // a tensor).
 #include <Python.h>
 
+#include <initializer_list>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
@@ -44,6 +45,22 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     const at::Tensor &t = THPVariable_Unpack(o);
     if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
     return t;
+}
+
+// Refuses tensors that are not on the device of the call's first: the launch goes
+// there, where another device's address may fault or be read before it is written.
+void on_device(const at::Tensor &t, const char *name, c10::Device device) {
+    if (t.device() != device)
+        refuse("%s must be on %s like the call's first tensor, not on %s", name, device.str().c_str(),
+               t.device().str().c_str());
+}
+struct Argument {
+    int at;
+    const char *name;
+};
+void on_device(PyObject *const *a, std::initializer_list<Argument> others, c10::Device device) {
+    for (const Argument &o : others)
+        if (a[o.at] != Py_None) on_device(tensor(a[o.at], o.name), o.name, device);
 }
 
 int type_of(const at::Tensor &t, const char *name) {
@@ -170,6 +187,7 @@ struct Workspace {
 // rmsnorm(x, weight, residual, eps, fmt, want_y, out_h) -> (h, y, codes, scales, rstd)
 PyObject *rmsnorm(PyObject *const *a) {
     const at::Tensor &x = matrix(a[0], "x");
+    on_device(a, {{1, "weight"}, {2, "residual"}, {6, "out_h"}}, x.device());
     const Here here(x);
     const int64_t T = x.size(0), K = x.size(1);
     const Matrix xm = matrix_of(x, "x", T, K);
@@ -200,6 +218,7 @@ PyObject *rmsnorm(PyObject *const *a) {
 // rmsnorm_backward(dy, h, weight, rstd, dres, want_dw, ws, out_dx) -> (dx, dw)
 PyObject *rmsnorm_backward(PyObject *const *a) {
     const at::Tensor &dy = matrix(a[0], "dy");
+    on_device(a, {{1, "h"}, {2, "weight"}, {3, "rstd"}, {4, "dres"}, {6, "workspace"}, {7, "out_dx"}}, dy.device());
     const Here here(dy);
     const int64_t T = dy.size(0), K = dy.size(1);
     const Matrix dm = matrix_of(dy, "dy", T, K);
@@ -251,6 +270,7 @@ PyObject *swiglu(PyObject *const *a) {
 // swiglu_backward(dy, gu, out) -> dgu
 PyObject *swiglu_backward(PyObject *const *a) {
     const at::Tensor &dy = matrix(a[0], "dy");
+    on_device(a, {{1, "gu"}, {2, "out"}}, dy.device());
     const Here here(dy);
     const int64_t T = dy.size(0), F = dy.size(1);
     const Matrix dm = matrix_of(dy, "dy", T, F);
@@ -263,14 +283,16 @@ PyObject *swiglu_backward(PyObject *const *a) {
     return wrap(out);
 }
 
-// The tensors of a Python sequence: addresses, sizes, types.
+// The tensors of a Python sequence (none for None): addresses, sizes, types; all on
+// the device of the sequence's first, or on the one given.
 struct Tensors {
     std::vector<void *> p;
     std::vector<int64_t> n;
     std::vector<int> type;
     at::Tensor first;
 
-    Tensors(PyObject *list, const char *name) {
+    Tensors(PyObject *list, const char *name, const at::Tensor *on = nullptr) {
+        if (list == Py_None) return;
         PyObject *s = PySequence_Fast(list, "a sequence of tensors is expected");
         if (s == nullptr) throw Raised{};
         struct Release {
@@ -283,11 +305,12 @@ struct Tensors {
         type.reserve(count);
         for (Py_ssize_t i = 0; i < count; ++i) {
             const at::Tensor &t = tensor(PySequence_Fast_GET_ITEM(s, i), name);
+            if (i == 0) first = t;
+            on_device(t, name, (on != nullptr ? *on : first).device());
             if (!t.is_contiguous()) refuse("%s must be contiguous", name);
             p.push_back(t.data_ptr());
             n.push_back(t.numel());
             type.push_back(type_of(t, name));
-            if (i == 0) first = t;
         }
     }
 };
@@ -298,6 +321,8 @@ PyObject *clip(PyObject *const *a) {
     const bool scale = truth(a[2]);
     if (g.p.empty()) refuse("no gradients");
     const at::Tensor &like = g.first;
+    const Tensors out(a[1], "out", &like);
+    on_device(a, {{5, "workspace"}}, like.device());
     const Here here(like);
     const int64_t count = static_cast<int64_t>(g.p.size());
     const at::Tensor norm = empty(like, {1}, at::kFloat);
@@ -312,7 +337,6 @@ PyObject *clip(PyObject *const *a) {
                             real(a[3]), real(a[4]), norm_p, ws.t.data_ptr(), ws.bytes, here.stream),
               "mx_clip_grads");
     } else {
-        const Tensors out(a[1], "out");
         if (out.n != g.n) refuse("out must hold one tensor of the same size for each gradient");
         check(mx_clip_grads(g.p.data(), g.n.data(), g.type.data(), out.p.data(), out.type.data(),
                             count, real(a[3]), real(a[4]), norm_p, ws.t.data_ptr(), ws.bytes,
