@@ -4,7 +4,8 @@ Each CUDA translation unit compiles in parallel to an object file, then they
 are linked into one shared library (static CUDA runtime, no libcuda link: the
 driver entry point for tensor-map encoding is fetched at run time).  Beside it,
 ``_build/mx_torch.so``: the Python entry points of the operators between the
-GEMMs (csrc/mx_torch.cpp, host code only, against the installed torch).
+GEMMs (csrc/mx_torch.cpp, host code only, against the installed torch); where
+torch is not installed the library alone is built, for users of its C ABI.
 """
 from __future__ import annotations
 
@@ -55,16 +56,15 @@ def _stale(lib: str | None = None) -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
+    """Folder of the installed torch; None without one."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or spec.origin is None:
-        raise RuntimeError("torch not found: the Python entry points need it to build")
-    return os.path.dirname(spec.origin)
+    return None if spec is None or spec.origin is None else os.path.dirname(spec.origin)
 
 
-def _compile_torch(verbose: bool) -> str:
+def _compile_torch(torch: str, verbose: bool) -> str:
     """Object file of the Python entry points (host code)."""
-    torch, obj = _torch_dir(), os.path.join(BUILD_DIR, "mx_torch.o")
+    obj = os.path.join(BUILD_DIR, "mx_torch.o")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c",
@@ -86,7 +86,10 @@ def _run(cmd: list[str], verbose: bool = False) -> None:
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
           checked: bool = False) -> str:
     out_dir, lib = (CHECKED_DIR, CHECKED_LIB) if checked else (BUILD_DIR, LIB)
-    if not force and not _stale(lib) and (checked or not _stale(TORCH_LIB)):
+    torch = None if checked else _torch_dir()
+    new_lib = force or _stale(lib)
+    new_torch = torch is not None and (force or _stale(TORCH_LIB))
+    if not new_lib and not new_torch:
         return lib
     os.makedirs(out_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -98,15 +101,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        torch_obj = None if checked else ex.submit(_compile_torch, verbose)
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = lib + f".tmp{os.getpid()}"
-    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
-    os.replace(tmp, lib)
+        torch_obj = ex.submit(_compile_torch, torch, verbose) if new_torch else None
+        objs = list(ex.map(compile_one, SOURCES)) if new_lib else []
+    if new_lib:
+        tmp = lib + f".tmp{os.getpid()}"
+        _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
+        os.replace(tmp, lib)
     if torch_obj is not None:
         tmp = TORCH_LIB + f".tmp{os.getpid()}"
         _run(["g++", "-shared", "-o", tmp, torch_obj.result(), "-L", out_dir, "-l:libmx.so", "-Wl,-rpath,$ORIGIN",
-              "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+              "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
         os.replace(tmp, TORCH_LIB)
     return lib
 
