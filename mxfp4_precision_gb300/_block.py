@@ -21,7 +21,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _binding as _b
-from .build import TORCH_LIB
+from .build import TORCH_LIB, fits_torch
 
 FMT_MXFP4, FMT_MXFP8 = 1, 2
 
@@ -36,6 +36,10 @@ def _load():
             if not os.path.exists(TORCH_LIB):
                 raise RuntimeError(
                     f"MXFP4 torch entry points not found at {TORCH_LIB}; build them with "
+                    "`python -c 'import __graft_entry__ as g; g.build()'`")
+            if not fits_torch():
+                raise RuntimeError(
+                    f"{TORCH_LIB} was built against another torch or Python; build it again with "
                     "`python -c 'import __graft_entry__ as g; g.build()'`")
             spec = importlib.util.spec_from_file_location("mx_torch", TORCH_LIB)
             module = importlib.util.module_from_spec(spec)

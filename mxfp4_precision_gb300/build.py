@@ -24,6 +24,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD_DIR, "libmx.so")
 TORCH_SOURCE = "mx_torch.cpp"
 TORCH_LIB = os.path.join(BUILD_DIR, "mx_torch.so")
+TORCH_STAMP = TORCH_LIB + ".built_against"
 # Bounds-checked variant (every kernel store guarded; see MX_ERR_BOUNDS in mx.h),
 # used by the tests only.
 CHECKED_DIR = os.path.join(HERE, "_build_checked")
@@ -62,6 +63,21 @@ def _torch_dir() -> str | None:
     return None if spec is None or spec.origin is None else os.path.dirname(spec.origin)
 
 
+def _torch_stamp(torch: str) -> str:
+    """What mx_torch.so is built against, beside the sources: Python, machine and torch."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([str(sysconfig.get_config_var("SOABI")), torch, f.read()])
+
+
+def fits_torch(torch: str | None = None) -> bool:
+    """Whether mx_torch.so was built against this Python and the installed torch."""
+    torch = torch or _torch_dir()
+    if torch is None or not os.path.exists(TORCH_LIB) or not os.path.exists(TORCH_STAMP):
+        return False
+    with open(TORCH_STAMP) as f:
+        return f.read() == _torch_stamp(torch)
+
+
 def _compile_torch(torch: str, verbose: bool) -> str:
     """Object file of the Python entry points (host code)."""
     obj = os.path.join(BUILD_DIR, "mx_torch.o")
@@ -88,7 +104,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     out_dir, lib = (CHECKED_DIR, CHECKED_LIB) if checked else (BUILD_DIR, LIB)
     torch = None if checked else _torch_dir()
     new_lib = force or _stale(lib)
-    new_torch = torch is not None and (force or _stale(TORCH_LIB))
+    new_torch = torch is not None and (force or _stale(TORCH_LIB) or not fits_torch(torch))
     if not new_lib and not new_torch:
         return lib
     os.makedirs(out_dir, exist_ok=True)
@@ -112,6 +128,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         _run(["g++", "-shared", "-o", tmp, torch_obj.result(), "-L", out_dir, "-l:libmx.so", "-Wl,-rpath,$ORIGIN",
               "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
         os.replace(tmp, TORCH_LIB)
+        with open(TORCH_STAMP, "w") as f:
+            f.write(_torch_stamp(torch))
     return lib
 
 
