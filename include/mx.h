@@ -396,12 +396,14 @@ mx_status mx_swiglu_backward(const void *d_dy, int dy_type, int64_t dy_pitch, co
  *                               g_i itself (same type).  NULL: all in place.
  *   d_norm                      one fp32 on the device
  *   d_ws                        mx_grad_workspace_bytes(count) bytes, 256-byte aligned
- * Pointers need only their element's alignment (slices of a flat bucket); whole
- * 16-byte vectors are used where gradient and output are 16-byte aligned.  A size
- * of 0 is skipped.  No tensors: the norm is 0.  A norm that is NaN makes every
+ * Pointers need only their element's alignment (slices of a flat bucket).  Vectors of
+ * 8 elements are used from the gradient's first boundary of one (16 bytes of bf16, 32
+ * of fp32), where the output is 16-byte aligned there; it is written element by element
+ * otherwise.  A size of 0 is skipped.  No tensors: the norm is 0.  A norm that is NaN makes every
  * output NaN, an infinite one every finite gradient 0.  In place with nothing to
  * clip (norm + eps <= max_norm) nothing is written.  The order of the sum is
- * fixed by the sizes: the same inputs give the same bits.
+ * fixed by the sizes, the types and the gradients' alignment to such a boundary: the
+ * same inputs give the same bits, elsewhere in memory the last ones may differ.
  */
 size_t mx_grad_workspace_bytes(int64_t count);
 mx_status mx_grad_norm(const void *const *h_grads, const int64_t *h_sizes, const int *h_types,

@@ -1,13 +1,13 @@
 """The operators between the GEMMs where their values are easily lost: the bits of
 SwiGLU's fp32 formula, elements beside gates beyond 80, the scales' padding of rows
-that hold no numbers."""
+that hold no numbers, gradients and outputs at every alignment."""
 import numpy as np
 import pytest
 import torch
 
 import mxfp4_precision_gb300 as mx
 import oracle
-from tests.block_testutil import canonical_scales
+from tests.block_testutil import DELTA, TINY, UB, assert_near, canonical_scales, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +114,28 @@ def test_swiglu_beside_far_gates_keeps_its_bits(dtype, far):
     mx.check_status()
     for a, b in zip(*runs):
         assert torch.equal(_bits(a) if a.dtype == BF16 else a, _bits(b) if b.dtype == BF16 else b)
+
+
+# --------------------------------------------------------------------------- clipping
+@pytest.mark.parametrize("n", [5, 300, 5000])
+@pytest.mark.parametrize("dt,ot", [(F32, BF16), (F32, F32), (BF16, F32), (BF16, BF16)])
+def test_clip_at_every_pair_of_alignments(n, dt, ot):
+    """Gradients that begin 0 to 8 elements off a 32-byte boundary into outputs that begin 0 to 8 off
+    one (an fp32 gradient 4 off and a bf16 output 0 off are both 16-byte aligned), in one call."""
+    pairs = [(a, b) for a in range(9) for b in range(9)]
+    wide = -(-(n + 8) // 16) * 16 + 16
+    x = _normal(len(pairs), wide, 31, 0.02).to(dt)
+    out = torch.full((len(pairs), wide), 7.0, dtype=ot, device="cuda")
+    grads = [x[i, a:a + n] for i, (a, _) in enumerate(pairs)]
+    outs = [out[i, b:b + n] for i, (_, b) in enumerate(pairs)]
+    norm = mx.clip_grads(grads, 0.1, out=outs)
+    mx.check_status()
+    want = np.sqrt(sum((f64(g) ** 2).sum() for g in grads))
+    assert_near(f64(norm), np.array([want]), want * 2.0 ** -22, "norm")
+    assert want > 0.2
+    gaps = torch.ones_like(out, dtype=torch.bool)
+    for i, (a, b) in enumerate(pairs):
+        ref = f64(grads[i]) * (0.1 / (want + 1e-6))
+        assert_near(outs[i], ref, np.abs(ref) * (DELTA + (UB if ot == BF16 else 0)) + TINY, f"{a} -> {b}")
+        gaps[i, b:b + n] = False
+    assert (out[gaps] == 7.0).all()
