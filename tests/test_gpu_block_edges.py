@@ -1,5 +1,5 @@
 """The operators between the GEMMs where their values are easily lost: the bits of
-SwiGLU's fp32 formula, elements beside gates beyond 80, the scales' padding of rows
+SwiGLU's fp32 formula, gates beyond 80 and elements beside them, the scales' padding of rows
 that hold no numbers, gradients and outputs at every alignment."""
 import numpy as np
 import pytest
@@ -7,7 +7,8 @@ import torch
 
 import mxfp4_precision_gb300 as mx
 import oracle
-from tests.block_testutil import DELTA, TINY, UB, assert_near, canonical_scales, f64
+from tests.block_testutil import (DELTA, TINY, UB, assert_near, canonical_scales, f64, sigmoid64, swiglu64,
+                                  swiglu_backward64)
 
 pytestmark = pytest.mark.gpu
 
@@ -114,6 +115,40 @@ def test_swiglu_beside_far_gates_keeps_its_bits(dtype, far):
     mx.check_status()
     for a, b in zip(*runs):
         assert torch.equal(_bits(a) if a.dtype == BF16 else a, _bits(b) if b.dtype == BF16 else b)
+
+
+@pytest.mark.parametrize("gt", [F32, BF16])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_swiglu_of_far_gates_beside_large_values(gt, dt):
+    """Gates from -80 to -98, where exp(-g) leaves fp32 but exp(g) times u, or u and dy, is a normal value.
+
+    The exponential's argument g log2(e) is rounded at up to 2^8 (2^-17 ln 2 of the result, 89 u), its
+    factor to fp32 (0.23 u |g|, 23 u), the hardware's 2^x adds 4 u and the products 4 u: 120 u of DELTA's
+    128.  Below 2^-126 the sigmoid has steps of 2^-149, of which one may be lost."""
+    F = 352
+    g = torch.cat([torch.linspace(-80.0, -98.0, F - 8), torch.tensor([80.5, 81, 88, 89, 100, 1e3, 1e10, 3e38])])
+    g = g.to(gt).cuda()
+    g64 = f64(g)
+    mag = 10.0 ** torch.linspace(20, 30, F)
+    mag[-8:] = 1e-3
+    sign = torch.where(torch.arange(F) % 3 == 0, -1.0, 1.0)
+    gu = torch.cat([g, (mag * sign).cuda().to(gt)]).view(1, 2 * F)
+    dy = mag.flip(0).clone()
+    dy[-8:] = 1e-3
+    dy = dy.cuda().to(dt).view(1, F)
+    o, d = mx.swiglu(gu), f64(mx.swiglu_backward(dy, gu))
+    mx.check_status()
+    u64, d64, s = f64(gu)[:, F:], f64(dy), sigmoid64(g64)
+    step = np.where(s < 2.0 ** -126, 2.0 ** -149, 0.0)
+    y = swiglu64(f64(gu))
+    dgu = swiglu_backward64(d64, f64(gu))
+    for got, ref, lost, what in ((f64(o.y), y, np.abs(g64 * u64) * step, "y"),
+                                 (d[:, :F], dgu[:, :F], np.abs(d64 * u64 * (1 + np.abs(g64))) * step, "dg"),
+                                 (d[:, F:], dgu[:, F:], np.abs(d64 * g64) * step, "du")):
+        assert (np.abs(ref) < 1e38).all() and (np.abs(ref[:, :-8]) > 2.0 ** -126).all(), what
+        bound = np.abs(ref) * (UB + DELTA) + lost + TINY
+        assert (bound[:, :-8] < 0.5 * np.abs(ref[:, :-8])).all(), f"{what}: a lost sigmoid would pass"
+        assert_near(got, ref, bound, what)
 
 
 # --------------------------------------------------------------------------- clipping
