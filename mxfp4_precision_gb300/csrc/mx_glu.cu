@@ -18,10 +18,11 @@ using namespace rows;
 // Three forms of the sigmoid s = 1 / (1 + exp(-g)) and of silu(g) = g s, u = 2^-24.
 //
 // kFast, |g| <= 80: the hardware's 2^x and reciprocal.  Their errors (2 and 1
-// units in the last place) and the rounded product g log2 e leave it within
-// (5 + |g|) u: far inside the outputs' roundings.  expf and a division instead
-// take 54 instructions an element, which bounds the kernel (bf16 in, 8192 x 14336:
-// 171 us against 87 us for the memory).
+// units in the last place, 6 u), the rounded sum (u), the rounded product g log2 e
+// and the rounding of log2 e itself (|g| u and 0.23 |g| u of the exponential) leave
+// it within (7 + 1.23 |g|) u, 106 u at most: inside the outputs' roundings of 2^16 u
+// (bf16) and more.  expf and a division instead take 54 instructions an element,
+// which bounds the kernel (bf16 in, 8192 x 14336: 171 us against 87 us for the memory).
 //
 // kFine, |g| <= 80: silu(g) = g / (1 + expf(-g)), each step rounded as fp32 rounds
 // it, where the kernel has the time for it (fp32 in, bound by memory).  y, its codes
@@ -30,7 +31,8 @@ using namespace rows;
 // the same time.
 //
 // kFar, any g: beyond 80, where the exponential of the forms above leaves fp32's
-// range, s is exp(g) down to the smallest subnormal below and 1 above; NaN for NaN.
+// range, s is exp(g) down to the smallest subnormal below, within 116 u (the product
+// is rounded at up to 2^8, 89 u) and a step of 2^-149, and 1 above; NaN for NaN.
 enum : int { kFast, kFine, kFar };
 template <int FORM>
 __device__ __forceinline__ float sigmoid(float g) {
