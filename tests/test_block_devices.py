@@ -1,6 +1,8 @@
 """The operators between the GEMMs refuse a call whose tensors lie on several devices
-before anything is launched.  The tensors have sizes and devices and no memory, so no
-GPU is needed."""
+before anything is launched, and a stream of another device.  The tensors have sizes
+and devices and no memory, so no GPU is needed."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -55,4 +57,14 @@ def test_gradients_on_two_devices_are_refused(where):
                  lambda: mx.clip_grads(same, 1.0, ws=_at((1 << 20,), torch.uint8, "cuda:1")),
                  lambda: mx.grad_norm(same, ws=_at((1 << 20,), torch.uint8, "cuda:1"))):
         with pytest.raises(ValueError, match="must be on cuda:[01] like"):
+            call()
+
+
+def test_a_stream_of_another_device_is_refused():
+    stream = SimpleNamespace(device=torch.device("cuda:1"))
+    x, w = _at((T, K)), _at((K,))
+    for call in (lambda: mx.rmsnorm(x, w, stream=stream), lambda: mx.rmsnorm_backward(x, x, w, _at((T,)), stream=stream),
+                 lambda: mx.swiglu(x, stream=stream), lambda: mx.swiglu_backward(x, _at((T, 2 * K)), stream=stream),
+                 lambda: mx.grad_norm([x], stream=stream), lambda: mx.clip_grads(iter([x]), 1.0, stream=stream)):
+        with pytest.raises(ValueError, match="stream must be on cuda:0"):
             call()
