@@ -21,8 +21,8 @@ using namespace rows;
 // units in the last place, 6 u), the rounded sum (u), the rounded product g log2 e
 // and the rounding of log2 e itself (|g| u and 0.23 |g| u of the exponential) leave
 // it within (7 + 1.23 |g|) u, 106 u at most: inside the outputs' roundings of 2^16 u
-// (bf16) and more.  expf and a division instead take 54 instructions an element,
-// which bounds the kernel (bf16 in, 8192 x 14336: 171 us against 87 us for the memory).
+// (bf16) and more.  With bf16 input, where instructions bound the kernel, the form
+// below takes 125 us against 99 us (8192 x 14336, codes alone; the memory 87 us).
 //
 // kFine, |g| <= 80: silu(g) = g / (1 + expf(-g)), each step rounded as fp32 rounds
 // it, where the kernel has the time for it (fp32 in, bound by memory).  y, its codes
