@@ -412,6 +412,162 @@ mx_status mx_clip_grads(const void *const *h_grads, const int64_t *h_sizes, cons
                         void *const *h_outs, const int *h_out_types, int64_t count, float max_norm,
                         float eps, float *d_norm, void *d_ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* Products with an epilogue                                                  */
+/* ------------------------------------------------------------------------ */
+/*
+ * Activations, in fp32 (relu2: the square of relu; gelu: x Phi(x); gelu_tanh: its form
+ * with tanh; silu: x / (1 + exp(-x))).
+ */
+typedef enum {
+    MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_RELU2 = 2, MX_ACT_GELU = 3, MX_ACT_GELU_TANH = 4,
+    MX_ACT_SILU = 5
+} mx_act;
+
+/*
+ * mx_gemm_bias_act -- z = A . B^T + bias,  y = act(z) + residual, in one launch.
+ *   operands  MX_FORMAT_MXFP4 or MX_FORMAT_MXFP8: the format of A (M lines) and B
+ *             (N lines), contraction K, as in mx_gemm and mx_gemm_mxfp8
+ *   d_bias    [N] of bias_type, or NULL
+ *   d_res     [M][N] of res_type, pitch res_pitch elements, or NULL
+ *   d_y       [M][N] of y_type without gaps, or NULL; may be d_res itself (same
+ *             type, pitch N)
+ *   d_z       [M][N] bf16, what mx_bias_act_backward takes; or NULL
+ *   format, d_codes, d_scales   y encoded along its rows as the next product's
+ *             operand (see above), or MX_FORMAT_NONE and NULL
+ * At least one output.  Everything after the product is in fp32; y, z and the codes
+ * are each rounded once, from fp32.  K % 32 == 0, N % 8 == 0 (N % 32 == 0 to
+ * encode), pointers 16-byte aligned.  K == 0: z = bias.  M or N == 0: MX_OK, nothing
+ * launched.
+ */
+mx_status mx_gemm_bias_act(const void *d_Aq, const void *d_As, const void *d_Bq, const void *d_Bs,
+                           int operands, int64_t M, int64_t N, int64_t K, const void *d_bias,
+                           int bias_type, int act, const void *d_res, int res_type,
+                           int64_t res_pitch, void *d_y, int y_type, void *d_z, int format,
+                           void *d_codes, void *d_scales, void *stream);
+
+/*
+ * mx_bias_act_backward -- dz = dy * act'(z),  dbias = sum over rows of dz.
+ *   d_dy    [T][N] of dy_type, d_z [T][N] of z_type as mx_gemm_bias_act left it
+ *           (NULL with MX_ACT_NONE, where it is not read)
+ *   d_dz    [T][N] bf16 without gaps (dY of the Wgrad and Dgrad), or NULL
+ *   format, d_codes, d_scales   dz encoded along its rows (the Dgrad's operand), or
+ *           MX_FORMAT_NONE and NULL
+ *   d_dbias [N] fp32, overwritten, or NULL; the sum of dz before its rounding, in an
+ *           order fixed by T and N
+ *   d_ws    mx_bias_act_backward_workspace_bytes(T, N) bytes, 256-byte aligned
+ *           (only for d_dbias; may be NULL where that is 0)
+ * At least one output.  N, pitches % 8 == 0.  T == 0: d_dbias is zero-filled.
+ */
+size_t mx_bias_act_backward_workspace_bytes(int64_t T, int64_t N);
+mx_status mx_bias_act_backward(const void *d_dy, int dy_type, int64_t dy_pitch, const void *d_z,
+                               int z_type, int64_t z_pitch, int act, int64_t T, int64_t N,
+                               void *d_dz, int format, void *d_codes, void *d_scales,
+                               float *d_dbias, void *d_ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Products by expert                                                         */
+/* ------------------------------------------------------------------------ */
+/*
+ * Each of T tokens goes to `picks` of `experts` experts.  The rows of one
+ * expert form a segment; segments follow one another in the experts' order, and each
+ * begins at a multiple of 128 rows, so that a segment begins with a scale atom
+ * whichever way its rows are encoded.  A plan says where the rows are:
+ *   offsets [experts + 1] int32   first row of each segment; the last: rows in use
+ *   counts  [experts] int32       rows that tokens take; the others of a segment
+ *                                 (padding) hold zeros
+ *   slot    [T][picks] int32      row of each choice, -1 if it was dropped
+ *   source  [rows] int32          token * picks + choice of each row, -1 for none
+ * rows = mx_expert_rows(T, picks, experts): what the segments can take at most, a
+ * multiple of 128.  A plan lies on the device and is read there; a call needs no copy
+ * of it.  Whatever it holds, the calls stay inside the buffers of the
+ * sizes they are given.  At most MX_EXPERTS_MAX experts.
+ *
+ * mx_expert_plan -- makes one from d_index [T][picks] (int32, or int64 with
+ * index_bytes 8): the expert of each choice.  Numbers outside 0 .. experts - 1 are dropped
+ * choices.  Rows of an expert are in the order of (token, choice).
+ */
+#define MX_EXPERTS_MAX 512
+int64_t mx_expert_rows(int64_t T, int64_t picks, int64_t experts);
+size_t mx_expert_plan_workspace_bytes(int64_t T, int64_t picks, int64_t experts);
+mx_status mx_expert_plan(const void *d_index, int index_bytes, int64_t T, int64_t picks,
+                         int64_t experts, int32_t *d_offsets, int32_t *d_counts, int32_t *d_slot,
+                         int32_t *d_source, void *d_ws, size_t ws_bytes, void *stream);
+
+/*
+ * mx_expert_dispatch -- y[slot] = x[token] for every choice; all other rows zero.
+ * x [T][K] of x_type; y [rows][K] in bf16 (d_y) and / or encoded along its rows.
+ * mx_expert_combine -- y[token] = res[token] + sum over its choices of
+ * weight * rows[slot]: d_rows [rows][K], d_weights [T][picks] fp32 (NULL: 1, which is
+ * the gradient of the dispatch), d_res [T][K] or NULL, d_y [T][K] without gaps (may
+ * be d_res itself, same type, pitch K).  Dropped choices add nothing.
+ * mx_expert_combine_backward -- drows[slot] = weight * dy[token] (bf16 in d_drows
+ * and / or encoded; all other rows zero) and d_dweights [T][picks] fp32 = dy[token] .
+ * rows[slot] (0 for dropped choices; NULL: not computed, d_rows not read).
+ * K and pitches % 8 == 0 (K % 32 == 0 to encode).  T == 0 or picks == 0: rows without a
+ * token are still zeroed, and y = res.
+ */
+mx_status mx_expert_dispatch(const void *d_x, int x_type, int64_t x_pitch, const int32_t *d_slot,
+                             const int32_t *d_source, int64_t T, int64_t picks, int64_t rows,
+                             int64_t K, void *d_y, int format, void *d_codes, void *d_scales,
+                             void *stream);
+mx_status mx_expert_combine(const void *d_rows, int rows_type, int64_t rows_pitch,
+                            const int32_t *d_slot, const float *d_weights, int64_t T,
+                            int64_t picks, int64_t rows, int64_t K, const void *d_res, int res_type,
+                            int64_t res_pitch, void *d_y, int y_type, void *stream);
+mx_status mx_expert_combine_backward(const void *d_dy, int dy_type, int64_t dy_pitch,
+                                     const void *d_rows, int rows_type, int64_t rows_pitch,
+                                     const int32_t *d_slot, const int32_t *d_source,
+                                     const float *d_weights, int64_t T, int64_t picks, int64_t rows,
+                                     int64_t K, void *d_drows, int format, void *d_codes,
+                                     void *d_scales, float *d_dweights, void *stream);
+
+/*
+ * mx_quantize_experts -- encodes [experts][rows][cols] bf16 matrices one by one, to
+ * nearest: expert e's codes at e * mx_codes_bytes(lines, k) (mx_mxfp8_codes_bytes), its
+ * scales at e * mx_scales_bytes(lines, k).  MXFP4 with the arguments of mx_quantize; MXFP8
+ * (rot MX_ROT_NONE) with MX_CONTRACT_ROWS alone, as mx_quantize_mxfp8, else
+ * MX_ERR_UNSUPPORTED.
+ */
+mx_status mx_quantize_experts(const void *d_src, int64_t experts, int64_t rows, int64_t cols,
+                              int operands, int contract, int rot, int rot_block, uint64_t seed,
+                              void *d_codes, void *d_scales, void *stream);
+
+/*
+ * mx_gemm_experts -- z[s] = A[s] . B_e^T + bias_e,  y = act(z), for the rows s of every
+ * expert e; rows without a token, and rows behind the last segment, are zero.
+ * A [rows] lines, B as mx_quantize_experts leaves [experts] times N lines, d_bias
+ * [experts][N] or NULL; outputs and the rest as mx_gemm_bias_act with M = rows.  For
+ * the Dgrad, B holds the transposed weights (mx_quantize_experts with
+ * MX_CONTRACT_ROWS).  experts * N < 2^31.
+ *
+ * mx_gemm_experts_wgrad -- C[e] [M][N] = A_e . B_e^T over expert e's rows: A with M and
+ * B with N lines, contraction `rows`, encoded down the rows (mx_quantize,
+ * mx_quantize_mxfp8 with MX_CONTRACT_ROWS); C of c_type.  Zero for an expert without rows.
+ * Rotations of up to 128 stay inside a segment.
+ *
+ * mx_linear_experts_wgrad -- dW[e] [N][K] = dY_e^T X_e with the encode:
+ * dY [rows][N], X [rows][K] bf16, whose rows without a token must be zero
+ * (mx_expert_dispatch, mx_expert_combine_backward and mx_gemm_experts leave them so).
+ * Arguments as mx_linear_wgrad, MXFP8 without rotation to nearest;
+ * rot_block 256 gets MX_ERR_UNSUPPORTED.  The workspace holds the operands.
+ */
+mx_status mx_gemm_experts(const void *d_Aq, const void *d_As, const void *d_Bq, const void *d_Bs,
+                          int operands, const int32_t *d_offsets, const int32_t *d_counts,
+                          int64_t experts, int64_t rows, int64_t N, int64_t K, const void *d_bias,
+                          int bias_type, int act, void *d_y, int y_type, void *d_z, int format,
+                          void *d_codes, void *d_scales, void *stream);
+mx_status mx_gemm_experts_wgrad(const void *d_Aq, const void *d_As, const void *d_Bq,
+                                const void *d_Bs, int operands, const int32_t *d_offsets,
+                                int64_t experts, int64_t rows, int64_t M, int64_t N, void *d_C,
+                                int c_type, void *stream);
+size_t mx_linear_experts_wgrad_workspace_bytes(int operands, int64_t rows, int64_t N, int64_t K);
+mx_status mx_linear_experts_wgrad(const void *d_dY, const void *d_X, int operands,
+                                  const int32_t *d_offsets, int64_t experts, int64_t rows,
+                                  int64_t N, int64_t K, int rot, int rot_block, int rnd,
+                                  uint64_t seed, void *d_dW, int dw_type, void *d_ws,
+                                  size_t ws_bytes, void *stream);
+
 /*
  * mx_linear_wgrad_noalloc -- mx_linear_wgrad without a caller workspace.
  * No counterpart in the paper: this is a deployment convenience.

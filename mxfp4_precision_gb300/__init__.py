@@ -3,7 +3,8 @@
 This package is a thin binding over the in-tree library ``_build/libmx.so``: it
 marshals torch tensors (device memory and the current CUDA stream) into the C
 calls and nothing else (ctypes for the encodes and GEMMs; a CPython module,
-``_build/mx_torch.so``, for the operators between them).  Every step of the path
+``_build/mx_torch.so``, for the operators between them, the products with an epilogue
+and those by expert).  Every step of the path
 runs in the library's CUDA kernels; there is no CPU fallback -- if the library
 is missing or fails to load, every call raises.
 """
@@ -21,6 +22,12 @@ from ._binding import (CONTRACT_COLS, CONTRACT_ROWS, OP_DGRAD, OP_FPROP, OP_WGRA
 from ._block import (FMT_MXFP4, FMT_MXFP8, RMSNormOut, SwiGLUOut, clip_grads, grad_norm,
                      grad_workspace_bytes, rmsnorm, rmsnorm_backward,
                      rmsnorm_backward_workspace_bytes, swiglu, swiglu_backward)
+from ._product import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_RELU2, ACT_SILU, BiasActGrad,
+                       ExpertGrad, ExpertPlan, ExpertRows, GemmOut, bias_act_backward,
+                       bias_act_backward_workspace_bytes, expert_combine, expert_combine_backward,
+                       expert_dispatch, expert_plan, expert_plan_workspace_bytes, expert_rows,
+                       gemm_bias_act, gemm_experts, gemm_experts_wgrad, linear_experts_wgrad,
+                       linear_experts_wgrad_workspace_bytes, quantize_experts)
 
 __all__ = [
     "CONTRACT_COLS", "CONTRACT_ROWS", "OP_DGRAD", "OP_FPROP", "OP_WGRAD", "ROT_HADAMARD_DET",
@@ -36,4 +43,10 @@ __all__ = [
     "FMT_MXFP4", "FMT_MXFP8", "RMSNormOut", "SwiGLUOut", "clip_grads", "grad_norm",
     "grad_workspace_bytes", "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
     "swiglu", "swiglu_backward",
+    "ACT_GELU", "ACT_GELU_TANH", "ACT_NONE", "ACT_RELU", "ACT_RELU2", "ACT_SILU", "BiasActGrad",
+    "ExpertGrad", "ExpertPlan", "ExpertRows", "GemmOut", "bias_act_backward",
+    "bias_act_backward_workspace_bytes", "expert_combine", "expert_combine_backward",
+    "expert_dispatch", "expert_plan", "expert_plan_workspace_bytes", "expert_rows",
+    "gemm_bias_act", "gemm_experts", "gemm_experts_wgrad", "linear_experts_wgrad",
+    "linear_experts_wgrad_workspace_bytes", "quantize_experts",
 ]

@@ -32,6 +32,10 @@ EXPORTED = [
     "mx_rmsnorm", "mx_rmsnorm_backward_workspace_bytes", "mx_rmsnorm_backward",
     "mx_swiglu", "mx_swiglu_backward",
     "mx_grad_workspace_bytes", "mx_grad_norm", "mx_clip_grads",
+    "mx_gemm_bias_act", "mx_bias_act_backward_workspace_bytes", "mx_bias_act_backward",
+    "mx_expert_rows", "mx_expert_plan_workspace_bytes", "mx_expert_plan", "mx_expert_dispatch",
+    "mx_expert_combine", "mx_expert_combine_backward", "mx_quantize_experts", "mx_gemm_experts",
+    "mx_gemm_experts_wgrad", "mx_linear_experts_wgrad_workspace_bytes", "mx_linear_experts_wgrad",
     "mx_check_status",
     "mx_debug_timeout_probe", "mx_bench_mma", "mx_status_string", "mx_version",
 ]
@@ -128,6 +132,39 @@ def lib() -> ctypes.CDLL:
             L.mx_grad_norm.restype = i32
             L.mx_clip_grads.argtypes = [P, P, P, P, P, i64, f32, f32, P, P, sz, P]
             L.mx_clip_grads.restype = i32
+            L.mx_gemm_bias_act.argtypes = [P, P, P, P, i32, i64, i64, i64, P, i32, i32, P, i32, i64, P, i32,
+                                           P, i32, P, P, P]
+            L.mx_gemm_bias_act.restype = i32
+            L.mx_bias_act_backward_workspace_bytes.argtypes = [i64, i64]
+            L.mx_bias_act_backward_workspace_bytes.restype = sz
+            L.mx_bias_act_backward.argtypes = [P, i32, i64, P, i32, i64, i32, i64, i64, P, i32, P, P, P, P,
+                                               sz, P]
+            L.mx_bias_act_backward.restype = i32
+            L.mx_expert_rows.argtypes = [i64, i64, i64]
+            L.mx_expert_rows.restype = i64
+            L.mx_expert_plan_workspace_bytes.argtypes = [i64, i64, i64]
+            L.mx_expert_plan_workspace_bytes.restype = sz
+            L.mx_expert_plan.argtypes = [P, i32, i64, i64, i64, P, P, P, P, P, sz, P]
+            L.mx_expert_plan.restype = i32
+            L.mx_expert_dispatch.argtypes = [P, i32, i64, P, P, i64, i64, i64, i64, P, i32, P, P, P]
+            L.mx_expert_dispatch.restype = i32
+            L.mx_expert_combine.argtypes = [P, i32, i64, P, P, i64, i64, i64, i64, P, i32, i64, P, i32, P]
+            L.mx_expert_combine.restype = i32
+            L.mx_expert_combine_backward.argtypes = [P, i32, i64, P, i32, i64, P, P, P, i64, i64, i64, i64, P,
+                                                     i32, P, P, P, P]
+            L.mx_expert_combine_backward.restype = i32
+            L.mx_quantize_experts.argtypes = [P, i64, i64, i64, i32, i32, i32, i32, u64, P, P, P]
+            L.mx_quantize_experts.restype = i32
+            L.mx_gemm_experts.argtypes = [P, P, P, P, i32, P, P, i64, i64, i64, i64, P, i32, i32, P, i32, P,
+                                          i32, P, P, P]
+            L.mx_gemm_experts.restype = i32
+            L.mx_gemm_experts_wgrad.argtypes = [P, P, P, P, i32, P, i64, i64, i64, i64, P, i32, P]
+            L.mx_gemm_experts_wgrad.restype = i32
+            L.mx_linear_experts_wgrad_workspace_bytes.argtypes = [i32, i64, i64, i64]
+            L.mx_linear_experts_wgrad_workspace_bytes.restype = sz
+            L.mx_linear_experts_wgrad.argtypes = [P, P, i32, P, i64, i64, i64, i64, i32, i32, i32, u64, P, i32,
+                                                  P, sz, P]
+            L.mx_linear_experts_wgrad.restype = i32
             L.mx_check_status.argtypes = [P]
             L.mx_check_status.restype = i32
             L.mx_debug_timeout_probe.argtypes = [i64, P]

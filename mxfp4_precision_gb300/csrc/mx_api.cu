@@ -1,5 +1,6 @@
 // mx_api.cu -- the library's C ABI (include/mx.h): argument checks, workspace
 // carving, tensor-map encoding, per-device status word, and the launches.
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -388,6 +389,84 @@ mx_status check_row_encode(const RowEncode &e, int64_t T, int64_t cols) {
     if (T == 0 || cols == 0) return MX_OK;
     if (e.codes == nullptr || e.scales == nullptr) return MX_ERR_INVALID_ARG;
     return aligned16(e.codes) && aligned16(e.scales) ? MX_OK : MX_ERR_ALIGN;
+}
+
+// ---- products with an epilogue, and by expert
+bool valid_act(int act) { return act >= MX_ACT_NONE && act <= MX_ACT_SILU; }
+
+// Outputs and bias of a product of p.M x p.N; set in p.
+mx_status check_epilogue(Product &p, const void *bias, int bias_type, int act, void *y, int y_type, void *z,
+                         int format, void *codes, void *scales) {
+    if (!valid_act(act) || (bias != nullptr && !valid_type(bias_type)) || (y != nullptr && !valid_type(y_type)))
+        return MX_ERR_INVALID_ARG;
+    if (p.M > 0 && p.N > 0 && y == nullptr && z == nullptr && format == MX_FORMAT_NONE) return MX_ERR_INVALID_ARG;
+    p.enc = {format, codes, scales};
+    mx_status st = check_row_sizes(p.M, p.N);
+    if (st != MX_OK || (st = check_row_encode(p.enc, p.M, p.N)) != MX_OK) return st;
+    if (!aligned16(bias) || !aligned16(y) || !aligned16(z)) return MX_ERR_ALIGN;
+    p.bias = bias;
+    p.bias_f32 = bias_type == MX_TYPE_F32;
+    p.act = act;
+    p.y = y;
+    p.y_f32 = y_type == MX_TYPE_F32;
+    p.z = z;
+    return MX_OK;
+}
+
+// Operands and sizes.
+mx_status check_product(Product &p, int operands) {
+    if (operands != MX_FORMAT_MXFP4 && operands != MX_FORMAT_MXFP8) return MX_ERR_INVALID_ARG;
+    p.fp8 = operands == MX_FORMAT_MXFP8;
+    if (p.M < 0 || p.N < 0 || p.K < 0 || p.M > 0x7FFFFFFF || p.N > 0x3FFFFFFF || p.K > 0x7FFFFFFF) return MX_ERR_SHAPE;
+    if (p.M == 0 || p.N == 0) return MX_OK;
+    if (p.K % 32 != 0) return MX_ERR_SHAPE;
+    if (p.N % 8 != 0) return MX_ERR_ALIGN;
+    if (p.K == 0) return MX_OK;
+    if (!p.Aq || !p.As || !p.Bq || !p.Bs) return MX_ERR_INVALID_ARG;
+    if (!aligned16(p.Aq) || !aligned16(p.As) || !aligned16(p.Bq) || !aligned16(p.Bs)) return MX_ERR_ALIGN;
+    return MX_OK;
+}
+
+mx_status check_experts(int64_t experts, const int32_t *offsets) {
+    if (experts < 1) return MX_ERR_SHAPE;
+    if (experts > MX_EXPERTS_MAX) return MX_ERR_UNSUPPORTED;
+    if (offsets == nullptr) return MX_ERR_INVALID_ARG;
+    return aligned16(offsets) ? MX_OK : MX_ERR_ALIGN;
+}
+
+// A plan's sizes: entries and rows are counted in 32 bits.
+mx_status check_expert_rows(const ExpertRows &r) {
+    if (r.T < 0 || r.picks < 0 || r.rows < 0 || r.T > 0x7FFFFFFF || r.picks > 0x7FFFFFFF) return MX_ERR_SHAPE;
+    if (r.T * r.picks > 0x7FFFFFFF || r.rows > 0x7FFFFFFF || r.rows % 128 != 0) return MX_ERR_SHAPE;
+    return aligned16(r.slot) && aligned16(r.source) ? MX_OK : MX_ERR_ALIGN;
+}
+
+mx_status run_product(const Product &p, void *stream) {
+    const DeviceInfo *dev = nullptr;
+    const mx_status st = device_or_error(&dev);
+    if (st != MX_OK) return st;
+    const cudaError_t e = launch_product(p, *dev, static_cast<cudaStream_t>(stream));
+    return e == cudaErrorNotSupported ? MX_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+mx_status experts_wgrad_impl(const void *Aq, const void *As, const void *Bq, const void *Bs, int operands,
+                             const int32_t *offsets, int64_t experts, int64_t rows, int64_t M, int64_t N, void *C,
+                             int c_type, void *stream) {
+    Product p{};
+    p.mode = kProductDepth;
+    p.M = M, p.N = N, p.K = rows, p.experts = experts;
+    p.Aq = Aq, p.As = As, p.Bq = Bq, p.Bs = Bs;
+    p.offsets = offsets;
+    if (!valid_type(c_type)) return MX_ERR_INVALID_ARG;
+    mx_status st = check_product(p, operands);
+    if (st != MX_OK) return st;
+    if (rows % 128 != 0) return MX_ERR_SHAPE;
+    if ((st = check_experts(experts, offsets)) != MX_OK || M == 0 || N == 0) return st;
+    if (C == nullptr) return MX_ERR_INVALID_ARG;
+    if (!aligned16(C)) return MX_ERR_ALIGN;
+    p.y = C;
+    p.y_f32 = c_type == MX_TYPE_F32;
+    return run_product(p, stream);
 }
 
 mx_status grad_impl(const void *const *h_grads, const int64_t *h_sizes, const int *h_types,
@@ -787,6 +866,282 @@ mx_status mx_clip_grads(const void *const *h_grads, const int64_t *h_sizes, cons
     if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return MX_ERR_INVALID_ARG;
     return grad_impl(h_grads, h_sizes, h_types, h_outs, h_out_types, count, true, max_norm, eps,
                      d_norm, d_ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+mx_status mx_gemm_bias_act(const void *d_Aq, const void *d_As, const void *d_Bq, const void *d_Bs,
+                           int operands, int64_t M, int64_t N, int64_t K, const void *d_bias,
+                           int bias_type, int act, const void *d_res, int res_type,
+                           int64_t res_pitch, void *d_y, int y_type, void *d_z, int format,
+                           void *d_codes, void *d_scales, void *stream) {
+    TraceRange trace("mx_gemm_bias_act");
+    Product p{};
+    p.mode = kProductDense;
+    p.M = M, p.N = N, p.K = K;
+    p.Aq = d_Aq, p.As = d_As, p.Bq = d_Bq, p.Bs = d_Bs;
+    mx_status st = check_epilogue(p, d_bias, bias_type, act, d_y, y_type, d_z, format, d_codes, d_scales);
+    if (st != MX_OK) return st;
+    if (d_res != nullptr && !valid_type(res_type)) return MX_ERR_INVALID_ARG;
+    if ((st = check_product(p, operands)) != MX_OK || M == 0 || N == 0) return st;
+    if (d_res != nullptr && (st = check_rows(d_res, res_pitch, N)) != MX_OK) return st;
+    p.res = {d_res, res_pitch, res_type == MX_TYPE_F32};
+    return run_product(p, stream);
+}
+
+size_t mx_bias_act_backward_workspace_bytes(int64_t T, int64_t N) {
+    return T <= 0 || N <= 0 ? 0 : align256(bias_act_backward_ws(T, N));
+}
+
+mx_status mx_bias_act_backward(const void *d_dy, int dy_type, int64_t dy_pitch, const void *d_z,
+                               int z_type, int64_t z_pitch, int act, int64_t T, int64_t N,
+                               void *d_dz, int format, void *d_codes, void *d_scales,
+                               float *d_dbias, void *d_ws, size_t ws_bytes, void *stream) {
+    TraceRange trace("mx_bias_act_backward");
+    if (!valid_type(dy_type) || !valid_act(act)) return MX_ERR_INVALID_ARG;
+    if (act != MX_ACT_NONE && !valid_type(z_type)) return MX_ERR_INVALID_ARG;
+    if (T > 0 && N > 0 && d_dz == nullptr && format == MX_FORMAT_NONE && d_dbias == nullptr) return MX_ERR_INVALID_ARG;
+    mx_status st = check_row_sizes(T, N);
+    if (st != MX_OK) return st;
+    const RowEncode e{format, d_codes, d_scales};
+    if ((st = check_row_encode(e, T, N)) != MX_OK || N == 0) return st;
+    if (!aligned16(d_dbias)) return MX_ERR_ALIGN;
+    if (T == 0)
+        return d_dbias == nullptr ? MX_OK
+                                  : from_cuda(cudaMemsetAsync(d_dbias, 0, static_cast<size_t>(N) * sizeof(float),
+                                                              static_cast<cudaStream_t>(stream)));
+    if ((st = check_rows(d_dy, dy_pitch, N)) != MX_OK) return st;
+    if (act != MX_ACT_NONE && (st = check_rows(d_z, z_pitch, N)) != MX_OK) return st;
+    if (!aligned16(d_dz)) return MX_ERR_ALIGN;
+    if (d_dbias != nullptr && bias_act_backward_ws(T, N) > 0) {
+        if (d_ws == nullptr || ws_bytes < mx_bias_act_backward_workspace_bytes(T, N)) return MX_ERR_WORKSPACE;
+        if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return MX_ERR_ALIGN;
+    }
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    RowIn z{d_z, z_pitch, z_type == MX_TYPE_F32};
+    if (act == MX_ACT_NONE) z = {nullptr, 0, false};
+    return from_cuda(launch_bias_act_backward({d_dy, dy_pitch, dy_type == MX_TYPE_F32}, z, act, T, N, d_dz, e,
+                                              d_dbias, d_ws, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t mx_expert_rows(int64_t T, int64_t picks, int64_t experts) {
+    if (T <= 0 || picks <= 0 || experts <= 0 || T > 0x7FFFFFFF || picks > 0x7FFFFFFF) return 0;
+    const int64_t n = T * picks;
+    return (n + 127 * std::min(experts, n)) / 128 * 128;
+}
+
+size_t mx_expert_plan_workspace_bytes(int64_t T, int64_t picks, int64_t experts) {
+    return mx_expert_rows(T, picks, experts) == 0 ? 0 : align256(expert_plan_ws(T * picks, experts));
+}
+
+mx_status mx_expert_plan(const void *d_index, int index_bytes, int64_t T, int64_t picks,
+                         int64_t experts, int32_t *d_offsets, int32_t *d_counts, int32_t *d_slot,
+                         int32_t *d_source, void *d_ws, size_t ws_bytes, void *stream) {
+    TraceRange trace("mx_expert_plan");
+    if (index_bytes != 4 && index_bytes != 8) return MX_ERR_INVALID_ARG;
+    const ExpertRows r{d_slot, d_source, T, picks, mx_expert_rows(T, picks, experts), 0};
+    mx_status st = check_expert_rows(r);
+    if (st != MX_OK) return st;
+    if ((st = check_experts(experts, d_offsets)) != MX_OK) return st;
+    if (d_counts == nullptr) return MX_ERR_INVALID_ARG;
+    if (!aligned16(d_counts)) return MX_ERR_ALIGN;
+    const int64_t n = T * picks;
+    if (n > 0) {
+        if (d_index == nullptr || d_slot == nullptr || d_source == nullptr) return MX_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(d_index) & static_cast<uintptr_t>(index_bytes - 1)) != 0) return MX_ERR_ALIGN;
+        if (expert_plan_ws(n, experts) > 0) {
+            if (d_ws == nullptr || ws_bytes < mx_expert_plan_workspace_bytes(T, picks, experts)) return MX_ERR_WORKSPACE;
+            if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return MX_ERR_ALIGN;
+        }
+    }
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_expert_plan(d_index, index_bytes == 8, n, experts, r.rows, d_offsets, d_counts, d_slot,
+                                        d_source, d_ws, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_expert_dispatch(const void *d_x, int x_type, int64_t x_pitch, const int32_t *d_slot,
+                             const int32_t *d_source, int64_t T, int64_t picks, int64_t rows,
+                             int64_t K, void *d_y, int format, void *d_codes, void *d_scales,
+                             void *stream) {
+    TraceRange trace("mx_expert_dispatch");
+    if (!valid_type(x_type)) return MX_ERR_INVALID_ARG;
+    if (rows > 0 && K > 0 && d_y == nullptr && format == MX_FORMAT_NONE) return MX_ERR_INVALID_ARG;
+    const ExpertRows r{d_slot, d_source, T, picks, rows, K};
+    mx_status st = check_expert_rows(r);
+    if (st != MX_OK || (st = check_row_sizes(rows, K)) != MX_OK) return st;
+    const RowEncode e{format, d_codes, d_scales};
+    if ((st = check_row_encode(e, rows, K)) != MX_OK || rows == 0 || K == 0) return st;
+    if (d_source == nullptr || (T * picks > 0 && d_slot == nullptr)) return MX_ERR_INVALID_ARG;
+    if (K % 8 != 0 || !aligned16(d_y)) return MX_ERR_ALIGN;
+    if (T > 0 && picks > 0 && (st = check_rows(d_x, x_pitch, K)) != MX_OK) return st;
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_expert_dispatch({d_x, x_pitch, x_type == MX_TYPE_F32}, r, d_y, e, *dev,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_expert_combine(const void *d_rows, int rows_type, int64_t rows_pitch,
+                            const int32_t *d_slot, const float *d_weights, int64_t T,
+                            int64_t picks, int64_t rows, int64_t K, const void *d_res, int res_type,
+                            int64_t res_pitch, void *d_y, int y_type, void *stream) {
+    TraceRange trace("mx_expert_combine");
+    if (!valid_type(rows_type) || !valid_type(y_type)) return MX_ERR_INVALID_ARG;
+    if (d_res != nullptr && !valid_type(res_type)) return MX_ERR_INVALID_ARG;
+    const ExpertRows r{d_slot, nullptr, T, picks, rows, K};
+    mx_status st = check_expert_rows(r);
+    if (st != MX_OK || (st = check_row_sizes(rows, K)) != MX_OK || T == 0 || K == 0) return st;
+    if (d_y == nullptr || (picks > 0 && d_slot == nullptr)) return MX_ERR_INVALID_ARG;
+    if (K % 8 != 0 || !aligned16(d_y) || !aligned16(d_weights)) return MX_ERR_ALIGN;
+    if (picks > 0 && rows > 0 && (st = check_rows(d_rows, rows_pitch, K)) != MX_OK) return st;
+    if (d_res != nullptr && (st = check_rows(d_res, res_pitch, K)) != MX_OK) return st;
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_expert_combine({d_rows, rows_pitch, rows_type == MX_TYPE_F32}, r, d_weights,
+                                           {d_res, res_pitch, res_type == MX_TYPE_F32}, d_y, y_type == MX_TYPE_F32,
+                                           *dev, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_expert_combine_backward(const void *d_dy, int dy_type, int64_t dy_pitch,
+                                     const void *d_rows, int rows_type, int64_t rows_pitch,
+                                     const int32_t *d_slot, const int32_t *d_source,
+                                     const float *d_weights, int64_t T, int64_t picks, int64_t rows,
+                                     int64_t K, void *d_drows, int format, void *d_codes,
+                                     void *d_scales, float *d_dweights, void *stream) {
+    TraceRange trace("mx_expert_combine_backward");
+    if (!valid_type(dy_type) || (d_dweights != nullptr && !valid_type(rows_type))) return MX_ERR_INVALID_ARG;
+    if (rows > 0 && K > 0 && d_drows == nullptr && format == MX_FORMAT_NONE && d_dweights == nullptr)
+        return MX_ERR_INVALID_ARG;
+    const ExpertRows r{d_slot, d_source, T, picks, rows, K};
+    mx_status st = check_expert_rows(r);
+    if (st != MX_OK || (st = check_row_sizes(rows, K)) != MX_OK) return st;
+    const RowEncode e{format, d_codes, d_scales};
+    if ((st = check_row_encode(e, rows, K)) != MX_OK) return st;
+    const int64_t n = T * picks;
+    if (!aligned16(d_dweights) || !aligned16(d_weights) || !aligned16(d_drows) || K % 8 != 0) return MX_ERR_ALIGN;
+    if (K == 0 || rows == 0)
+        return d_dweights == nullptr || n == 0
+                   ? MX_OK
+                   : from_cuda(cudaMemsetAsync(d_dweights, 0, static_cast<size_t>(n) * sizeof(float),
+                                               static_cast<cudaStream_t>(stream)));
+    const bool writes = d_drows != nullptr || format != MX_FORMAT_NONE;
+    if (writes && d_source == nullptr) return MX_ERR_INVALID_ARG;
+    if (n > 0) {
+        if (d_slot == nullptr || d_weights == nullptr) return MX_ERR_INVALID_ARG;
+        if ((st = check_rows(d_dy, dy_pitch, K)) != MX_OK) return st;
+        if (d_dweights != nullptr && (st = check_rows(d_rows, rows_pitch, K)) != MX_OK) return st;
+    } else if (!writes) {
+        return MX_OK;
+    }
+    const DeviceInfo *dev = nullptr;
+    if ((st = device_or_error(&dev)) != MX_OK) return st;
+    return from_cuda(launch_expert_combine_backward({d_dy, dy_pitch, dy_type == MX_TYPE_F32},
+                                                    {d_rows, rows_pitch, rows_type == MX_TYPE_F32}, r, d_weights,
+                                                    d_drows, e, d_dweights, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_quantize_experts(const void *d_src, int64_t experts, int64_t rows, int64_t cols,
+                              int operands, int contract, int rot, int rot_block, uint64_t seed,
+                              void *d_codes, void *d_scales, void *stream) {
+    TraceRange trace("mx_quantize_experts");
+    const bool fp8 = operands == MX_FORMAT_MXFP8;
+    if (operands != MX_FORMAT_MXFP4 && !fp8) return MX_ERR_INVALID_ARG;
+    if (experts < 0) return MX_ERR_SHAPE;
+    mx_status st = check_encode(d_src, rows, cols, contract, rot, rot_block, MX_ROUND_RNE, d_codes, d_scales);
+    if (st != MX_OK || experts == 0 || rows == 0 || cols == 0) return st;
+    if (experts > MX_EXPERTS_MAX || (fp8 && (contract != MX_CONTRACT_ROWS || rot != MX_ROT_NONE)))
+        return MX_ERR_UNSUPPORTED;
+    const int64_t lines = contract == MX_CONTRACT_ROWS ? cols : rows, k = contract == MX_CONTRACT_ROWS ? rows : cols;
+    const size_t codes = fp8 ? mx_mxfp8_codes_bytes(lines, k) : mx_codes_bytes(lines, k), scales = mx_scales_bytes(lines, k);
+    if (codes % 16 != 0) return MX_ERR_ALIGN;  // the next expert's codes
+    const uint8_t *src = static_cast<const uint8_t *>(d_src);
+    uint8_t *c = static_cast<uint8_t *>(d_codes), *s = static_cast<uint8_t *>(d_scales);
+    const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+    // Whole scale groups along the rows: all experts' lines are one operand's.
+    if (contract == MX_CONTRACT_COLS && rows % 128 == 0 && experts * rows <= 0x7FFFFFFF)
+        return quantize_impl(d_src, experts * rows, cols, contract, rot, rot_block, MX_ROUND_RNE, seed, 1, c, s, st_);
+    for (int64_t e = 0; e < experts; ++e) {
+        const uint8_t *from = src + static_cast<size_t>(e) * rows * cols * 2;
+        st = fp8 ? quantize_mxfp8_impl(from, rows, cols, nullptr, 0, 0, c + e * codes, s + e * scales, nullptr, nullptr, st_)
+                 : quantize_impl(from, rows, cols, contract, rot, rot_block, MX_ROUND_RNE, seed, 1, c + e * codes,
+                                 s + e * scales, st_);
+        if (st != MX_OK) return st;
+    }
+    return MX_OK;
+}
+
+mx_status mx_gemm_experts(const void *d_Aq, const void *d_As, const void *d_Bq, const void *d_Bs,
+                          int operands, const int32_t *d_offsets, const int32_t *d_counts,
+                          int64_t experts, int64_t rows, int64_t N, int64_t K, const void *d_bias,
+                          int bias_type, int act, void *d_y, int y_type, void *d_z, int format,
+                          void *d_codes, void *d_scales, void *stream) {
+    TraceRange trace("mx_gemm_experts");
+    Product p{};
+    p.mode = kProductRows;
+    p.M = rows, p.N = N, p.K = K, p.experts = experts;
+    p.Aq = d_Aq, p.As = d_As, p.Bq = d_Bq, p.Bs = d_Bs;
+    p.offsets = d_offsets, p.counts = d_counts;
+    mx_status st = check_epilogue(p, d_bias, bias_type, act, d_y, y_type, d_z, format, d_codes, d_scales);
+    if (st != MX_OK) return st;
+    if (rows % 128 != 0) return MX_ERR_SHAPE;
+    if ((st = check_product(p, operands)) != MX_OK) return st;
+    if ((st = check_experts(experts, d_offsets)) != MX_OK) return st;
+    if (d_counts == nullptr) return MX_ERR_INVALID_ARG;
+    if (!aligned16(d_counts)) return MX_ERR_ALIGN;
+    if (rows == 0 || N == 0) return MX_OK;
+    if (experts * N > 0x7FFFFFFF) return MX_ERR_SHAPE;
+    return run_product(p, stream);
+}
+
+mx_status mx_gemm_experts_wgrad(const void *d_Aq, const void *d_As, const void *d_Bq,
+                                const void *d_Bs, int operands, const int32_t *d_offsets,
+                                int64_t experts, int64_t rows, int64_t M, int64_t N, void *d_C,
+                                int c_type, void *stream) {
+    TraceRange trace("mx_gemm_experts_wgrad");
+    return experts_wgrad_impl(d_Aq, d_As, d_Bq, d_Bs, operands, d_offsets, experts, rows, M, N, d_C, c_type, stream);
+}
+
+size_t mx_linear_experts_wgrad_workspace_bytes(int operands, int64_t rows, int64_t N, int64_t K) {
+    if (rows <= 0 || N <= 0 || K <= 0) return 0;
+    const bool fp8 = operands == MX_FORMAT_MXFP8;
+    const auto codes = [&](int64_t lines) { return fp8 ? mx_mxfp8_codes_bytes(lines, rows) : mx_codes_bytes(lines, rows); };
+    return align256(codes(N)) + align256(mx_scales_bytes(N, rows)) + align256(codes(K)) + align256(mx_scales_bytes(K, rows));
+}
+
+mx_status mx_linear_experts_wgrad(const void *d_dY, const void *d_X, int operands,
+                                  const int32_t *d_offsets, int64_t experts, int64_t rows,
+                                  int64_t N, int64_t K, int rot, int rot_block, int rnd,
+                                  uint64_t seed, void *d_dW, int dw_type, void *d_ws,
+                                  size_t ws_bytes, void *stream) {
+    TraceRange trace("mx_linear_experts_wgrad");
+    const bool fp8 = operands == MX_FORMAT_MXFP8;
+    if (operands != MX_FORMAT_MXFP4 && !fp8) return MX_ERR_INVALID_ARG;
+    if (rows < 0 || rows % 128 != 0 || N < 0 || K < 0) return MX_ERR_SHAPE;
+    if (!valid_type(dw_type)) return MX_ERR_INVALID_ARG;
+    mx_status st = check_experts(experts, d_offsets);
+    if (st != MX_OK || N == 0 || K == 0) return st;
+    if (rows == 0)
+        return experts_wgrad_impl(nullptr, nullptr, nullptr, nullptr, operands, d_offsets, experts, 0, N, K, d_dW,
+                                  dw_type, stream);
+    if ((st = check_encode(d_dY, rows, N, MX_CONTRACT_ROWS, rot, rot_block, rnd, d_dY, d_dY)) != MX_OK) return st;
+    if ((st = check_encode(d_X, rows, K, MX_CONTRACT_ROWS, rot, rot_block, rnd, d_X, d_X)) != MX_OK) return st;
+    // A rotation must not mix two experts' rows.
+    if (rot != MX_ROT_NONE && (fp8 || rot_block > 128)) return MX_ERR_UNSUPPORTED;
+    if (fp8 && rnd != MX_ROUND_RNE) return MX_ERR_UNSUPPORTED;
+    if (d_dW == nullptr) return MX_ERR_INVALID_ARG;
+    if (!aligned16(d_dW)) return MX_ERR_ALIGN;
+    if (d_ws == nullptr || ws_bytes < mx_linear_experts_wgrad_workspace_bytes(operands, rows, N, K))
+        return MX_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return MX_ERR_ALIGN;
+    const auto codes = [&](int64_t lines) { return fp8 ? mx_mxfp8_codes_bytes(lines, rows) : mx_codes_bytes(lines, rows); };
+    uint8_t *aq = static_cast<uint8_t *>(d_ws);
+    uint8_t *as = aq + align256(codes(N));
+    uint8_t *bq = as + align256(mx_scales_bytes(N, rows));
+    uint8_t *bs = bq + align256(codes(K));
+    const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+    st = fp8 ? quantize_mxfp8_impl(d_dY, rows, N, d_X, rows, K, aq, as, bq, bs, st_)
+             : quantize_pair_impl(d_dY, rows, N, d_X, rows, K, rot, rot_block, rnd, seed, aq, as, bq, bs, st_);
+    if (st != MX_OK) return st;
+    return experts_wgrad_impl(aq, as, bq, bs, operands, d_offsets, experts, rows, N, K, d_dW, dw_type, stream);
 }
 
 mx_status mx_check_status(void *stream) {

@@ -139,4 +139,50 @@ cudaError_t launch_grad_clip(const GradTensor *t, int64_t count, bool scale, flo
                              float eps, float *norm, void *ws, const DeviceInfo &dev,
                              cudaStream_t stream);
 
+// ---- products with an epilogue, and by expert (mx_product.cu)
+// dense: [M][N] = A[M] . B[N]^T; rows: A's M rows in the experts' segments, B [experts][N];
+// depth: [experts][M][N] over the experts' slices of the contraction K.
+enum : int { kProductDense = 0, kProductRows = 1, kProductDepth = 2 };
+struct Product {
+    int mode;
+    bool fp8;
+    const void *Aq, *As, *Bq, *Bs;
+    int64_t M, N, K, experts;
+    const int32_t *offsets, *counts;
+    const void *bias;
+    int bias_f32;
+    int act;
+    RowIn res;
+    void *y;
+    int y_f32;
+    void *z;
+    RowEncode enc;
+};
+cudaError_t launch_product(const Product &p, const DeviceInfo &dev, cudaStream_t stream);
+
+// ---- gradient of bias and activation (mx_act.cu)
+size_t bias_act_backward_ws(int64_t T, int64_t N);
+// z null: no activation.  dz (bf16), e and dbias may each be absent.
+cudaError_t launch_bias_act_backward(const RowIn &dy, const RowIn &z, int act, int64_t T, int64_t N, void *dz,
+                                     const RowEncode &e, float *dbias, void *ws, const DeviceInfo &dev,
+                                     cudaStream_t stream);
+
+// ---- rows by expert (mx_experts.cu)
+size_t expert_plan_ws(int64_t n, int64_t experts);
+// n entries; `rows`: capacity of all segments.
+cudaError_t launch_expert_plan(const void *index, bool wide, int64_t n, int64_t experts, int64_t rows,
+                               int32_t *offsets, int32_t *counts, int32_t *slot, int32_t *source, void *ws,
+                               const DeviceInfo &dev, cudaStream_t stream);
+struct ExpertRows {
+    const int32_t *slot, *source;
+    int64_t T, picks, rows, K;
+};
+cudaError_t launch_expert_dispatch(const RowIn &x, const ExpertRows &r, void *y, const RowEncode &e,
+                                   const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_expert_combine(const RowIn &rows, const ExpertRows &r, const float *weights, const RowIn &res,
+                                  void *y, int y_f32, const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_expert_combine_backward(const RowIn &dy, const RowIn &rows, const ExpertRows &r,
+                                           const float *weights, void *drows, const RowEncode &e, float *dweights,
+                                           const DeviceInfo &dev, cudaStream_t stream);
+
 }  // namespace mx

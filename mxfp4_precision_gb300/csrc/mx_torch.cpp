@@ -1,5 +1,5 @@
-// mx_torch.cpp -- Python entry points of the operators between the GEMMs over
-// the C ABI (include/mx.h): checks and unpacks torch tensors, allocates the
+// mx_torch.cpp -- Python entry points of the operators between the GEMMs, of the
+// products with an epilogue and of those by expert over the C ABI (include/mx.h): checks and unpacks torch tensors, allocates the
 // outputs and passes the current stream.  No arithmetic here.
 //
 // A CPython module rather than ctypes because these calls are short: a norm of
@@ -8,6 +8,7 @@
 // a tensor).
 #include <Python.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <vector>
 
@@ -138,6 +139,12 @@ struct Here {
 int64_t integer(PyObject *o) {
     const int64_t v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred() != nullptr) throw Raised{};
+    return v;
+}
+// 64 bits as they are: a seed may be a negative number or one from 2^63 on.
+uint64_t bits(PyObject *o) {
+    const uint64_t v = PyLong_AsUnsignedLongLongMask(o);
+    if (v == static_cast<uint64_t>(-1) && PyErr_Occurred() != nullptr) throw Raised{};
     return v;
 }
 float real(PyObject *o) {
@@ -346,6 +353,348 @@ PyObject *clip(PyObject *const *a) {
     return wrap(norm);
 }
 
+// ---- products with an epilogue, and by expert
+
+// An operand's codes or scales: contiguous bytes, `need` of them at least.
+void *bytes_of(PyObject *o, const char *name, size_t need) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.element_size() != 1 || !t.is_contiguous()) refuse("%s must be contiguous and of 8-bit elements", name);
+    if (t.nbytes() < need)
+        refuse("%s must hold %llu bytes, not %llu", name, static_cast<unsigned long long>(need),
+               static_cast<unsigned long long>(t.nbytes()));
+    return t.data_ptr();
+}
+int operands_of(PyObject *o) {
+    const int64_t f = integer(o);
+    if (f != MX_FORMAT_MXFP4 && f != MX_FORMAT_MXFP8) refuse("operands must be FMT_MXFP4 or FMT_MXFP8");
+    return static_cast<int>(f);
+}
+size_t codes_need(int operands, int64_t lines, int64_t k) {
+    return operands == MX_FORMAT_MXFP8 ? mx_mxfp8_codes_bytes(lines, k) : mx_codes_bytes(lines, k);
+}
+// The codes and scales at a[0..3] of A ([a_lines], k) and B (`matrices` of [b_lines], k).
+struct Operands {
+    int format;
+    void *aq, *as, *bq, *bs;
+    Operands(PyObject *const *a, PyObject *fmt, int64_t a_lines, int64_t matrices, int64_t b_lines, int64_t k)
+        : format(operands_of(fmt)) {
+        if (a_lines < 0 || b_lines < 0 || k < 0) refuse("sizes must not be negative");
+        aq = bytes_of(a[0], "Aq", codes_need(format, a_lines, k));
+        as = bytes_of(a[1], "As", mx_scales_bytes(a_lines, k));
+        bq = bytes_of(a[2], "Bq", matrices * codes_need(format, b_lines, k));
+        bs = bytes_of(a[3], "Bs", matrices * mx_scales_bytes(b_lines, k));
+    }
+};
+
+// A contiguous int32 tensor of one of a plan's parts.
+int32_t *part_of(PyObject *o, const char *name, int64_t *n = nullptr, int64_t want = -1) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kInt || !t.is_contiguous()) refuse("%s must be contiguous and int32", name);
+    if (want >= 0 && t.numel() != want) refuse("%s must have %lld elements", name, static_cast<long long>(want));
+    if (n != nullptr) *n = t.numel();
+    return static_cast<int32_t *>(t.data_ptr());
+}
+// The plan's tensors at a[0..3]: offsets, counts, slot, source.
+struct Plan {
+    int32_t *offsets, *counts, *slot, *source;
+    int64_t experts, rows, T, picks;
+    explicit Plan(PyObject *const *a) {
+        int64_t n;
+        offsets = part_of(a[0], "plan.offsets", &n);
+        experts = n - 1;
+        if (experts < 1) refuse("plan.offsets must have an element more than there are experts");
+        counts = part_of(a[1], "plan.counts", nullptr, experts);
+        slot = part_of(a[2], "plan.slot");
+        const at::Tensor &s = THPVariable_Unpack(a[2]);
+        if (s.dim() != 2) refuse("plan.slot must be [tokens, choices]");
+        T = s.size(0), picks = s.size(1);
+        source = part_of(a[3], "plan.source", &rows);
+        if (rows % 128 != 0) refuse("plan.source must have a multiple of 128 elements");
+    }
+};
+
+at::ScalarType out_type(PyObject *f32) { return truth(f32) ? at::kFloat : at::kBFloat16; }
+
+// Bias of `matrices` times [N]; none for None.
+void *bias_of(PyObject *o, int64_t matrices, int64_t N, int *type) {
+    *type = MX_TYPE_BF16;
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, "bias");
+    const bool shaped = matrices == 0 ? t.dim() == 1 && t.size(0) == N
+                                      : t.dim() == 2 && t.size(0) == matrices && t.size(1) == N;
+    if (!shaped || !t.is_contiguous())
+        refuse(matrices == 0 ? "bias must be contiguous and [N]" : "bias must be contiguous and [experts, N]");
+    *type = type_of(t, "bias");
+    return t.data_ptr();
+}
+
+// gemm_bias_act(Aq, As, Bq, Bs, M, N, K, bias, act, residual, f32, want_y, want_z, fmt, operands, out) -> (y, z, codes, scales)
+PyObject *gemm_bias_act(PyObject *const *a) {
+    const at::Tensor &like = tensor(a[0], "Aq");
+    on_device(a, {{1, "As"}, {2, "Bq"}, {3, "Bs"}, {7, "bias"}, {9, "residual"}, {15, "out"}}, like.device());
+    const Here here(like);
+    const int64_t M = integer(a[4]), N = integer(a[5]), K = integer(a[6]);
+    const Operands o(a, a[14], M, 1, N, K);
+    int bias_type;
+    void *bias = bias_of(a[7], 0, N, &bias_type);
+    Matrix res;
+    if (a[9] != Py_None) res = matrix_of(matrix(a[9], "residual"), "residual", M, N);
+    at::Tensor y, z;
+    int y_type = MX_TYPE_BF16;
+    if (a[15] != Py_None) {
+        y = tensor(a[15], "out");
+        const Matrix m = matrix_of(y, "out", M, N);
+        if (m.pitch != N) refuse("out must be contiguous");
+        y_type = m.type;
+    } else if (truth(a[11])) {
+        y = empty(like, {M, N}, out_type(a[10]));
+        y_type = type_of(y, "y");
+    }
+    if (truth(a[12])) z = empty(like, {M, N}, at::kBFloat16);
+    const EncodedRows e(like, a[13], M, N);
+    check(mx_gemm_bias_act(o.aq, o.as, o.bq, o.bs, o.format, M, N, K, bias, bias_type, static_cast<int>(integer(a[8])), res.p,
+                           res.type, res.pitch, y.defined() ? y.data_ptr() : nullptr, y_type,
+                           z.defined() ? z.data_ptr() : nullptr, e.format, e.codes_p, e.scales_p, here.stream),
+          "mx_gemm_bias_act");
+    return tuple_of(y, z, e.codes, e.scales);
+}
+
+// bias_act_backward(dy, z, act, want_dz, want_dbias, fmt, ws) -> (dz, codes, scales, dbias)
+PyObject *bias_act_backward(PyObject *const *a) {
+    const at::Tensor &dy = matrix(a[0], "dy");
+    on_device(a, {{1, "z"}, {6, "workspace"}}, dy.device());
+    const Here here(dy);
+    const int64_t T = dy.size(0), N = dy.size(1);
+    const Matrix dm = matrix_of(dy, "dy", T, N);
+    const int act = static_cast<int>(integer(a[2]));
+    Matrix zm;
+    if (a[1] != Py_None) zm = matrix_of(matrix(a[1], "z"), "z", T, N);
+    else if (act != MX_ACT_NONE) refuse("an activation's gradient needs z");
+    at::Tensor dz, dbias, ws;
+    size_t bytes = 0;
+    if (truth(a[3])) dz = empty(dy, {T, N}, at::kBFloat16);
+    const EncodedRows e(dy, a[5], T, N);
+    if (truth(a[4])) {
+        dbias = empty(dy, {N}, at::kFloat);
+        const size_t need = mx_bias_act_backward_workspace_bytes(T, N);
+        if (need > 0 || a[6] != Py_None) {
+            const Workspace given(dy, a[6], need);
+            ws = given.t;
+            bytes = given.bytes;
+        }
+    }
+    check(mx_bias_act_backward(dm.p, dm.type, dm.pitch, zm.p, zm.type, zm.pitch, act, T, N,
+                               dz.defined() ? dz.data_ptr() : nullptr, e.format, e.codes_p, e.scales_p,
+                               dbias.defined() ? static_cast<float *>(dbias.data_ptr()) : nullptr,
+                               ws.defined() ? ws.data_ptr() : nullptr, bytes, here.stream),
+          "mx_bias_act_backward");
+    return tuple_of(dz, e.codes, e.scales, dbias);
+}
+
+// expert_plan(experts, count, ws) -> (offsets, counts, slot, source)
+PyObject *expert_plan(PyObject *const *a) {
+    const at::Tensor &x = matrix(a[0], "experts");
+    on_device(a, {{2, "workspace"}}, x.device());
+    const Here here(x);
+    if ((x.scalar_type() != at::kInt && x.scalar_type() != at::kLong) || !x.is_contiguous())
+        refuse("experts must be contiguous and int32 or int64");
+    const int64_t T = x.size(0), picks = x.size(1), count = integer(a[1]);
+    if (count < 1) refuse("there must be an expert");
+    const at::Tensor offsets = empty(x, {count + 1}, at::kInt), counts = empty(x, {count}, at::kInt),
+                     slot = empty(x, {T, picks}, at::kInt), source = empty(x, {mx_expert_rows(T, picks, count)}, at::kInt);
+    at::Tensor ws;
+    size_t bytes = 0;
+    const size_t need = mx_expert_plan_workspace_bytes(T, picks, count);
+    if (need > 0 || a[2] != Py_None) {
+        const Workspace given(x, a[2], need);
+        ws = given.t;
+        bytes = given.bytes;
+    }
+    check(mx_expert_plan(x.data_ptr(), static_cast<int>(x.element_size()), T, picks, count,
+                         static_cast<int32_t *>(offsets.data_ptr()), static_cast<int32_t *>(counts.data_ptr()),
+                         static_cast<int32_t *>(slot.data_ptr()), static_cast<int32_t *>(source.data_ptr()),
+                         ws.defined() ? ws.data_ptr() : nullptr, bytes, here.stream),
+          "mx_expert_plan");
+    return tuple_of(offsets, counts, slot, source);
+}
+
+// expert_dispatch(x, offsets, counts, slot, source, fmt, want_y) -> (y, codes, scales)
+PyObject *expert_dispatch(PyObject *const *a) {
+    const at::Tensor &x = matrix(a[0], "x");
+    on_device(a, {{1, "plan.offsets"}, {2, "plan.counts"}, {3, "plan.slot"}, {4, "plan.source"}}, x.device());
+    const Here here(x);
+    const Plan plan(a + 1);
+    const int64_t K = x.size(1);
+    const Matrix m = matrix_of(x, "x", plan.T, K);
+    at::Tensor y;
+    if (truth(a[6])) y = empty(x, {plan.rows, K}, at::kBFloat16);
+    const EncodedRows e(x, a[5], plan.rows, K);
+    check(mx_expert_dispatch(m.p, m.type, m.pitch, plan.slot, plan.source, plan.T, plan.picks, plan.rows, K,
+                             y.defined() ? y.data_ptr() : nullptr, e.format, e.codes_p, e.scales_p, here.stream),
+          "mx_expert_dispatch");
+    return tuple_of(y, e.codes, e.scales);
+}
+
+const float *weights_of(PyObject *o, const Plan &plan) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, "weights");
+    if (t.scalar_type() != at::kFloat || !t.is_contiguous() || t.dim() != 2 || t.size(0) != plan.T || t.size(1) != plan.picks)
+        refuse("weights must be contiguous, float32 and [tokens, choices]");
+    return static_cast<const float *>(t.data_ptr());
+}
+
+// expert_combine(rows, offsets, counts, slot, source, weights, residual, f32, out) -> y
+PyObject *expert_combine(PyObject *const *a) {
+    const at::Tensor &rows = matrix(a[0], "rows");
+    on_device(a,
+              {{1, "plan.offsets"}, {2, "plan.counts"}, {3, "plan.slot"}, {4, "plan.source"}, {5, "weights"}, {6, "residual"}, {8, "out"}},
+              rows.device());
+    const Here here(rows);
+    const Plan plan(a + 1);
+    const int64_t K = rows.size(1);
+    const Matrix rm = matrix_of(rows, "rows", plan.rows, K);
+    const float *weights = weights_of(a[5], plan);
+    Matrix res;
+    at::ScalarType type = rows.scalar_type() == at::kFloat ? at::kFloat : at::kBFloat16;
+    if (a[6] != Py_None) {
+        const at::Tensor &r = matrix(a[6], "residual");
+        res = matrix_of(r, "residual", plan.T, K);
+        type = res.type == MX_TYPE_F32 ? at::kFloat : at::kBFloat16;
+    }
+    if (a[7] != Py_None) type = out_type(a[7]);
+    const at::Tensor y = a[8] != Py_None ? tensor(a[8], "out") : empty(rows, {plan.T, K}, type);
+    const Matrix ym = matrix_of(y, "out", plan.T, K);
+    if (ym.pitch != K) refuse("out must be contiguous");
+    check(mx_expert_combine(rm.p, rm.type, rm.pitch, plan.slot, weights, plan.T, plan.picks, plan.rows, K, res.p, res.type,
+                            res.pitch, ym.p, ym.type, here.stream),
+          "mx_expert_combine");
+    return wrap(y);
+}
+
+// expert_combine_backward(dy, rows, offsets, counts, slot, source, weights, fmt, want_y, want_dweights)
+//   -> (drows, codes, scales, dweights)
+PyObject *expert_combine_backward(PyObject *const *a) {
+    const at::Tensor &dy = matrix(a[0], "dy");
+    on_device(a, {{1, "rows"}, {2, "plan.offsets"}, {3, "plan.counts"}, {4, "plan.slot"}, {5, "plan.source"}, {6, "weights"}},
+              dy.device());
+    const Here here(dy);
+    const Plan plan(a + 2);
+    const int64_t K = dy.size(1);
+    const Matrix dm = matrix_of(dy, "dy", plan.T, K);
+    const float *weights = weights_of(a[6], plan);
+    Matrix rm;
+    at::Tensor drows, dweights;
+    if (truth(a[9])) {
+        if (a[1] == Py_None) refuse("dweights need rows");
+        rm = matrix_of(matrix(a[1], "rows"), "rows", plan.rows, K);
+        dweights = empty(dy, {plan.T, plan.picks}, at::kFloat);
+    }
+    if (weights == nullptr) refuse("weights must be a torch.Tensor");
+    if (truth(a[8])) drows = empty(dy, {plan.rows, K}, at::kBFloat16);
+    const EncodedRows e(dy, a[7], plan.rows, K);
+    check(mx_expert_combine_backward(dm.p, dm.type, dm.pitch, rm.p, rm.type, rm.pitch, plan.slot, plan.source, weights, plan.T,
+                                     plan.picks, plan.rows, K, drows.defined() ? drows.data_ptr() : nullptr, e.format,
+                                     e.codes_p, e.scales_p,
+                                     dweights.defined() ? static_cast<float *>(dweights.data_ptr()) : nullptr, here.stream),
+          "mx_expert_combine_backward");
+    return tuple_of(drows, e.codes, e.scales, dweights);
+}
+
+// quantize_experts(w, contract, operands, rot, rot_block, seed) -> (codes, scales)
+PyObject *quantize_experts(PyObject *const *a) {
+    const at::Tensor &w = tensor(a[0], "w");
+    if (w.dim() != 3 || !w.is_contiguous()) refuse("w must be contiguous and [experts, rows, columns]");
+    if (type_of(w, "w") != MX_TYPE_BF16) refuse("w must be bf16 (torch.bfloat16 or raw 16-bit patterns)");
+    const Here here(w);
+    const int64_t E = w.size(0), rows = w.size(1), cols = w.size(2), contract = integer(a[1]);
+    const int operands = operands_of(a[2]);
+    const int64_t lines = contract == MX_CONTRACT_ROWS ? cols : rows, k = contract == MX_CONTRACT_ROWS ? rows : cols;
+    const int64_t row_bytes = operands == MX_FORMAT_MXFP8 ? k : k / 2;
+    const at::Tensor codes = empty(w, {E * lines, row_bytes}, at::kByte),
+                     scales = empty(w, {std::max<int64_t>(1, E * static_cast<int64_t>(mx_scales_bytes(lines, k)))}, at::kByte);
+    check(mx_quantize_experts(w.data_ptr(), E, rows, cols, operands, static_cast<int>(contract), static_cast<int>(integer(a[3])),
+                              static_cast<int>(integer(a[4])), bits(a[5]), codes.data_ptr(),
+                              scales.data_ptr(), here.stream),
+          "mx_quantize_experts");
+    return tuple_of(codes, scales);
+}
+
+// gemm_experts(Aq, As, Bq, Bs, offsets, counts, slot, source, N, K, bias, act, f32, want_y, want_z, fmt, operands)
+//   -> (y, z, codes, scales)
+PyObject *gemm_experts(PyObject *const *a) {
+    const at::Tensor &like = tensor(a[0], "Aq");
+    on_device(a,
+              {{1, "As"}, {2, "Bq"}, {3, "Bs"}, {4, "plan.offsets"}, {5, "plan.counts"}, {6, "plan.slot"}, {7, "plan.source"}, {10, "bias"}},
+              like.device());
+    const Here here(like);
+    const Plan plan(a + 4);
+    const int64_t N = integer(a[8]), K = integer(a[9]);
+    const Operands o(a, a[16], plan.rows, plan.experts, N, K);
+    int bias_type;
+    void *bias = bias_of(a[10], plan.experts, N, &bias_type);
+    at::Tensor y, z;
+    const at::ScalarType type = out_type(a[12]);
+    if (truth(a[13])) y = empty(like, {plan.rows, N}, type);
+    if (truth(a[14])) z = empty(like, {plan.rows, N}, at::kBFloat16);
+    const EncodedRows e(like, a[15], plan.rows, N);
+    check(mx_gemm_experts(o.aq, o.as, o.bq, o.bs, o.format, plan.offsets, plan.counts, plan.experts, plan.rows, N, K, bias,
+                          bias_type, static_cast<int>(integer(a[11])), y.defined() ? y.data_ptr() : nullptr,
+                          type == at::kFloat ? MX_TYPE_F32 : MX_TYPE_BF16, z.defined() ? z.data_ptr() : nullptr, e.format,
+                          e.codes_p, e.scales_p, here.stream),
+          "mx_gemm_experts");
+    return tuple_of(y, z, e.codes, e.scales);
+}
+
+// An output [experts, M, N] of either type: the one given, or a new one.
+at::Tensor stack_of(PyObject *given, const at::Tensor &like, at::ScalarType type, int64_t E, int64_t M, int64_t N) {
+    if (given == Py_None) return empty(like, {E, M, N}, type);
+    const at::Tensor &t = tensor(given, "out");
+    if (t.dim() != 3 || t.size(0) != E || t.size(1) != M || t.size(2) != N || !t.is_contiguous())
+        refuse("out must be contiguous and [%lld, %lld, %lld]", static_cast<long long>(E), static_cast<long long>(M),
+               static_cast<long long>(N));
+    return t;
+}
+
+// gemm_experts_wgrad(Aq, As, Bq, Bs, offsets, counts, slot, source, M, N, f32, operands, out) -> C
+PyObject *gemm_experts_wgrad(PyObject *const *a) {
+    const at::Tensor &like = tensor(a[0], "Aq");
+    on_device(a,
+              {{1, "As"}, {2, "Bq"}, {3, "Bs"}, {4, "plan.offsets"}, {5, "plan.counts"}, {6, "plan.slot"}, {7, "plan.source"}, {12, "out"}},
+              like.device());
+    const Here here(like);
+    const Plan plan(a + 4);
+    const int64_t M = integer(a[8]), N = integer(a[9]);
+    const Operands o(a, a[11], M, 1, N, plan.rows);
+    const at::Tensor c = stack_of(a[12], like, out_type(a[10]), plan.experts, M, N);
+    check(mx_gemm_experts_wgrad(o.aq, o.as, o.bq, o.bs, o.format, plan.offsets, plan.experts, plan.rows, M, N, c.data_ptr(),
+                                type_of(c, "out"), here.stream),
+          "mx_gemm_experts_wgrad");
+    return wrap(c);
+}
+
+// linear_experts_wgrad(dY, X, offsets, counts, slot, source, operands, rot, rot_block, rnd, seed, f32, ws, out) -> dW
+PyObject *linear_experts_wgrad(PyObject *const *a) {
+    const at::Tensor &dY = matrix(a[0], "dY"), &X = matrix(a[1], "X");
+    on_device(a,
+              {{1, "X"}, {2, "plan.offsets"}, {3, "plan.counts"}, {4, "plan.slot"}, {5, "plan.source"}, {12, "workspace"}, {13, "out"}},
+              dY.device());
+    const Here here(dY);
+    const Plan plan(a + 2);
+    const int64_t N = dY.size(1), K = X.size(1);
+    const Matrix dm = matrix_of(dY, "dY", plan.rows, N), xm = matrix_of(X, "X", plan.rows, K);
+    if (dm.type != MX_TYPE_BF16 || xm.type != MX_TYPE_BF16 || dm.pitch != N || xm.pitch != K)
+        refuse("dY and X must be contiguous and bf16 (torch.bfloat16 or raw 16-bit patterns)");
+    const int operands = operands_of(a[6]);
+    const at::Tensor dW = stack_of(a[13], dY, out_type(a[11]), plan.experts, N, K);
+    const Workspace ws(dY, a[12], mx_linear_experts_wgrad_workspace_bytes(operands, plan.rows, N, K));
+    check(mx_linear_experts_wgrad(dm.p, xm.p, operands, plan.offsets, plan.experts, plan.rows, N, K,
+                                  static_cast<int>(integer(a[7])), static_cast<int>(integer(a[8])),
+                                  static_cast<int>(integer(a[9])), bits(a[10]), dW.data_ptr(),
+                                  type_of(dW, "out"), ws.t.data_ptr(), ws.bytes, here.stream),
+          "mx_linear_experts_wgrad");
+    return wrap(dW);
+}
+
 // Argument count, and C++ exceptions turned into Python's (torch's own by its rules).
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -377,6 +726,16 @@ PyMethodDef g_methods[] = {method<rmsnorm, 7>("rmsnorm"),
                            method<swiglu, 3>("swiglu"),
                            method<swiglu_backward, 3>("swiglu_backward"),
                            method<clip, 6>("clip"),
+                           method<gemm_bias_act, 16>("gemm_bias_act"),
+                           method<bias_act_backward, 7>("bias_act_backward"),
+                           method<expert_plan, 3>("expert_plan"),
+                           method<expert_dispatch, 7>("expert_dispatch"),
+                           method<expert_combine, 9>("expert_combine"),
+                           method<expert_combine_backward, 10>("expert_combine_backward"),
+                           method<quantize_experts, 6>("quantize_experts"),
+                           method<gemm_experts, 17>("gemm_experts"),
+                           method<gemm_experts_wgrad, 13>("gemm_experts_wgrad"),
+                           method<linear_experts_wgrad, 14>("linear_experts_wgrad"),
                            {"set_check", set_check, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "mx_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
