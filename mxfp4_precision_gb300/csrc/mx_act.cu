@@ -42,9 +42,9 @@ struct ActGradArgs {
 };
 
 template <int ACT>
-__device__ __forceinline__ void slopes(const float (&z)[8], float (&d)[8]) {
+__device__ __forceinline__ void slopes(const V8 &z, V8 &d) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] *= act::slope<ACT>(z[i]);
+    for (int i = 0; i < 4; ++i) d.v[i] = mul2(d.v[i], act::slope2<ACT>(z.v[i]));
 }
 
 template <typename D, typename Z, int WARPS>
@@ -83,23 +83,18 @@ __global__ void __launch_bounds__(32 * WARPS) mx_bias_act_backward_kernel(const 
         for (int k = 0; k < kAhead; ++k) {
             const int64_t r = row + k * WARPS;
             if (r >= end) break;
-            float d[8], x[8];
-            floats_of(to_v8(dr[k]), d);
-            floats_of(to_v8(zr[k]), x);
+            V8 g = to_v8(dr[k]);
+            const V8 x = to_v8(zr[k]);
             switch (p.act) {
-                case act::kRelu: slopes<act::kRelu>(x, d); break;
-                case act::kRelu2: slopes<act::kRelu2>(x, d); break;
-                case act::kGelu: slopes<act::kGelu>(x, d); break;
-                case act::kGeluTanh: slopes<act::kGeluTanh>(x, d); break;
-                case act::kSilu: slopes<act::kSilu>(x, d); break;
+                case act::kRelu: slopes<act::kRelu>(x, g); break;
+                case act::kRelu2: slopes<act::kRelu2>(x, g); break;
+                case act::kGelu: slopes<act::kGelu>(x, g); break;
+                case act::kGeluTanh: slopes<act::kGeluTanh>(x, g); break;
+                case act::kSilu: slopes<act::kSilu>(x, g); break;
                 default: break;
             }
-            V8 g;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                g.v[i] = pack2(d[2 * i], d[2 * i + 1]);
-                sum.v[i] = add2(sum.v[i], g.v[i]);
-            }
+            for (int i = 0; i < 4; ++i) sum.v[i] = add2(sum.v[i], g.v[i]);
             if (in && p.dz.p != nullptr) store8<BF16>(p.dz, p.dz.p + (r * p.N + col) * 2, g, true, p.status);
             if (p.enc.fmt != kEncNone && c < p.enc.katoms * 16)
                 encode8(p.enc, encoded_row(p.enc, r), c, in, g, p.status);

@@ -1,32 +1,48 @@
 // mx_act.cuh -- the activations of a product's epilogue and their derivatives,
-// in fp32 (u = 2^-24).
+// in fp32 (u = 2^-24), two columns at a time (the f32x2 instructions round each
+// half like the scalar ones, at half the issue slots).
 //
-// All but ReLU's need one 2^x and one reciprocal (the hardware's, within 2 and
-// 1 units in the last place), taken of -|x| so that neither leaves fp32's range:
-//   s(t) = 1 / (1 + 2^-t):  e = 2^-|t|, r = 1 / (1 + e);  t >= 0: r, else e r;
-//                           s (1 - s) = e r^2, without a difference that cancels
-//   silu        x s(x log2 e)
-//   gelu_tanh   x s(t), t = 2 sqrt(2/pi) log2 e (x + 0.044715 x^3):
+// silu, gelu_tanh and gelu are x less the part that a factor 1 - h takes away, with h
+// of |x| so that nothing leaves fp32's range or cancels:
+//   act(x) = x [x > 0] - |x| h(|x|)
+//   silu        h = e r,  e = 2^(-|x| log2 e),  r = 1 / (1 + e)     (1 - h = r)
+//   gelu_tanh   the same with e = 2^-t, t = 2 sqrt(2/pi) log2 e (|x| + 0.044715 |x|^3):
 //               (1 + tanh(a)) / 2 = 1 / (1 + exp(-2a))
-//   gelu        x Phi(x);  Phi(-|x|) = erfcx(|x| / sqrt 2) / 2 exp(-x^2 / 2)
-// with erfcx(w) = exp(w^2) erfc(w) by a polynomial of degree 9 in
-// 1 / (1 + 0.3 w), fitted here by reweighted least squares to a relative 3.7e-8 over
-// 0 <= w <= 10.5, where exp(-w^2) has left fp32's range.  Phi is within 4 u absolutely;
-// relatively within (8 + 3 x^2) u below 0 (the exponent's rounding), so that small
-// values of the left tail keep their digits, which 1 + erf(x / sqrt 2) loses.
-// Infinities and NaN give what the formulas give (x = -Inf: -Inf * 0 = NaN).
+//   gelu        h = Phi(-|x|) = erfcx(|x| / sqrt 2) / 2 * e,  e = exp(-x^2 / 2)
+// one 2^x and one reciprocal each (the hardware's, within 2 and 1 units in the last
+// place).  2^y is the square of 2^(y/2), which keeps values below fp32's normal range.
+// erfcx(w) = exp(w^2) erfc(w) is a polynomial of degree 9 in 1 / (1 + 0.3 w),
+// fitted here by reweighted least squares to a relative 3.7e-8 over 0 <= w <= 10.5,
+// where exp(-w^2) has left fp32's range.  h is relatively within (12 + 3 x^2) u (the
+// exponent's rounding), so small values of the left tail keep their digits, which
+// 1 + erf(x / sqrt 2) loses.  |x| is held to 32 inside h, which is below fp32's range from there
+// on (silu: to 128).  x = -Inf gives the formulas' -Inf * 0 = NaN.
 #pragma once
 
+#include <cstdint>
 #include <cuda_runtime.h>
+
+#include "mx_encode.cuh"
 
 namespace mx {
 namespace act {
 
 enum : int { kNone = 0, kRelu = 1, kRelu2 = 2, kGelu = 3, kGeluTanh = 4, kSilu = 5 };
 
+using enc::add2;
+using enc::mul2;
+using enc::pack2;
+using enc::unpack2;
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t same2(float v) { return pack2(v, v); }
+
 __device__ __forceinline__ float exp2_of(float x) {
     float e;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
     return e;
 }
 __device__ __forceinline__ float reciprocal(float x) {
@@ -40,74 +56,115 @@ __device__ __forceinline__ float positive(float x) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(0.0f));
     return r;
 }
-
-// s(t) and s (1 - s).
-struct Sigmoid {
-    float s, slope;
-};
-__device__ __forceinline__ Sigmoid sigmoid(float t) {
-    const float e = exp2_of(-fabsf(t)), r = reciprocal(1.0f + e), er = e * r;
-    return {t < 0.0f ? er : r, er * r};
+// 1 where x > 0, else 0.
+__device__ __forceinline__ float step(float x) {
+    float r;
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(0.0f));
+    return r;
 }
-
-// Phi(x) and exp(-x^2 / 2).
-struct Normal {
-    float below, e;
-};
-__device__ __forceinline__ Normal normal(float x) {
-    const float t = reciprocal(fmaf(fabsf(x), 0x1.b27248p-3f, 1.0f));  // 0.3 / sqrt 2
-    float p = -0x1.05624cp-4f;
-    p = fmaf(p, t, 0x1.e673e6p-3f);
-    p = fmaf(p, t, -0x1.f29f92p-3f);
-    p = fmaf(p, t, 0x1.06a07ep-2f);
-    p = fmaf(p, t, -0x1.093d10p-5f);
-    p = fmaf(p, t, 0x1.960778p-4f);
-    p = fmaf(p, t, 0x1.3c2144p-4f);
-    p = fmaf(p, t, 0x1.5ad880p-4f);
-    p = fmaf(p, t, 0x1.5ad9f0p-4f);
-    p = fmaf(p, t, -0x1.3ec9bep-18f);
-    const float e = exp2_of(x * x * -0x1.715476p-1f);  // log2 e / 2
-    const float h = p * e;
-    return {x < 0.0f ? h : 1.0f - h, e};
+__device__ __forceinline__ uint64_t step2(uint64_t x) {
+    float a, b;
+    unpack2(x, a, b);
+    return pack2(step(a), step(b));
+}
+// max(-|x|, -most); -most for NaN.
+__device__ __forceinline__ uint64_t bounded2(uint64_t x, float most) {
+    float a, b;
+    unpack2(x, a, b);
+    return pack2(fmaxf(-fabsf(a), -most), fmaxf(-fabsf(b), -most));
+}
+// 2^(2 y).
+__device__ __forceinline__ uint64_t exp2_twice2(uint64_t y) {
+    float a, b;
+    unpack2(y, a, b);
+    const uint64_t e = pack2(exp2_of(a), exp2_of(b));
+    return mul2(e, e);
+}
+__device__ __forceinline__ uint64_t reciprocal2(uint64_t x) {
+    float a, b;
+    unpack2(x, a, b);
+    return pack2(reciprocal(a), reciprocal(b));
 }
 
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr float kTanh = 1.5957691216f;  // 2 sqrt(2/pi)
 constexpr float kCubic = 0.044715f;
 
+// Of n = -|x|: h, and what its derivative needs (logistic forms: r; gelu: exp(-x^2 / 2)).
+struct Part {
+    uint64_t h, more;
+};
 template <int ACT>
-__device__ __forceinline__ float value(float x) {
-    if constexpr (ACT == kRelu) return positive(x);
-    if constexpr (ACT == kRelu2) {
-        const float p = positive(x);
-        return p * p;
+__device__ __forceinline__ Part part2(uint64_t n) {
+    if constexpr (ACT == kGelu) {
+        const uint64_t t = reciprocal2(fma2(n, same2(-0x1.b27248p-3f), same2(1.0f)));  // 0.3 / sqrt 2
+        uint64_t p = same2(-0x1.05624cp-4f);
+        p = fma2(p, t, same2(0x1.e673e6p-3f));
+        p = fma2(p, t, same2(-0x1.f29f92p-3f));
+        p = fma2(p, t, same2(0x1.06a07ep-2f));
+        p = fma2(p, t, same2(-0x1.093d10p-5f));
+        p = fma2(p, t, same2(0x1.960778p-4f));
+        p = fma2(p, t, same2(0x1.3c2144p-4f));
+        p = fma2(p, t, same2(0x1.5ad880p-4f));
+        p = fma2(p, t, same2(0x1.5ad9f0p-4f));
+        p = fma2(p, t, same2(-0x1.3ec9bep-18f));
+        const uint64_t e = exp2_twice2(mul2(mul2(n, n), same2(-0.25f * kLog2e)));
+        return {mul2(p, e), e};
+    } else {
+        uint64_t y;
+        if constexpr (ACT == kGeluTanh)
+            y = mul2(n, fma2(mul2(n, n), same2(0.5f * kTanh * kCubic * kLog2e), same2(0.5f * kTanh * kLog2e)));
+        else
+            y = mul2(n, same2(0.5f * kLog2e));
+        const uint64_t e = exp2_twice2(y), r = reciprocal2(add2(e, same2(1.0f)));
+        return {mul2(e, r), r};
     }
-    if constexpr (ACT == kGelu) return x * normal(x).below;
-    if constexpr (ACT == kGeluTanh)
-        return x * sigmoid(x * fmaf(x * x, kTanh * kCubic * kLog2e, kTanh * kLog2e)).s;
-    if constexpr (ACT == kSilu) return x * sigmoid(x * kLog2e).s;
-    return x;
+}
+template <int ACT>
+__device__ __forceinline__ constexpr float most() {
+    return ACT == kSilu ? 128.0f : 32.0f;
 }
 
+// act(x) of two columns.
 template <int ACT>
-__device__ __forceinline__ float slope(float x) {
-    if constexpr (ACT == kRelu) return x > 0.0f ? 1.0f : 0.0f;
-    if constexpr (ACT == kRelu2) return 2.0f * positive(x);
-    if constexpr (ACT == kGelu) {
-        const Normal n = normal(x);
-        return fmaf(x * n.e, 0.3989422804f, n.below);  // 1 / sqrt(2 pi)
+__device__ __forceinline__ uint64_t value2(uint64_t x) {
+    if constexpr (ACT == kRelu || ACT == kRelu2) {
+        float a, b;
+        unpack2(x, a, b);
+        const uint64_t p = pack2(positive(a), positive(b));
+        return ACT == kRelu ? p : mul2(p, p);
+    } else if constexpr (ACT == kNone) {
+        return x;
+    } else {
+        const uint64_t n = bounded2(x, most<ACT>());
+        return fma2(x, step2(x), mul2(n, part2<ACT>(n).h));
     }
-    if constexpr (ACT == kGeluTanh) {
-        // Beyond |x| = 10^4 the slope of s is 0; the bound keeps x^2 from making 0 * Inf of it.
-        const float x2 = fminf(x * x, 1e8f);
-        const Sigmoid q = sigmoid(x * fmaf(x2, kTanh * kCubic * kLog2e, kTanh * kLog2e));
-        return fmaf(x * q.slope, fmaf(x2, 3.0f * kTanh * kCubic, kTanh), q.s);
+}
+
+// act'(x) of two columns: s' = s + x s (1 - s) c for the logistic forms, s = [x > 0] + sign h;
+// Phi(x) + x phi(x) for gelu.  h and the second term are even and odd in x.
+template <int ACT>
+__device__ __forceinline__ uint64_t slope2(uint64_t x) {
+    if constexpr (ACT == kRelu) return step2(x);
+    if constexpr (ACT == kRelu2) {
+        float a, b;
+        unpack2(x, a, b);
+        return mul2(same2(2.0f), pack2(positive(a), positive(b)));
     }
-    if constexpr (ACT == kSilu) {
-        const Sigmoid q = sigmoid(x * kLog2e);
-        return fmaf(x, q.slope, q.s);
-    }
-    return 1.0f;
+    if constexpr (ACT == kNone) return same2(1.0f);
+    const uint64_t n = bounded2(x, most<ACT>());
+    const Part q = part2<ACT>(n);
+    uint64_t low;  // the slope at -|x|: h - |x| (-h')
+    if constexpr (ACT == kGelu) low = fma2(mul2(n, q.more), same2(0.3989422804f), q.h);  // 1 / sqrt(2 pi)
+    else if constexpr (ACT == kSilu) low = fma2(n, mul2(q.h, q.more), q.h);
+    else low = fma2(mul2(n, mul2(q.h, q.more)), fma2(mul2(n, n), same2(3.0f * kTanh * kCubic), same2(kTanh)), q.h);
+    float u, v, xa, xb;
+    unpack2(low, u, v);
+    unpack2(x, xa, xb);
+    // x > 0: 1 - low; NaN stays NaN.
+    u = xa > 0.0f ? 1.0f - u : xa <= 0.0f ? u : xa;
+    v = xb > 0.0f ? 1.0f - v : xb <= 0.0f ? v : xb;
+    return pack2(u, v);
 }
 
 }  // namespace act

@@ -50,12 +50,14 @@ constexpr int kKSub = 2;                          // sub-tiles per stage
 constexpr int kStages = 3;
 constexpr int kSFRing = kStages + 2;
 constexpr int kWriterWarp0 = 4;                   // warps 4..7: scale writers
-constexpr int kEpiWarp0 = 8;                      // warps 8..15: epilogue
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 512;
-constexpr int kLaunchRegs = 128;
-constexpr int kRegsLow = 56, kRegsHigh = 200;
-static_assert(256 * (kRegsLow + kRegsHigh) <= kThreads * kLaunchRegs, "register split fits the launch");
+constexpr int kEpiWarp0 = 8;                      // warps 8..23: epilogue
+constexpr int kEpiWarps = 16;
+constexpr int kEpiCols = 64;                      // columns of an epilogue warp
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kLaunchRegs = 80;
+constexpr int kRegsLow = 48, kRegsHigh = 96;
+static_assert(32 * (kEpiWarp0 * kRegsLow + kEpiWarps * kRegsHigh) <= kThreads * kLaunchRegs, "register split fits the launch");
+static_assert(kThreads * kLaunchRegs <= 65536, "launch registers fit the SM");
 constexpr uint32_t kSubBytes = kHalf * kBKBytes;  // 16 KB: 128 rows x one K sub-tile
 constexpr uint32_t kStageBytes = 2 * kKSub * kSubBytes;
 constexpr uint32_t kOffB = kKSub * kSubBytes;
@@ -79,6 +81,20 @@ struct Elem {
 
 enum : int { kDense = 0, kRows = 1, kDepth = 2 };
 
+// n / d for 0 <= n < 2^31 as a multiplication: with 2^(l-1) < d <= 2^l, m = floor(2^(31+l) / d) + 1
+// fits 32 bits, and n m / 2^(31+l) is above n / d by less than n / 2^(31+l) <= 1 / d.
+struct Divisor {
+    uint32_t m, shift, d;
+};
+inline Divisor divisor(int64_t d) {
+    uint32_t l = 0;
+    while ((int64_t{1} << l) < d) ++l;
+    return {static_cast<uint32_t>((uint64_t{1} << (31 + l)) / static_cast<uint64_t>(d) + 1), 31 + l, static_cast<uint32_t>(d)};
+}
+__device__ __forceinline__ int divide(int n, const Divisor &d) {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.m) >> d.shift);
+}
+
 struct ProductArgs {
     const uint8_t *As, *Bs;
     int64_t M, N;            // rows: M is the capacity of all segments; depth: per expert
@@ -86,6 +102,7 @@ struct ProductArgs {
     int64_t a_groups, b_groups;  // 128-line scale groups of A, and of B (per expert in `rows`)
     int k_units;             // contraction in units of 128 elements (depth: of all experts)
     int m_tiles, n_tiles;    // per expert in `depth`
+    Divisor by_n, by_band, by_last, by_expert;  // n_tiles, a band's tiles, the last band's rows, an expert's tiles (depth)
     int num_items;           // dense, depth
     int experts;
     const int32_t *offsets;  // [experts + 1] rows
@@ -98,7 +115,7 @@ struct ProductArgs {
     size_t y_bytes, z_bytes, codes_bytes, scales_bytes;
     int64_t out_katoms;
     int act, bias_f32, res_f32, y_f32, fmt;
-    int wide;                // y's and z's rows allow 32-byte stores
+    int wide, wide_codes;    // y's and z's rows, and codes, allow 32-byte stores
     int *status;
 };
 
@@ -112,12 +129,11 @@ struct SharedCtl {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
-    int issued;                  // stages whose operand loads this CTA has issued (monotonic)
     uint32_t warp_tiles[kThreads / 32];
     int start[MX_EXPERTS_MAX + 1];              // segments' first rows in units of 128
     uint16_t tiles_before[MX_EXPERTS_MAX + 1];  // tile rows of the experts before (rows)
 };
-static_assert(MX_EXPERTS_MAX <= kThreads, "one thread per expert in the set-up");
+static_assert(MX_EXPERTS_MAX < kThreads, "one thread per expert in the set-up");
 
 constexpr size_t kSmem = kStages * kStageBytes + kSFRing * kSFSlotBytes + sizeof(SharedCtl) + 1024;
 static_assert(kSmem <= 232448, "shared memory of an SM");
@@ -134,14 +150,13 @@ struct Tile {
     int m_left;                // rows of the expert's segment from `row` on (padding included)
 };
 
-template <int MODE>
-__device__ __forceinline__ void band_coords(int t, int m_tiles, int n_tiles, int &mb, int &nb) {
-    const int per_band = kBand * n_tiles;
-    const int band = t / per_band, r = t - band * per_band;
-    const int first = band * kBand;
-    const int rows = m_tiles - first < kBand ? m_tiles - first : kBand;
-    nb = r / rows;
-    mb = first + r - nb * rows;
+// Tile t of m_tiles x n_tiles: bands of kBand tile rows, column by column within a band.
+// by_last: the last band's rows (0: not known, an ordinary division).
+__device__ __forceinline__ void band_coords(const ProductArgs &g, int t, int m_tiles, const Divisor *by_last, int &mb, int &nb) {
+    const int band = divide(t, g.by_band), r = t - band * kBand * g.n_tiles;
+    const int first = band * kBand, rows = m_tiles - first;
+    nb = rows >= kBand ? r / kBand : by_last != nullptr ? divide(r, *by_last) : r / rows;
+    mb = first + r - nb * (rows >= kBand ? kBand : rows);
 }
 
 template <int MODE>
@@ -152,14 +167,14 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs &g, const SharedCtl *c
     w.units = g.k_units;
     w.expert = 0;
     if constexpr (MODE == kDense) {
-        band_coords<MODE>(t, g.m_tiles, g.n_tiles, mb, nb);
+        band_coords(g, t, g.m_tiles, &g.by_last, mb, nb);
         w.row = mb * kTile;
         w.b_row = nb * kTile;
         w.b_group = 2 * static_cast<int64_t>(nb);
         w.m_left = static_cast<int>(g.M - w.row);
     } else if constexpr (MODE == kRows) {
         // The last expert whose tiles begin at or before t (experts without rows have none).
-        const int tm = t / g.n_tiles;
+        const int tm = divide(t, g.by_n);
         int lo = 0, hi = g.experts - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -167,16 +182,15 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs &g, const SharedCtl *c
             else hi = mid - 1;
         }
         const int before = ctl->tiles_before[lo];
-        band_coords<MODE>(t - before * g.n_tiles, ctl->tiles_before[lo + 1] - before, g.n_tiles, mb, nb);
+        band_coords(g, t - before * g.n_tiles, ctl->tiles_before[lo + 1] - before, nullptr, mb, nb);
         w.expert = lo;
         w.row = ctl->start[lo] * 128 + mb * kTile;
         w.m_left = ctl->start[lo + 1] * 128 - w.row;
         w.b_row = lo * static_cast<int>(g.N) + nb * kTile;
         w.b_group = static_cast<int64_t>(lo) * g.b_groups + 2 * nb;
     } else {
-        const int per = g.m_tiles * g.n_tiles;
-        w.expert = t / per;
-        band_coords<MODE>(t - w.expert * per, g.m_tiles, g.n_tiles, mb, nb);
+        w.expert = divide(t, g.by_expert);
+        band_coords(g, t - w.expert * static_cast<int>(g.by_expert.d), g.m_tiles, &g.by_last, mb, nb);
         w.unit0 = ctl->start[w.expert];
         w.units = max(0, ctl->start[w.expert + 1] - w.unit0);
         w.row = mb * kTile;
@@ -206,10 +220,6 @@ __device__ __forceinline__ int read_segments(const ProductArgs &g, SharedCtl *ct
         const int s = g.offsets[e] >> 7;
         ctl->start[e] = s < 0 ? 0 : s > limit ? limit : s;
     }
-    if (e == 0 && g.experts == kThreads) {
-        const int s = g.offsets[kThreads] >> 7;
-        ctl->start[kThreads] = s < 0 ? 0 : s > limit ? limit : s;
-    }
     __syncthreads();
     if constexpr (MODE == kDepth) return g.num_items;
     const int lane = e & 31, warp = e >> 5;
@@ -238,28 +248,6 @@ __device__ __forceinline__ void arrive_even(uint64_t *bar) {
     mbar_arrive_remote(mapa_shared(smem_u32(bar), 0u));
 }
 
-// Bounded wait until this CTA's producer has issued at least `target` stages.
-__device__ __forceinline__ bool wait_issued(const SharedCtl *ctl, int target, int *status,
-                                            volatile int *abort) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) {
-        const volatile int *issued = &ctl->issued;
-        if (*issued < target) {
-            const uint64_t t0 = global_timer_ns();
-            while (*issued < target) {
-                if (*abort || global_timer_ns() - t0 > kWaitLimitNs) {
-                    if (!*abort) atomicExch(status, kDevTimeout);
-                    *abort = 1;
-                    ok = 0;
-                    break;
-                }
-                __nanosleep(64);
-            }
-        }
-    }
-    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-}
-
 // Outputs are written once and not read here: past L1, first to leave L2.
 __device__ __forceinline__ void st_out32(void *p, const uint32_t *v) {
     asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
@@ -271,36 +259,48 @@ __device__ __forceinline__ void st_out16(void *p, const uint32_t *v) {
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
+    float lo, hi;
+    enc::unpack2(v, lo, hi);
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-// 32 columns from p (columns c .. c + 31 of a row of N) in bf16 or fp32.  N is a multiple of 8.
-__device__ __forceinline__ void store_bf16(uint8_t *p, const uint8_t *base, size_t bytes, const float (&v)[32], int left,
-                                           bool wide, int *status) {
+// 32 columns of a row, as 16 packed fp32 pairs.
+struct Row32 {
+    uint64_t v[16];
+};
+
+// To p (columns c .. c + 31 of a row of N, the first `cols` of them inside it; nothing where the
+// lane's row is not stored) in bf16 or fp32.  N is a multiple of 8; cols is the warp's.
+__device__ __forceinline__ void store_bf16(uint8_t *p, const uint8_t *base, size_t bytes, const Row32 &a, int cols,
+                                           bool stored, bool wide, int *status) {
     uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-    if (wide && left >= 32) {
+    for (int i = 0; i < 16; ++i) w[i] = bf16_pair(a.v[i]);
+    if (wide && cols >= 32) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (MX_STORE_OK(p + 32 * i, 32, base, bytes, status)) st_out32(p + 32 * i, &w[8 * i]);
+            if (stored && MX_STORE_OK(p + 32 * i, 32, base, bytes, status)) st_out32(p + 32 * i, &w[8 * i]);
         return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (8 * i < left && MX_STORE_OK(p + 16 * i, 16, base, bytes, status)) st_out16(p + 16 * i, &w[4 * i]);
+        if (stored && 8 * i < cols && MX_STORE_OK(p + 16 * i, 16, base, bytes, status)) st_out16(p + 16 * i, &w[4 * i]);
 }
-__device__ __forceinline__ void store_f32(uint8_t *p, const uint8_t *base, size_t bytes, const float (&v)[32], int left,
-                                          bool wide, int *status) {
+__device__ __forceinline__ void store_f32(uint8_t *p, const uint8_t *base, size_t bytes, const Row32 &a, int cols,
+                                          bool stored, bool wide, int *status) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (8 * i >= left || !MX_STORE_OK(p + 32 * i, 32, base, bytes, status)) continue;
+        if (!stored || 8 * i >= cols || !MX_STORE_OK(p + 32 * i, 32, base, bytes, status)) continue;
         uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * i + k]);
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            enc::unpack2(a.v[4 * i + k], lo, hi);
+            w[2 * k] = __float_as_uint(lo), w[2 * k + 1] = __float_as_uint(hi);
+        }
         if (wide) {
             st_out32(p + 32 * i, w);
         } else {
@@ -310,104 +310,146 @@ __device__ __forceinline__ void store_f32(uint8_t *p, const uint8_t *base, size_
     }
 }
 
-// Adds 32 columns of a bf16 or fp32 row (16-byte aligned) to v.
-__device__ __forceinline__ void add_row(float (&v)[32], const uint8_t *p, bool f32, int left) {
+// Adds 32 columns of a bf16 or fp32 row (16-byte aligned).
+__device__ __forceinline__ void add_row(Row32 &a, const uint8_t *p, bool f32, int cols) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (8 * i >= left) break;
+        if (8 * i >= cols) break;
         if (f32) {
-            const float4 a = *reinterpret_cast<const float4 *>(p + 32 * i);
-            const float4 b = *reinterpret_cast<const float4 *>(p + 32 * i + 16);
-            v[8 * i] += a.x, v[8 * i + 1] += a.y, v[8 * i + 2] += a.z, v[8 * i + 3] += a.w;
-            v[8 * i + 4] += b.x, v[8 * i + 5] += b.y, v[8 * i + 6] += b.z, v[8 * i + 7] += b.w;
+            const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(p + 32 * i);
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2 *>(p + 32 * i + 16);
+            a.v[4 * i] = enc::add2(a.v[4 * i], s.x), a.v[4 * i + 1] = enc::add2(a.v[4 * i + 1], s.y);
+            a.v[4 * i + 2] = enc::add2(a.v[4 * i + 2], t.x), a.v[4 * i + 3] = enc::add2(a.v[4 * i + 3], t.y);
         } else {
-            const uint4 a = *reinterpret_cast<const uint4 *>(p + 16 * i);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            const uint4 s = *reinterpret_cast<const uint4 *>(p + 16 * i);
+            const uint32_t w[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[8 * i + 2 * k] += __uint_as_float(w[k] << 16);
-                v[8 * i + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
-            }
+            for (int k = 0; k < 4; ++k)
+                a.v[4 * i + k] = enc::add2(a.v[4 * i + k], enc::pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
         }
     }
 }
 
-template <int ACT>
-__device__ __forceinline__ void activate(float (&v)[32]) {
+template <int ACT, int P>
+__device__ __forceinline__ void activate(uint64_t (&v)[P]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act::value<ACT>(v[i]);
+    for (int i = 0; i < P; ++i) v[i] = act::value2<ACT>(v[i]);
 }
 
 // Codes of one 32-column block; its scale byte is returned.
-__device__ __forceinline__ uint32_t encode32(const ProductArgs &g, uint8_t *p, const float (&v)[32]) {
+__device__ __forceinline__ uint32_t encode32(const ProductArgs &g, uint8_t *p, const Row32 &a, bool stored) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) enc::unpack2(a.v[i], v[2 * i], v[2 * i + 1]);
     const float top = enc::block_amax32(v);
     float inv;
     const bool fp8 = g.fmt == kEncMX8;
     const uint32_t s = fp8 ? enc::scale_of_e4m3(top, inv) : enc::scale_of(top, inv);
-    if (s == 0xFFu) inv = 0.0f;
+    const uint64_t inv2 = act::same2(inv);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) enc::unpack2(enc::mul2(a.v[i], inv2), v[2 * i], v[2 * i + 1]);
     uint32_t w[8];
     if (fp8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            w[i] = s == 0xFFu ? 0u
-                              : enc::cvt_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-        if (MX_STORE_OK(p, 32, g.codes, g.codes_bytes, g.status)) {
-            st_out16(p, w);
-            st_out16(p + 16, w + 4);
+            w[i] = s == 0xFFu ? 0u : enc::cvt_e4m3x4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        if (stored && MX_STORE_OK(p, 32, g.codes, g.codes_bytes, g.status)) {
+            if (g.wide_codes) {
+                st_out32(p, w);
+            } else {
+                st_out16(p, w);
+                st_out16(p + 16, w + 4);
+            }
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             w[i] = s == 0xFFu ? 0u
-                              : enc::cvt_e2m1x8(v[8 * i] * inv, v[8 * i + 1] * inv, v[8 * i + 2] * inv, v[8 * i + 3] * inv,
-                                                v[8 * i + 4] * inv, v[8 * i + 5] * inv, v[8 * i + 6] * inv,
-                                                v[8 * i + 7] * inv);
-        if (MX_STORE_OK(p, 16, g.codes, g.codes_bytes, g.status)) st_out16(p, w);
+                              : enc::cvt_e2m1x8(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3], v[8 * i + 4], v[8 * i + 5],
+                                                v[8 * i + 6], v[8 * i + 7]);
+        if (stored && MX_STORE_OK(p, 16, g.codes, g.codes_bytes, g.status)) st_out16(p, w);
     }
     return s;
 }
 
-// A thread's place in the epilogue: its row, the first of its 128 columns.
-struct EpiRow {
-    int64_t out;             // row of the output (depth: of all experts' rows)
-    int64_t bias;            // first element of the bias
-    bool stored, real;       // inside the output; not padding
-    bool scaled;             // its scales exist (rows up to a multiple of 128)
-    uint8_t *scale;          // its scales' word of column 0
+// A warp's place in the epilogue: 32 rows and 64 columns of a tile.
+struct EpiTile {
+    int row;         // the lane's row of the output (depth: of its expert's)
+    int expert;
+    int col;         // first column
+    bool stored;     // the row is inside the output,
+    bool real;       // not padding,
+    bool scaled;     // or padding of the scales
 };
 
-// Columns col .. col + 31 of a row: v is the accumulator on entry.  Returns the scale byte.
-__device__ __forceinline__ uint32_t finish32(const ProductArgs &g, const EpiRow &at, int64_t col, uint32_t (&acc)[32]) {
-    const int left = static_cast<int>(g.N - col < 32 ? g.N - col : 32);
-    if (left <= 0 || !at.stored) return 0;
-    float v[32];
-    if (at.real) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]);
-        if (g.bias != nullptr)
-            add_row(v, g.bias + (at.bias + col) * (g.bias_f32 ? 4 : 2), g.bias_f32, left);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    }
-    const int64_t e = at.out * g.N + col;
-    if (g.z != nullptr) store_bf16(g.z + 2 * e, g.z, g.z_bytes, v, left, g.wide, g.status);
+// Two blocks' scale bytes of a row (blocks of columns col, col + 32): half a word of the tiled
+// layout.  Rows and columns of its padding get zeros.
+__device__ __forceinline__ void put_scales(const ProductArgs &g, const EpiTile &at, uint32_t two) {
+    if (g.fmt == kEncNone || !at.scaled) return;
+    uint8_t *p = g.scales + ((at.row >> 7) * g.out_katoms + (at.col >> 7)) * 512 + (at.row & 31) * 16 + ((at.row & 127) >> 5) * 4 +
+                 ((at.col >> 5) & 3);
+    if (MX_STORE_OK(p, 2, g.scales, g.scales_bytes, g.status)) *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(two);
+}
+
+template <int P>
+__device__ __forceinline__ void activate(const ProductArgs &g, uint64_t (&v)[P]) {
     switch (g.act) {  // all of them keep 0 (padding rows)
-        case act::kRelu: activate<act::kRelu>(v); break;
-        case act::kRelu2: activate<act::kRelu2>(v); break;
-        case act::kGelu: activate<act::kGelu>(v); break;
-        case act::kGeluTanh: activate<act::kGeluTanh>(v); break;
-        case act::kSilu: activate<act::kSilu>(v); break;
+        case act::kRelu: activate<act::kRelu, P>(v); break;
+        case act::kRelu2: activate<act::kRelu2, P>(v); break;
+        case act::kGelu: activate<act::kGelu, P>(v); break;
+        case act::kGeluTanh: activate<act::kGeluTanh, P>(v); break;
+        case act::kSilu: activate<act::kSilu, P>(v); break;
         default: break;
     }
-    if (g.res != nullptr)
-        add_row(v, g.res + at.out * g.res_pitch + col * (g.res_f32 ? 4 : 2), g.res_f32, left);
+}
+
+// Columns at.col + part .. + 31 of the lane's row from its accumulator.  Returns the scale byte.
+template <int MODE>
+__device__ __forceinline__ uint32_t finish32(const ProductArgs &g, const EpiTile &at, int part, const uint32_t (&acc)[32]) {
+    const int col = at.col + part;
+    const int cols = static_cast<int>(g.N) - col;
+    if (cols <= 0) return 0;
+    Row32 a;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a.v[i] = enc::pack2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
+    if constexpr (MODE == kDepth) {
+        const int64_t e = (at.expert * g.M + at.row) * g.N + col;
+        if (g.y_f32) store_f32(g.y + 4 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
+        else store_bf16(g.y + 2 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
+        return 0;
+    }
+    if (g.bias != nullptr)
+        add_row(a, g.bias + ((MODE == kRows ? at.expert * g.N : 0) + col) * (g.bias_f32 ? 4 : 2), g.bias_f32, cols);
+    if constexpr (MODE == kRows) {
+        if (!at.real) {  // padding: zero, which every activation keeps
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a.v[i] = 0;
+        }
+    }
+    const int64_t e = at.row * g.N + col;
+    if (g.z != nullptr) store_bf16(g.z + 2 * e, g.z, g.z_bytes, a, cols, at.stored, g.wide, g.status);
+    activate(g, a.v);
+    if (MODE == kDense && g.res != nullptr && at.stored)
+        add_row(a, g.res + at.row * g.res_pitch + static_cast<int64_t>(col) * (g.res_f32 ? 4 : 2), g.res_f32, cols);
     if (g.y != nullptr) {
-        if (g.y_f32) store_f32(g.y + 4 * e, g.y, g.y_bytes, v, left, g.wide, g.status);
-        else store_bf16(g.y + 2 * e, g.y, g.y_bytes, v, left, g.wide, g.status);
+        if (g.y_f32) store_f32(g.y + 4 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
+        else store_bf16(g.y + 2 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
     }
     if (g.fmt == kEncNone) return 0;
-    return encode32(g, g.codes + (g.fmt == kEncMX8 ? e : e / 2), v);
+    const uint32_t scale = encode32(g, g.codes + (g.fmt == kEncMX8 ? e : e / 2), a, at.stored);
+    return at.stored ? scale : 0u;
+}
+template <int MODE>
+__device__ __forceinline__ void finish_row(const ProductArgs &g, const EpiTile &at, uint32_t (&v0)[32], const uint32_t (&v1)[32]) {
+    uint32_t scales = 0;
+    // A loop and not two copies: half the code, which a tile runs through once.
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        scales |= finish32<MODE>(g, at, 32 * h, v0) << (8 * h);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v0[i] = v1[i];
+    }
+    if (MODE != kDepth) put_scales(g, at, scales);
 }
 
 // Zeroes [from, base + bytes) of an output, 16 bytes at a time: the n-th of `threads` threads.
@@ -446,7 +488,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(&ctl->acc_empty, 2 * kEpiWarps);
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
-        ctl->issued = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -472,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // Warp 0 fills the operand ring, warp 2 the scale ring.
             const bool scales = warp == 2;
             const int ring = scales ? kSFRing : kStages;
-            int stage = 0, n_issued = 0;
+            int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int t = pair; ok && t < num_items; t += npairs) {
@@ -516,7 +557,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_2d_pair(st + kOffB + u * kSubBytes, &map_b, full_even, byte0 + u * kBKBytes,
                                              w.b_row + kHalf * static_cast<int>(rank));
                         }
-                        *reinterpret_cast<volatile int *>(&ctl->issued) = ++n_issued;
                     }
                     if (++stage == ring) {
                         stage = 0;
@@ -549,27 +589,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int left = w.units - ks * kKSub * E::kUnits;
                     const uint32_t sbase = smem_u32(smem + stage * kStageBytes);
                     const uint32_t slot = tmem + kSFCol + kSFSlot * static_cast<uint32_t>(stage);
-#pragma unroll
-                    for (int u = 0; u < kKSub; ++u) {
-                        if (u * E::kUnits >= left) break;
-                        const uint32_t sa = sbase + u * kSubBytes;
-                        const uint32_t sb = sbase + kOffB + u * kSubBytes;
+                    // The issue of these leaves no slack: a full stage's eight go without a test in between.
+                    const auto multiply = [&](int u, int j) {
+                        const uint32_t sa = sbase + u * kSubBytes + 32u * j;
+                        const uint32_t sb = sbase + kOffB + u * kSubBytes + 32u * j;
                         const uint32_t sf = slot + kSFCols * static_cast<uint32_t>(u);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            // Half a sub-tile ends an odd length: what follows in shared memory
-                            // is zeros, or (depth) the next expert's.
-                            if (FMT == kFmtMX4 && j >= 2 && left == 2 * u + 1) break;
-                            const uint32_t acc = (ks > 0 || u > 0 || j > 0) ? 1u : 0u;
-                            if constexpr (FMT == kFmtMX8) {
-                                mma_mxf8_pair(tmem + kAccCol, sdesc_sw128(sa + 32u * j), sdesc_sw128(sb + 32u * j), idesc8[j],
-                                              sf, sf + 8u, acc);
-                            } else {
-                                const uint32_t ka = static_cast<uint32_t>(j / 2);
-                                mma_mxf4_pair(tmem + kAccCol, sdesc_sw128(sa + 32u * j), sdesc_sw128(sb + 32u * j),
-                                              (j & 1) ? idesc2 : idesc0, sf + 4u * ka, sf + 8u + 8u * ka, acc);
-                            }
+                        const uint32_t acc = (ks > 0 || u > 0 || j > 0) ? 1u : 0u;
+                        if constexpr (FMT == kFmtMX8) {
+                            mma_mxf8_pair(tmem + kAccCol, sdesc_sw128(sa), sdesc_sw128(sb), idesc8[j], sf, sf + 8u, acc);
+                        } else {
+                            const uint32_t ka = static_cast<uint32_t>(j / 2);
+                            mma_mxf4_pair(tmem + kAccCol, sdesc_sw128(sa), sdesc_sw128(sb), (j & 1) ? idesc2 : idesc0,
+                                          sf + 4u * ka, sf + 8u + 8u * ka, acc);
                         }
+                    };
+                    if (left >= kKSub * E::kUnits) {
+#pragma unroll
+                        for (int u = 0; u < kKSub; ++u)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) multiply(u, j);
+                    } else {
+                        // An odd length ends in half an FP4 sub-tile: what follows in shared memory is
+                        // zeros, or (depth) the next expert's.
+#pragma unroll
+                        for (int u = 0; u < kKSub; ++u)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (4 * u + j < 4 * left / E::kUnits) multiply(u, j);
                     }
                     tc_commit_pair(&ctl->empty[stage], 0x3);
                     if (++stage == kStages) {
@@ -658,28 +704,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh) : "memory");
         const int q = warp & 3;                   // tensor-memory lane quarter this warp may access
-        const int half = (warp - kEpiWarp0) / 4;  // column half of the 256-wide tile
+        const int part = (warp - kEpiWarp0) / 4;  // column quarter of the 256-wide tile
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + kEpiCols * static_cast<uint32_t>(part);
         uint32_t acc_phase = 0;
-        int staged = 0;                           // stages of this pair's tiles so far
         for (int t = pair; t < num_items; t += npairs) {
             const Tile w = tile_of<MODE>(g, ctl, t);
-            const int ns = stages_of<FMT>(w);
-            staged += ns;
-            const int r = kHalf * static_cast<int>(rank) + 32 * q + lane;  // row of the tile
-            EpiRow at;
-            at.out = static_cast<int64_t>(w.row) + r;
-            at.bias = 0;
-            at.stored = at.real = r < w.m_left;
-            at.scaled = MODE == kRows ? at.stored : at.out < ((g.M + 127) & ~int64_t(127));
-            if constexpr (MODE == kRows) {
-                at.bias = static_cast<int64_t>(w.expert) * g.N;
-                at.real = at.stored && at.out - static_cast<int64_t>(ctl->start[w.expert]) * 128 < g.counts[w.expert];
-            }
-            at.scale = g.scales + (at.out >> 7) * g.out_katoms * 512 + (at.out & 31) * 16 + ((at.out & 127) >> 5) * 4;
-            if constexpr (MODE == kDepth) at.out += static_cast<int64_t>(w.expert) * g.M;
-
-            uint32_t v0[32], v1[32], v2[32], v3[32];
-            if (ns > 0) {
+            const bool empty = stages_of<FMT>(w) == 0;
+            EpiTile at;
+            const int r = kHalf * static_cast<int>(rank) + 32 * q + lane;
+            at.row = w.row + r;
+            at.expert = w.expert;
+            at.col = w.col + kEpiCols * part;
+            at.stored = r < w.m_left;
+            at.scaled = r < ((w.m_left + 127) & ~127);
+            at.real = at.stored;
+            if constexpr (MODE == kRows) at.real = at.stored && at.row - ctl->start[w.expert] * 128 < g.counts[w.expert];
+            uint32_t v0[32], v1[32];
+            if (!empty) {
                 // One lane waits; its result is broadcast so the warp stays
                 // converged for the .sync.aligned tensor-memory loads.
                 int ok = 1;
@@ -688,11 +729,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 acc_phase ^= 1u;
-                const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + 128u * static_cast<uint32_t>(half);
                 tmem_ld_32x32b_x32(tbase, v0);
                 tmem_ld_32x32b_x32(tbase + 32u, v1);
-                tmem_ld_32x32b_x32(tbase + 64u, v2);
-                tmem_ld_32x32b_x32(tbase + 96u, v3);
                 tmem_ld_wait();
                 // The accumulator is in registers: the next tile may start.
                 tc_fence_before();
@@ -700,33 +738,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) arrive_even(&ctl->acc_empty);
             } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v0[i] = v1[i] = v2[i] = v3[i] = 0;
+                for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0;
             }
-            // 32 columns at a time, each once the producer has issued another
-            // quarter of the next tile's stages, so that the outputs of all SMs do not
-            // reach L2 in one burst.
-            const int next = t + npairs;
-            const int nn = next < num_items ? stages_of<FMT>(tile_of<MODE>(g, ctl, next)) : 0;
-            const int64_t col0 = static_cast<int64_t>(w.col) + 128 * half;
-            uint32_t word = 0;
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                if (nn > 0 && !wait_issued(ctl, staged + 1 + (j * nn) / 4, g.status, abort)) break;
-                word |= finish32(g, at, col0 + 32 * j, v0) << (8 * j);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v0[i] = v1[i], v1[i] = v2[i], v2[i] = v3[i];
-            }
-            // The four blocks' scale bytes are one word of the tiled layout; rows and
-            // columns of its padding get zeros.
-            if (g.fmt != kEncNone && at.scaled) {
-                uint8_t *p = at.scale + (col0 >> 7) * 512;
-                if (MX_STORE_OK(p, 4, g.scales, g.scales_bytes, g.status)) *reinterpret_cast<uint32_t *>(p) = word;
-            }
+            finish_row<MODE>(g, at, v0, v1);
         }
         if constexpr (MODE == kRows) {
             // Rows behind the last segment are zero.
             const size_t row = static_cast<size_t>(ctl->start[g.experts]) * 128;
-            const size_t n = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x - 32 * kEpiWarp0, all = static_cast<size_t>(gridDim.x) * 256;
+            const size_t n = static_cast<size_t>(blockIdx.x) * 32 * kEpiWarps + threadIdx.x - 32 * kEpiWarp0,
+                         all = static_cast<size_t>(gridDim.x) * 32 * kEpiWarps;
             const size_t N = static_cast<size_t>(g.N);
             zero_from(g.y, row * N * (g.y_f32 ? 4 : 2), g.y_bytes, n, all, g.status);
             zero_from(g.z, row * N * 2, g.z_bytes, n, all, g.status);
@@ -833,6 +853,10 @@ cudaError_t launch_product(const Product &p, const DeviceInfo &dev, cudaStream_t
     g.m_tiles = static_cast<int>(m_tiles);
     g.n_tiles = static_cast<int>(n_tiles);
     g.num_items = static_cast<int>(tiles);
+    g.by_n = divisor(n_tiles);
+    g.by_band = divisor(kBand * n_tiles);
+    g.by_last = divisor((m_tiles - 1) % kBand + 1);
+    g.by_expert = divisor(m_tiles * n_tiles);
     g.experts = static_cast<int>(p.experts);
     g.offsets = p.offsets;
     g.counts = p.counts;
@@ -856,10 +880,13 @@ cudaError_t launch_product(const Product &p, const DeviceInfo &dev, cudaStream_t
     g.act = p.act;
     const uintptr_t ends = reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.z);
     g.wide = (ends & 31) == 0 && p.N % 16 == 0;
+    g.wide_codes = (reinterpret_cast<uintptr_t>(p.enc.codes) & 31) == 0;
     g.status = dev.status;
-    return depth  ? launch_mode<kDepth>(p.fp8, map_a, map_b, g, tiles, dev, stream)
-           : rows ? launch_mode<kRows>(p.fp8, map_a, map_b, g, tiles, dev, stream)
-                  : launch_mode<kDense>(p.fp8, map_a, map_b, g, tiles, dev, stream);
+    switch (p.mode) {
+        case kProductRows: return launch_mode<kRows>(p.fp8, map_a, map_b, g, tiles, dev, stream);
+        case kProductDepth: return launch_mode<kDepth>(p.fp8, map_a, map_b, g, tiles, dev, stream);
+        default: return launch_mode<kDense>(p.fp8, map_a, map_b, g, tiles, dev, stream);
+    }
 }
 
 }  // namespace mx
