@@ -156,6 +156,19 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_lines64(CUtensorMap *map, const void *base, uint64_t row_bytes, uint64_t lines,
+                         uint32_t box_inner, uint32_t box_lines, CUtensorMapSwizzle swizzle) {
+    if (g_encode == nullptr) return false;
+    cuuint64_t dims[5] = {row_bytes, 2, 4, 8, lines / 64};
+    cuuint64_t strides[4] = {row_bytes, 16 * row_bytes, 2 * row_bytes, 64 * row_bytes};
+    cuuint32_t box[5] = {box_inner, 2, 4, 8, box_lines / 64};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace mx
 
 using namespace mx;

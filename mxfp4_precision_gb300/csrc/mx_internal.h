@@ -22,6 +22,12 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
                     uint64_t inner_elems, uint64_t outer_elems, uint64_t row_bytes,
                     uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
+// Map of a row-major byte matrix whose lines (a multiple of 64) are loaded 64 by 64 in the order
+// position 8 i + 2 c + b <- line 16 c + 2 i + b (b < 2, c < 4, i < 8): dimensions (bytes, b, c, i,
+// group of 64), a box of box_inner bytes by box_lines lines.
+bool encode_tmap_lines64(CUtensorMap *map, const void *base, uint64_t row_bytes, uint64_t lines,
+                         uint32_t box_inner, uint32_t box_lines, CUtensorMapSwizzle swizzle);
+
 // Scale-layout geometry (see mx.h): k-atoms (4 blocks of 32) per 128-line group.
 inline int64_t scale_katoms(int64_t k) { return 2 * ((k + 255) / 256); }
 inline int64_t scale_groups(int64_t mn) { return (mn + 127) / 128; }

@@ -374,20 +374,20 @@ __device__ __forceinline__ uint32_t encode32(const ProductArgs &g, uint8_t *p, c
 
 // A warp's place in the epilogue: 32 rows and 64 columns of a tile.
 struct EpiTile {
-    int row;         // the lane's row of the output (depth: of its expert's)
+    int row;     // the lane's row of the output (depth: of its expert's)
     int expert;
-    int col;         // first column
-    bool stored;     // the row is inside the output,
-    bool real;       // not padding,
-    bool scaled;     // or padding of the scales
+    int col;     // first column
+    int left;    // rows from the lane's on that are inside the output (none: 0 or less)
+    int real;    // ... that are not padding
+    int scaled;  // ... whose scales exist
 };
 
 // Two blocks' scale bytes of a row (blocks of columns col, col + 32): half a word of the tiled
 // layout.  Rows and columns of its padding get zeros.
-__device__ __forceinline__ void put_scales(const ProductArgs &g, const EpiTile &at, uint32_t two) {
-    if (g.fmt == kEncNone || !at.scaled) return;
-    uint8_t *p = g.scales + ((at.row >> 7) * g.out_katoms + (at.col >> 7)) * 512 + (at.row & 31) * 16 + ((at.row & 127) >> 5) * 4 +
-                 ((at.col >> 5) & 3);
+__device__ __forceinline__ void put_scales(const ProductArgs &g, const EpiTile &at, int more, uint32_t two) {
+    if (g.fmt == kEncNone || more >= at.scaled) return;
+    const int row = at.row + more;
+    uint8_t *p = g.scales + ((row >> 7) * g.out_katoms + (at.col >> 7)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + ((at.col >> 5) & 3);
     if (MX_STORE_OK(p, 2, g.scales, g.scales_bytes, g.status)) *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(two);
 }
 
@@ -409,35 +409,36 @@ __device__ __forceinline__ uint32_t finish32(const ProductArgs &g, const EpiTile
     const int col = at.col + part;
     const int cols = static_cast<int>(g.N) - col;
     if (cols <= 0) return 0;
+    const bool stored = at.left > 0;
     Row32 a;
 #pragma unroll
     for (int i = 0; i < 16; ++i) a.v[i] = enc::pack2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
     if constexpr (MODE == kDepth) {
         const int64_t e = (at.expert * g.M + at.row) * g.N + col;
-        if (g.y_f32) store_f32(g.y + 4 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
-        else store_bf16(g.y + 2 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
+        if (g.y_f32) store_f32(g.y + 4 * e, g.y, g.y_bytes, a, cols, stored, g.wide, g.status);
+        else store_bf16(g.y + 2 * e, g.y, g.y_bytes, a, cols, stored, g.wide, g.status);
         return 0;
     }
     if (g.bias != nullptr)
         add_row(a, g.bias + ((MODE == kRows ? at.expert * g.N : 0) + col) * (g.bias_f32 ? 4 : 2), g.bias_f32, cols);
     if constexpr (MODE == kRows) {
-        if (!at.real) {  // padding: zero, which every activation keeps
+        if (at.real <= 0) {  // padding: zero, which every activation keeps
 #pragma unroll
             for (int i = 0; i < 16; ++i) a.v[i] = 0;
         }
     }
     const int64_t e = at.row * g.N + col;
-    if (g.z != nullptr) store_bf16(g.z + 2 * e, g.z, g.z_bytes, a, cols, at.stored, g.wide, g.status);
+    if (g.z != nullptr) store_bf16(g.z + 2 * e, g.z, g.z_bytes, a, cols, stored, g.wide, g.status);
     activate(g, a.v);
-    if (MODE == kDense && g.res != nullptr && at.stored)
+    if (MODE == kDense && g.res != nullptr && stored)
         add_row(a, g.res + at.row * g.res_pitch + static_cast<int64_t>(col) * (g.res_f32 ? 4 : 2), g.res_f32, cols);
     if (g.y != nullptr) {
-        if (g.y_f32) store_f32(g.y + 4 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
-        else store_bf16(g.y + 2 * e, g.y, g.y_bytes, a, cols, at.stored, g.wide, g.status);
+        if (g.y_f32) store_f32(g.y + 4 * e, g.y, g.y_bytes, a, cols, stored, g.wide, g.status);
+        else store_bf16(g.y + 2 * e, g.y, g.y_bytes, a, cols, stored, g.wide, g.status);
     }
     if (g.fmt == kEncNone) return 0;
-    const uint32_t scale = encode32(g, g.codes + (g.fmt == kEncMX8 ? e : e / 2), a, at.stored);
-    return at.stored ? scale : 0u;
+    const uint32_t scale = encode32(g, g.codes + (g.fmt == kEncMX8 ? e : e / 2), a, stored);
+    return stored ? scale : 0u;
 }
 template <int MODE>
 __device__ __forceinline__ void finish_row(const ProductArgs &g, const EpiTile &at, uint32_t (&v0)[32], const uint32_t (&v1)[32]) {
@@ -449,7 +450,186 @@ __device__ __forceinline__ void finish_row(const ProductArgs &g, const EpiTile &
 #pragma unroll
         for (int i = 0; i < 32; ++i) v0[i] = v1[i];
     }
-    if (MODE != kDepth) put_scales(g, at, scales);
+    if (MODE != kDepth) put_scales(g, at, 0, scales);
+}
+
+// ---- N a multiple of 64: four lanes have 16 columns each of a row
+// A store of 32 lanes on 32 rows touches 32 lines, one a clock and SM, which is what an
+// epilogue of fp32 spends its time on.  So the B lines of a 64-line group are loaded in
+// another order, such that the tensor memory's 16 x 256-bit load, which gives lane 4 r + c of a
+// warp columns 8 i + 2 c + {0, 1} of rows r and r + 8, gives it 16 columns that follow one
+// another: column 8 i + 2 c + b holds line line_of(8 i + 2 c + b) = 16 c + 2 i + b, and the
+// scale writers gather the lines' scales in that order.  Four lanes then write a line together.
+__device__ __forceinline__ uint32_t line_of(uint32_t p) { return 16u * ((p >> 1) & 3u) + 2u * (p >> 3) + (p & 1u); }
+
+// Brings the bias of a warp's 64 columns into L1 while it waits for the tile.
+template <int MODE>
+__device__ __forceinline__ void warm_bias(const ProductArgs &g, const EpiTile &at) {
+    const int lane = threadIdx.x & 31, per = g.bias_f32 ? 4 : 8;  // columns of 16 bytes
+    if (MODE == kDepth || g.bias == nullptr || per * lane >= kEpiCols || at.col >= g.N) return;
+    asm volatile("{\n\t.reg .b32 a, b, c, d;\n\tld.global.v4.b32 {a, b, c, d}, [%0];\n\t}" ::"l"(
+        g.bias + ((MODE == kRows ? at.expert * g.N : 0) + at.col + per * lane) * (g.bias_f32 ? 4 : 2)));
+}
+
+// Adds 16 columns of a bf16 or fp32 row (16-byte aligned).
+__device__ __forceinline__ void add16(uint64_t *v, const uint8_t *p, bool f32) {
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(p + 16 * i);
+            v[2 * i] = enc::add2(v[2 * i], s.x), v[2 * i + 1] = enc::add2(v[2 * i + 1], s.y);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 s = *reinterpret_cast<const uint4 *>(p + 16 * i);
+        const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            v[4 * i + k] = enc::add2(v[4 * i + k], enc::pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
+    }
+}
+__device__ __forceinline__ void put16_bf16(uint8_t *p, const uint8_t *base, size_t bytes, const uint64_t *v, bool wide, int *status) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = bf16_pair(v[i]);
+    if (!MX_STORE_OK(p, 32, base, bytes, status)) return;
+    if (wide) {
+        st_out32(p, w);
+    } else {
+        st_out16(p, w);
+        st_out16(p + 16, w + 4);
+    }
+}
+__device__ __forceinline__ void put16_f32(uint8_t *p, const uint8_t *base, size_t bytes, const uint64_t *v, bool wide, int *status) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            enc::unpack2(v[4 * i + k], lo, hi);
+            w[2 * k] = __float_as_uint(lo), w[2 * k + 1] = __float_as_uint(hi);
+        }
+        if (!MX_STORE_OK(p + 32 * i, 32, base, bytes, status)) continue;
+        if (wide) {
+            st_out32(p + 32 * i, w);
+        } else {
+            st_out16(p + 32 * i, w);
+            st_out16(p + 32 * i + 16, w + 4);
+        }
+    }
+}
+__device__ __forceinline__ void put16(uint8_t *y, int64_t e, size_t bytes, const uint64_t *v, bool f32, bool wide, int *status) {
+    if (f32) put16_f32(y + 4 * e, y, bytes, v, wide, status);
+    else put16_bf16(y + 2 * e, y, bytes, v, wide, status);
+}
+
+// Codes of the lane's 16 columns of a row, of which two lanes hold a block (whole warps); the
+// block's scale byte is returned.
+__device__ __forceinline__ uint32_t encode16(const ProductArgs &g, int64_t e, const uint64_t *v, bool stored) {
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) enc::unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    float top = enc::absmax2_nan(f[0], f[1]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = enc::absmax3_nan(top, f[2 * i], f[2 * i + 1]);
+    top = enc::absmax2_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    float inv;
+    const bool fp8 = g.fmt == kEncMX8;
+    const uint32_t s = fp8 ? enc::scale_of_e4m3(top, inv) : enc::scale_of(top, inv);
+    const uint64_t inv2 = act::same2(inv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) enc::unpack2(enc::mul2(v[i], inv2), f[2 * i], f[2 * i + 1]);
+    const bool none = s == 0xFFu;
+    if (fp8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = none ? 0u : enc::cvt_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        uint8_t *p = g.codes + e;
+        if (stored && MX_STORE_OK(p, 16, g.codes, g.codes_bytes, g.status)) st_out16(p, w);
+    } else {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = none ? 0u
+                        : enc::cvt_e2m1x8(f[8 * i], f[8 * i + 1], f[8 * i + 2], f[8 * i + 3], f[8 * i + 4], f[8 * i + 5], f[8 * i + 6],
+                                          f[8 * i + 7]);
+        uint8_t *p = g.codes + e / 2;
+        if (stored && MX_STORE_OK(p, 8, g.codes, g.codes_bytes, g.status)) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+    return stored ? s : 0u;
+}
+
+// The lane's 16 columns of rows `more` and `more + 8` below its own.
+// Returns both rows' two scale bytes (in lane 0 of four), the first row's in the low half.
+template <int MODE>
+__device__ __forceinline__ uint32_t finish_two(const ProductArgs &g, const EpiTile &at, int more, const uint32_t (&acc)[32]) {
+    const int col = at.col + 16 * static_cast<int>(threadIdx.x & 3);
+    uint64_t v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = enc::pack2(__uint_as_float(acc[4 * i]), __uint_as_float(acc[4 * i + 1]));
+        v[8 + i] = enc::pack2(__uint_as_float(acc[4 * i + 2]), __uint_as_float(acc[4 * i + 3]));
+    }
+    const bool first = more < at.left, second = more + 8 < at.left;
+    const int64_t e0 = ((MODE == kDepth ? at.expert * g.M : 0) + at.row + more) * g.N + col, e1 = e0 + 8 * g.N;
+    if constexpr (MODE == kDepth) {
+        if (first) put16(g.y, e0, g.y_bytes, v, g.y_f32, g.wide, g.status);
+        if (second) put16(g.y, e1, g.y_bytes, v + 8, g.y_f32, g.wide, g.status);
+        return 0;
+    }
+    if (g.bias != nullptr) {
+        const uint8_t *p = g.bias + ((MODE == kRows ? at.expert * g.N : 0) + col) * (g.bias_f32 ? 4 : 2);
+        add16(v, p, g.bias_f32);
+        add16(v + 8, p, g.bias_f32);
+    }
+    if constexpr (MODE == kRows) {  // padding: zero, which every activation keeps
+        if (more >= at.real) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0;
+        }
+        if (more + 8 >= at.real) {
+#pragma unroll
+            for (int i = 8; i < 16; ++i) v[i] = 0;
+        }
+    }
+    if (g.z != nullptr) {
+        if (first) put16_bf16(g.z + 2 * e0, g.z, g.z_bytes, v, g.wide, g.status);
+        if (second) put16_bf16(g.z + 2 * e1, g.z, g.z_bytes, v + 8, g.wide, g.status);
+    }
+    activate(g, v);
+    if (MODE == kDense && g.res != nullptr) {
+        const uint8_t *p = g.res + (at.row + more) * g.res_pitch + static_cast<int64_t>(col) * (g.res_f32 ? 4 : 2);
+        if (first) add16(v, p, g.res_f32);
+        if (second) add16(v + 8, p + 8 * g.res_pitch, g.res_f32);
+    }
+    if (g.y != nullptr) {
+        if (first) put16(g.y, e0, g.y_bytes, v, g.y_f32, g.wide, g.status);
+        if (second) put16(g.y, e1, g.y_bytes, v + 8, g.y_f32, g.wide, g.status);
+    }
+    if (g.fmt == kEncNone) return 0;
+    const uint32_t s = encode16(g, e0, v, first) | encode16(g, e1, v + 8, second) << 16;
+    return s | __shfl_down_sync(0xFFFFFFFFu, s, 2) << 8;
+}
+template <int MODE>
+__device__ __forceinline__ void finish_rows(const ProductArgs &g, const EpiTile &at, uint32_t (&v0)[32], const uint32_t (&v1)[32]) {
+    const bool inside = at.col < g.N;  // else only padding of the scales
+    uint32_t low = 0, high = 0;        // scales of rows 0 and 8, 16 and 24 from the lane's own
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        low = high;
+        high = inside ? finish_two<MODE>(g, at, 16 * h, v0) : 0u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v0[i] = v1[i];
+    }
+    if (MODE == kDepth || g.fmt == kEncNone) return;
+    // Each of four lanes stores one of their four rows' halves of a word.
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    low = __shfl_sync(0xFFFFFFFFu, low, lane & ~3);
+    high = __shfl_sync(0xFFFFFFFFu, high, lane & ~3);
+    put_scales(g, at, 8 * c, (c < 2 ? low : high) >> (16 * (c & 1)));
 }
 
 // Zeroes [from, base + bytes) of an output, 16 bytes at a time: the n-th of `threads` threads.
@@ -460,7 +640,7 @@ __device__ __forceinline__ void zero_from(uint8_t *base, size_t from, size_t byt
         if (MX_STORE_OK(base + i, 16, base, bytes, status)) st_out16(base + i, none);
 }
 
-template <int FMT, int MODE>
+template <int FMT, int MODE, bool GATHER>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ ProductArgs g) {
@@ -554,8 +734,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int u = 0; u < nsub; ++u) {
                             tma_load_2d_pair(st + u * kSubBytes, &map_a, full_even, byte0 + u * kBKBytes,
                                              w.a_row + kHalf * static_cast<int>(rank));
-                            tma_load_2d_pair(st + kOffB + u * kSubBytes, &map_b, full_even, byte0 + u * kBKBytes,
-                                             w.b_row + kHalf * static_cast<int>(rank));
+                            const int b_row = w.b_row + kHalf * static_cast<int>(rank);
+                            if constexpr (GATHER)
+                                tma_load_5d_pair(st + kOffB + u * kSubBytes, &map_b, full_even, byte0 + u * kBKBytes, 0, 0, 0, b_row >> 6);
+                            else
+                                tma_load_2d_pair(st + kOffB + u * kSubBytes, &map_b, full_even, byte0 + u * kBKBytes, b_row);
                         }
                     }
                     if (++stage == ring) {
@@ -637,6 +820,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // The tensor-memory layout of a sub-tile's scales is described in mx_gemm.cu.
         const int q = warp & 3;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        // GATHER: where the four B lines of this lane lie in an atom (line_of's order).
+        uint32_t b_at[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t n = 64u * (k >> 1) + line_of(32u * (k & 1) + lane);
+            b_at[k] = (n & 31u) * 16u + (n >> 5) * 4u;
+        }
         int stage = 0, sj = 0;
         uint32_t phase = 0, sphase = 0;
         for (int t = pair; t < num_items; t += npairs) {
@@ -669,9 +859,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         a[4 * ka + 0] = v.x, a[4 * ka + 1] = v.y, a[4 * ka + 2] = v.z, a[4 * ka + 3] = v.w;
 #pragma unroll
                         for (int rb = 0; rb < 2; ++rb) {
-                            const uint4 s = *reinterpret_cast<const uint4 *>(sfb + rb * kKSub * kSFSub + ka * 512 + lane * 16);
-                            b[8 * ka + 4 * rb + 0] = s.x, b[8 * ka + 4 * rb + 1] = s.y;
-                            b[8 * ka + 4 * rb + 2] = s.z, b[8 * ka + 4 * rb + 3] = s.w;
+                            const uint8_t *from = sfb + rb * kKSub * kSFSub + ka * 512;
+                            if constexpr (GATHER) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    b[8 * ka + 4 * rb + k] = *reinterpret_cast<const uint32_t *>(from + b_at[k]);
+                            } else {
+                                const uint4 s = *reinterpret_cast<const uint4 *>(from + lane * 16);
+                                b[8 * ka + 4 * rb + 0] = s.x, b[8 * ka + 4 * rb + 1] = s.y;
+                                b[8 * ka + 4 * rb + 2] = s.z, b[8 * ka + 4 * rb + 3] = s.w;
+                            }
                         }
                     }
                     if constexpr (FMT == kFmtMX8) {
@@ -711,14 +908,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Tile w = tile_of<MODE>(g, ctl, t);
             const bool empty = stages_of<FMT>(w) == 0;
             EpiTile at;
-            const int r = kHalf * static_cast<int>(rank) + 32 * q + lane;
+            const int r = kHalf * static_cast<int>(rank) + 32 * q + (GATHER ? lane >> 2 : lane);
             at.row = w.row + r;
             at.expert = w.expert;
             at.col = w.col + kEpiCols * part;
-            at.stored = r < w.m_left;
-            at.scaled = r < ((w.m_left + 127) & ~127);
-            at.real = at.stored;
-            if constexpr (MODE == kRows) at.real = at.stored && at.row - ctl->start[w.expert] * 128 < g.counts[w.expert];
+            at.left = w.m_left - r;
+            at.scaled = ((w.m_left + 127) & ~127) - r;
+            at.real = at.left;
+            if constexpr (MODE == kRows) at.real = min(at.left, g.counts[w.expert] - (at.row - ctl->start[w.expert] * 128));
+            if constexpr (GATHER) warm_bias<MODE>(g, at);
             uint32_t v0[32], v1[32];
             if (!empty) {
                 // One lane waits; its result is broadcast so the warp stays
@@ -729,8 +927,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 acc_phase ^= 1u;
-                tmem_ld_32x32b_x32(tbase, v0);
-                tmem_ld_32x32b_x32(tbase + 32u, v1);
+                if constexpr (GATHER) {
+                    tmem_ld_16x256b_x8(tbase, v0);
+                    tmem_ld_16x256b_x8(tbase + (16u << 16), v1);
+                } else {
+                    tmem_ld_32x32b_x32(tbase, v0);
+                    tmem_ld_32x32b_x32(tbase + 32u, v1);
+                }
                 tmem_ld_wait();
                 // The accumulator is in registers: the next tile may start.
                 tc_fence_before();
@@ -740,7 +943,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0;
             }
-            finish_row<MODE>(g, at, v0, v1);
+            if constexpr (GATHER) finish_rows<MODE>(g, at, v0, v1);
+            else finish_row<MODE>(g, at, v0, v1);
         }
         if constexpr (MODE == kRows) {
             // Rows behind the last segment are zero.
@@ -769,28 +973,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Co-resident 2-CTA clusters of a kernel variant on a device, measured once.
-template <int FMT, int MODE>
+template <int FMT, int MODE, bool GATHER>
 int product_clusters(const DeviceInfo &dev) {
     static std::atomic<int> cache[64];
     const int idx = dev.ordinal >= 0 && dev.ordinal < 64 ? dev.ordinal : 0;
     int n = cache[idx].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    if (cudaFuncSetAttribute(mx_product_kernel<FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(mx_product_kernel<FMT, MODE, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmem)) != cudaSuccess)
         return 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = kSmem;
-    if (cudaOccupancyMaxActiveClusters(&n, mx_product_kernel<FMT, MODE>, &cfg) != cudaSuccess || n < 1) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, mx_product_kernel<FMT, MODE, GATHER>, &cfg) != cudaSuccess || n < 1) return 0;
     cache[idx].store(n, std::memory_order_relaxed);
     return n;
 }
 
-template <int FMT, int MODE>
+template <int FMT, int MODE, bool GATHER>
 cudaError_t launch_variant(const CUtensorMap &map_a, const CUtensorMap &map_b, const ProductArgs &g, int64_t most_items,
                            const DeviceInfo &dev, cudaStream_t stream) {
-    const int pairs_max = product_clusters<FMT, MODE>(dev);
+    const int pairs_max = product_clusters<FMT, MODE, GATHER>(dev);
     if (pairs_max < 1) return cudaErrorLaunchOutOfResources;
     int64_t pairs = std::min<int64_t>(most_items, pairs_max);
     // As many rounds of tiles as all pairs need, spread evenly over fewer pairs (where the
@@ -809,31 +1013,39 @@ cudaError_t launch_variant(const CUtensorMap &map_a, const CUtensorMap &map_b, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_product_kernel<FMT, MODE>, map_a, map_b, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_product_kernel<FMT, MODE, GATHER>, map_a, map_b, g);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int MODE>
+template <int MODE, bool GATHER>
 cudaError_t launch_mode(bool fp8, const CUtensorMap &map_a, const CUtensorMap &map_b, const ProductArgs &g, int64_t most_items,
                         const DeviceInfo &dev, cudaStream_t stream) {
-    return fp8 ? launch_variant<kFmtMX8, MODE>(map_a, map_b, g, most_items, dev, stream)
-               : launch_variant<kFmtMX4, MODE>(map_a, map_b, g, most_items, dev, stream);
+    return fp8 ? launch_variant<kFmtMX8, MODE, GATHER>(map_a, map_b, g, most_items, dev, stream)
+               : launch_variant<kFmtMX4, MODE, GATHER>(map_a, map_b, g, most_items, dev, stream);
 }
-
 }  // namespace
 
 cudaError_t launch_product(const Product &p, const DeviceInfo &dev, cudaStream_t stream) {
     const bool rows = p.mode == kProductRows, depth = p.mode == kProductDepth;
     const int64_t row_bytes = p.fp8 ? p.K : p.K / 2;
+    // Four lanes a row (GATHER) where lines are what the epilogue waits for: a residual is read
+    // (8192 x 14336 x 4096: 167 us, 230 without), and the experts' Wgrad, whose outputs are many
+    // for the length of its products (8 experts of 14336 x 4096 over 16384 rows, fp32: 437 us, 510
+    // without).  Elsewhere a lane's own row is no slower (bf16 150 us, 151 to 156) or faster
+    // (z, y and codes with gelu 210 us, 242).  Whole groups of 64 lines alone can be loaded in
+    // that order: a partial one could not be kept inside its buffer.
+    const bool gather = p.N % 64 == 0 && (depth || p.res.p != nullptr);
     CUtensorMap map_a, map_b;
     std::memset(&map_a, 0, sizeof(map_a));
     std::memset(&map_b, 0, sizeof(map_b));
     if (p.K > 0) {  // without a contraction nothing is loaded
         const int64_t b_lines = rows ? p.N * p.experts : p.N;
         if (!encode_tmap_2d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Aq, row_bytes, p.M, row_bytes, kBKBytes, kHalf,
-                            CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode_tmap_2d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Bq, row_bytes, b_lines, row_bytes, kBKBytes, kHalf,
                             CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+        if (gather ? !encode_tmap_lines64(&map_b, p.Bq, row_bytes, b_lines, kBKBytes, kHalf, CU_TENSOR_MAP_SWIZZLE_128B)
+                   : !encode_tmap_2d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Bq, row_bytes, b_lines, row_bytes, kBKBytes, kHalf,
+                                     CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
     ProductArgs g{};
@@ -882,11 +1094,12 @@ cudaError_t launch_product(const Product &p, const DeviceInfo &dev, cudaStream_t
     g.wide = (ends & 31) == 0 && p.N % 16 == 0;
     g.wide_codes = (reinterpret_cast<uintptr_t>(p.enc.codes) & 31) == 0;
     g.status = dev.status;
-    switch (p.mode) {
-        case kProductRows: return launch_mode<kRows>(p.fp8, map_a, map_b, g, tiles, dev, stream);
-        case kProductDepth: return launch_mode<kDepth>(p.fp8, map_a, map_b, g, tiles, dev, stream);
-        default: return launch_mode<kDense>(p.fp8, map_a, map_b, g, tiles, dev, stream);
-    }
+    if (depth)
+        return gather ? launch_mode<kDepth, true>(p.fp8, map_a, map_b, g, tiles, dev, stream)
+                      : launch_mode<kDepth, false>(p.fp8, map_a, map_b, g, tiles, dev, stream);
+    if (rows) return launch_mode<kRows, false>(p.fp8, map_a, map_b, g, tiles, dev, stream);
+    return gather ? launch_mode<kDense, true>(p.fp8, map_a, map_b, g, tiles, dev, stream)
+                  : launch_mode<kDense, false>(p.fp8, map_a, map_b, g, tiles, dev, stream);
 }
 
 }  // namespace mx
