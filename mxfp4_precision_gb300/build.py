@@ -31,7 +31,7 @@ CHECKED_DIR = os.path.join(HERE, "_build_checked")
 CHECKED_LIB = os.path.join(CHECKED_DIR, "libmx.so")
 SOURCES = ["mx_api.cu", "mx_quant.cu", "mx_gemm.cu", "mx_noalloc.cu", "mx_scales.cu",
            "mx_peak.cu", "mx_norm.cu", "mx_glu.cu", "mx_grad.cu", "mx_product.cu",
-           "mx_act.cu", "mx_experts.cu"]
+           "mx_act.cu", "mx_experts.cu", "mx_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE]

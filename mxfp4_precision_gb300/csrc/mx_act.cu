@@ -47,8 +47,11 @@ __device__ __forceinline__ void slopes(const V8 &z, V8 &d) {
     for (int i = 0; i < 4; ++i) d.v[i] = mul2(d.v[i], act::slope2<ACT>(z.v[i]));
 }
 
+// Two rows in flight a warp and four blocks an SM: with four rows, whose registers leave two
+// blocks, gelu's slope waits for its own instructions (fp32 dy, 8192 x 14336: 160 us, 143 us).
+// The few rows of a small call are all read at once.
 template <typename D, typename Z, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) mx_bias_act_backward_kernel(const __grid_constant__ ActGradArgs p) {
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 4 : 1) mx_bias_act_backward_kernel(const __grid_constant__ ActGradArgs p) {
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x >= p.tiles) {
@@ -64,7 +67,7 @@ __global__ void __launch_bounds__(32 * WARPS) mx_bias_act_backward_kernel(const 
     const int64_t end = min(p.T, first + p.share);
     const uint8_t *dy = p.dy + static_cast<size_t>(col) * D::kBytes;
     const uint8_t *z = p.z + static_cast<size_t>(col) * Z::kBytes;
-    constexpr int kAhead = 4;  // rows in flight
+    constexpr int kAhead = WARPS == 8 ? 2 : 4;  // rows in flight
     V8 sum = zero_v8();
     for (int64_t row = first + warp; row < end; row += kAhead * WARPS) {
         Raw8<D> dr[kAhead];

@@ -430,7 +430,7 @@ mx_status check_epilogue(Product &p, const void *bias, int bias_type, int act, v
 mx_status check_product(Product &p, int operands) {
     if (operands != MX_FORMAT_MXFP4 && operands != MX_FORMAT_MXFP8) return MX_ERR_INVALID_ARG;
     p.fp8 = operands == MX_FORMAT_MXFP8;
-    if (p.M < 0 || p.N < 0 || p.K < 0 || p.M > 0x7FFFFFFF || p.N > 0x3FFFFFFF || p.K > 0x7FFFFFFF) return MX_ERR_SHAPE;
+    if (p.M < 0 || p.N < 0 || p.K < 0 || p.M > 0x7FFFFF00 || p.N > 0x3FFFFFFF || p.K > 0x7FFFFFFF) return MX_ERR_SHAPE;
     if (p.M == 0 || p.N == 0) return MX_OK;
     if (p.K % 32 != 0) return MX_ERR_SHAPE;
     if (p.N % 8 != 0) return MX_ERR_ALIGN;
@@ -458,7 +458,8 @@ mx_status run_product(const Product &p, void *stream) {
     const DeviceInfo *dev = nullptr;
     const mx_status st = device_or_error(&dev);
     if (st != MX_OK) return st;
-    const cudaError_t e = launch_product(p, *dev, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = few_rows(p) ? launch_few(p, *dev, st_) : launch_product(p, *dev, st_);
     return e == cudaErrorNotSupported ? MX_ERR_UNSUPPORTED : from_cuda(e);
 }
 

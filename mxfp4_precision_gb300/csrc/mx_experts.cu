@@ -39,7 +39,7 @@ struct PlanArgs {
     const void *index;
     int64_t n, rows;
     int experts, chunks;
-    int64_t chunk;           // a multiple of 512
+    int64_t chunk;           // a multiple of kChunk
     int32_t *offsets, *counts, *slot, *source;
     uint32_t *chunk_counts;  // [chunks][experts]
     int *status;
@@ -70,22 +70,39 @@ __global__ void __launch_bounds__(kPlanThreads) mx_expert_count_kernel(const __g
         p.chunk_counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = count[e];
 }
 
+// A warp's entries, kGroups times 32 at a time so that their loads are in flight together.
+constexpr int kGroups = 4;
+template <typename I>
+struct Entries {
+    int x[kGroups];
+    __device__ __forceinline__ Entries(const PlanArgs &p, int64_t first) {
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) x[k] = expert_of<I>(p, first + 32 * k + (threadIdx.x & 31));
+    }
+};
+
 template <typename I>
 __global__ void __launch_bounds__(kPlanThreads) mx_expert_plan_kernel(const __grid_constant__ PlanArgs p) {
     griddep_wait();
     griddep_launch_dependents();
     __shared__ uint32_t at[kPlanWarps][MX_EXPERTS_MAX];  // counts, then next rows
     __shared__ uint32_t part[kPlanWarps];
+    __shared__ uint32_t begin[MX_EXPERTS_MAX], full[MX_EXPERTS_MAX];  // first row of the padding, first row behind it
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
-    for (int i = threadIdx.x; i < kPlanWarps * MX_EXPERTS_MAX; i += kPlanThreads) (&at[0][0])[i] = 0;
-    __syncthreads();
-    const int64_t each = p.chunk / kPlanWarps;  // a multiple of 32
+    const int64_t each = p.chunk / kPlanWarps;  // a multiple of 32 * kGroups
     const int64_t first = blockIdx.x * p.chunk + warp * each;
-    for (int64_t i = lane; i < each; i += 32) {
-        const int x = expert_of<I>(p, first + i);
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, x);
-        if (x >= 0 && lane == __ffs(same) - 1) at[warp][x] += __popc(same);
-        __syncwarp();
+    const Entries<I> head(p, first);
+    for (int i = lane; i < p.experts; i += 32) at[warp][i] = 0;
+    __syncwarp();
+    for (int64_t i = 0; i < each; i += 32 * kGroups) {
+        const Entries<I> now = i == 0 ? head : Entries<I>(p, first + i);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int x = now.x[k];
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, x);
+            if (x >= 0 && lane == __ffs(same) - 1) at[warp][x] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // Entries of expert e in the chunks before this one, and in all.
@@ -123,6 +140,8 @@ __global__ void __launch_bounds__(kPlanThreads) mx_expert_plan_kernel(const __gr
             p.offsets[e] = static_cast<int32_t>(start);
             p.counts[e] = static_cast<int32_t>(total);
         }
+        begin[e] = start + total;
+        full[e] = start + size;
         uint32_t next = start + before;
 #pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) {
@@ -130,37 +149,42 @@ __global__ void __launch_bounds__(kPlanThreads) mx_expert_plan_kernel(const __gr
             at[w][e] = next;
             next += v;
         }
-        // This expert's padding rows.
-        if (e % gridDim.x == blockIdx.x)
-            for (uint32_t r = start + total; r < start + size && r < p.rows; ++r) p.source[r] = -1;
     }
     if (threadIdx.x == 0 && blockIdx.x == 0) p.offsets[p.experts] = static_cast<int32_t>(used);
     __syncthreads();
-    for (int64_t i = lane; i < each; i += 32) {
-        const int x = expert_of<I>(p, first + i);
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, x);
-        int32_t row = -1;
-        if (x >= 0) row = static_cast<int32_t>(at[warp][x] + __popc(same & ((1u << lane) - 1u)));
-        __syncwarp();
-        if (x >= 0 && lane == __ffs(same) - 1) at[warp][x] += __popc(same);
-        __syncwarp();
-        if (first + i < p.n) {
-            p.slot[first + i] = row;
-            if (row >= 0 && row < p.rows) p.source[row] = static_cast<int32_t>(first + i);
+    for (int64_t i = 0; i < each; i += 32 * kGroups) {
+        const Entries<I> now = i == 0 ? head : Entries<I>(p, first + i);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int x = now.x[k];
+            const int64_t entry = first + i + 32 * k + lane;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, x);
+            int32_t row = -1;
+            if (x >= 0) row = static_cast<int32_t>(at[warp][x] + __popc(same & ((1u << lane) - 1u)));
+            __syncwarp();
+            if (x >= 0 && lane == __ffs(same) - 1) at[warp][x] += __popc(same);
+            __syncwarp();
+            if (entry < p.n) {
+                p.slot[entry] = row;
+                if (row >= 0 && row < p.rows) p.source[row] = static_cast<int32_t>(entry);
+            }
         }
     }
-    // Rows behind the last segment.
+    // Padding rows (a warp takes an expert's), and the rows behind the last segment.
+    for (int i = blockIdx.x * kPlanWarps + warp; i < p.experts; i += gridDim.x * kPlanWarps)
+        for (uint32_t r = begin[i] + lane; r < full[i] && r < p.rows; r += 32) p.source[r] = -1;
     for (int64_t r = used + static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x; r < p.rows;
          r += static_cast<int64_t>(gridDim.x) * kPlanThreads)
         p.source[r] = -1;
 }
 
 // ---------------------------------------------------------------- rows in
-// A warp takes one token's strip of 256 columns (a 32-column block is four
-// lanes), reads it once, encodes it once and stores it to each of the token's rows;
-// bound by memory.  Blocks behind those of the tokens zero the rows without a token.
+// A warp takes one token's strip of 512 columns, a lane 16 of them (two lanes a block), reads it
+// once, encodes it once and stores it to each of the token's rows; bound by memory.
+// Blocks before those of the tokens zero the rows without a token.
 constexpr int kWarps = 8;
 constexpr int kZeroRows = 8;  // rows a warp looks through for padding
+constexpr int kStrip = 512;
 
 struct RowsArgs {
     const uint8_t *x, *rows, *res;
@@ -172,7 +196,7 @@ struct RowsArgs {
     int64_t T, P;
     uint32_t K;
     int picks, strips;
-    uint32_t tiles;  // blocks that hold tokens
+    uint32_t zeros;  // blocks that look for rows without a token
     bool aligned32, aligned_out;
     int *status;
 };
@@ -181,55 +205,89 @@ __device__ __forceinline__ bool there(const RowsArgs &p, int32_t slot) {
     return static_cast<uint32_t>(slot) < static_cast<uint64_t>(p.P);
 }
 
-// Codes and scale byte of the lane's eight columns, kept to be stored to several rows.
-struct Codes8 {
-    uint32_t w[2];
-    uint32_t scale;
+// The lane's 16 columns: those from 8 col on, and whether each eight are inside the row.
+struct Lane16 {
+    uint32_t col;
+    bool in0, in1;
 };
-__device__ __forceinline__ Codes8 codes8(int fmt, const V8 &a) {
-    float f[8];
-    floats_of(a, f);
-    float m = enc::absmax2_nan(enc::absmax3_nan(f[0], f[1], f[2]), enc::absmax3_nan(f[3], f[4], f[5]));
-    m = enc::absmax3_nan(m, f[6], f[7]);
-    m = enc::absmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = enc::absmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    float inv;
-    Codes8 r;
-    r.scale = fmt == kEncMX8 ? enc::scale_of_e4m3(m, inv) : enc::scale_of(m, inv);
-    V8 q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q.v[i] = mul2(a.v[i], same2(inv));
-    floats_of(q, f);
-    if (fmt == kEncMX8) {
-        r.w[0] = enc::cvt_e4m3x4(f[0], f[1], f[2], f[3]);
-        r.w[1] = enc::cvt_e4m3x4(f[4], f[5], f[6], f[7]);
-    } else {
-        r.w[0] = enc::cvt_e2m1x8(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]);
-        r.w[1] = 0;
-    }
-    if (r.scale == 0xFFu) r.w[0] = r.w[1] = 0;
-    return r;
+__device__ __forceinline__ Lane16 lane16(const RowsArgs &p, uint32_t strip) {
+    const uint32_t col = strip * kStrip + 16 * (threadIdx.x & 31);
+    return {col, col < p.K, col + 8 < p.K};
+}
+template <typename X>
+__device__ __forceinline__ void load(Raw8<X> (&r)[2], const uint8_t *row, const Lane16 &at, bool aligned32) {
+    zero8(r[0]);
+    zero8(r[1]);
+    if (at.in0) load8(r[0], row + static_cast<size_t>(at.col) * X::kBytes, aligned32);
+    if (at.in1) load8(r[1], row + static_cast<size_t>(at.col + 8) * X::kBytes, aligned32);
 }
 
-// The lane's eight columns (chunk c) of a row of the output: bf16, codes and scale byte; all
-// lanes of a warp on one row.
-__device__ __forceinline__ void put8(const RowsArgs &p, int64_t row, uint32_t c, bool in, const V8 &a, const Codes8 &q) {
-    if (in && p.y.p != nullptr) store8<BF16>(p.y, p.y.p + (row * p.K + 8 * c) * 2, a, true, p.status);
+// The lane's 16 columns of an output row, kept to be stored to several rows: bf16, codes, scale byte.
+struct Packed16 {
+    uint32_t y[8], w[4], scale;
+};
+__device__ __forceinline__ void pack(Packed16 &q, const RowsArgs &p, const V8 &a, const V8 &b) {
+    Raw8<BF16> r;
+    from_v8(r, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q.y[i] = r.w[i];
+    from_v8(r, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q.y[4 + i] = r.w[i];
     if (p.enc.fmt == kEncNone) return;
-    const EncodedRow at = encoded_row(p.enc, row);
-    if (in) {
-        if (p.enc.fmt == kEncMX8) {
-            uint8_t *d = at.codes + 8u * c;
-            if (MX_STORE_OK(d, 8, p.enc.codes.p, p.enc.codes.bytes, p.status))
-                *reinterpret_cast<uint2 *>(d) = make_uint2(q.w[0], q.w[1]);
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2(a.v[i], f[2 * i], f[2 * i + 1]), unpack2(b.v[i], f[8 + 2 * i], f[9 + 2 * i]);
+    float m = enc::absmax2_nan(f[0], f[1]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = enc::absmax3_nan(m, f[2 * i], f[2 * i + 1]);
+    m = enc::absmax2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    float inv;
+    q.scale = p.enc.fmt == kEncMX8 ? enc::scale_of_e4m3(m, inv) : enc::scale_of(m, inv);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] *= inv;
+    if (p.enc.fmt == kEncMX8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q.w[i] = enc::cvt_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            q.w[i] = enc::cvt_e2m1x8(f[8 * i], f[8 * i + 1], f[8 * i + 2], f[8 * i + 3], f[8 * i + 4], f[8 * i + 5], f[8 * i + 6], f[8 * i + 7]);
+    }
+    if (q.scale == 0xFFu) q.w[0] = q.w[1] = q.w[2] = q.w[3] = 0;
+}
+__device__ __forceinline__ void put(const RowsArgs &p, int64_t row, const Lane16 &at, const Packed16 &q) {
+    if (p.y.p != nullptr) {
+        uint8_t *d = p.y.p + (row * p.K + at.col) * 2;
+        if (at.in1 && p.aligned_out) {
+            if (MX_STORE_OK(d, 32, p.y.p, p.y.bytes, p.status))
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(d), "r"(q.y[0]), "r"(q.y[1]), "r"(q.y[2]),
+                             "r"(q.y[3]), "r"(q.y[4]), "r"(q.y[5]), "r"(q.y[6]), "r"(q.y[7])
+                             : "memory");
         } else {
-            uint8_t *d = at.codes + 4u * c;
-            if (MX_STORE_OK(d, 4, p.enc.codes.p, p.enc.codes.bytes, p.status)) *reinterpret_cast<uint32_t *>(d) = q.w[0];
+            if (at.in0 && MX_STORE_OK(d, 16, p.y.p, p.y.bytes, p.status))
+                reinterpret_cast<uint4 *>(d)[0] = make_uint4(q.y[0], q.y[1], q.y[2], q.y[3]);
+            if (at.in1 && MX_STORE_OK(d + 16, 16, p.y.p, p.y.bytes, p.status))
+                reinterpret_cast<uint4 *>(d)[1] = make_uint4(q.y[4], q.y[5], q.y[6], q.y[7]);
         }
     }
-    if ((threadIdx.x & 3) == 0) {
-        uint8_t *d = at.scales + (c >> 4) * 512u + ((c >> 2) & 3u);
-        if (MX_STORE_OK(d, 1, p.enc.scales.p, p.enc.scales.bytes, p.status)) *d = static_cast<uint8_t>(in ? q.scale : 0u);
+    if (p.enc.fmt == kEncNone) return;
+    // Encoded rows are whole blocks: both eights are inside or neither.
+    const EncodedRow to = encoded_row(p.enc, row);
+    if (at.in1) {
+        if (p.enc.fmt == kEncMX8) {
+            uint8_t *d = to.codes + at.col;
+            if (MX_STORE_OK(d, 16, p.enc.codes.p, p.enc.codes.bytes, p.status))
+                *reinterpret_cast<uint4 *>(d) = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
+        } else {
+            uint8_t *d = to.codes + at.col / 2;
+            if (MX_STORE_OK(d, 8, p.enc.codes.p, p.enc.codes.bytes, p.status)) *reinterpret_cast<uint2 *>(d) = make_uint2(q.w[0], q.w[1]);
+        }
+    }
+    const uint32_t block = at.col >> 5;
+    if ((threadIdx.x & 1) == 0 && block < 4 * static_cast<uint32_t>(p.enc.katoms)) {
+        uint8_t *d = to.scales + (block >> 2) * 512u + (block & 3u);
+        if (MX_STORE_OK(d, 1, p.enc.scales.p, p.enc.scales.bytes, p.status)) *d = static_cast<uint8_t>(at.in0 ? q.scale : 0u);
     }
 }
 
@@ -238,13 +296,10 @@ __device__ __forceinline__ void zero_rows(const RowsArgs &p, int64_t n) {
     const int lane = threadIdx.x & 31;
     const int64_t first = n * kZeroRows;
     const bool free_row = lane < kZeroRows && first + lane < p.P && p.source[first + lane] < 0;
+    const Packed16 none{};
     for (uint32_t mask = __ballot_sync(0xFFFFFFFFu, free_row); mask != 0; mask &= mask - 1) {
         const int64_t row = first + __ffs(mask) - 1;
-        const Codes8 none{{0, 0}, 0};
-        for (int s = 0; s < p.strips; ++s) {
-            const uint32_t c = static_cast<uint32_t>(s) * 32 + lane;
-            put8(p, row, c, 8 * c < p.K, zero_v8(), none);
-        }
+        for (int s = 0; s < p.strips; ++s) put(p, row, lane16(p, s), none);
     }
 }
 
@@ -252,31 +307,36 @@ template <typename X>
 __global__ void __launch_bounds__(32 * kWarps) mx_expert_dispatch_kernel(const __grid_constant__ RowsArgs p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (blockIdx.x >= p.tiles) {
-        zero_rows(p, static_cast<int64_t>(blockIdx.x - p.tiles) * kWarps + warp);
+    const int warp = threadIdx.x >> 5;
+    if (blockIdx.x < p.zeros) {
+        zero_rows(p, static_cast<int64_t>(blockIdx.x) * kWarps + warp);
         return;
     }
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x - p.zeros) * kWarps + warp;
     const int64_t t = unit / p.strips;
     if (t >= p.T) return;
-    const uint32_t c = static_cast<uint32_t>(unit - t * p.strips) * 32 + lane;
-    const bool in = 8 * c < p.K;
-    Raw8<X> r;
-    zero8(r);
-    if (in) load8(r, p.x + t * p.x_pitch + static_cast<size_t>(8 * c) * X::kBytes, p.aligned32);
-    const V8 a = to_v8(r);
-    Codes8 q{{0, 0}, 0};
-    if (p.enc.fmt != kEncNone) q = codes8(p.enc.fmt, a);
-    for (int j = 0; j < p.picks; ++j) {
-        const int32_t s = p.slot[t * p.picks + j];
-        if (there(p, s)) put8(p, s, c, in, a, q);
+    const Lane16 at = lane16(p, static_cast<uint32_t>(unit - t * p.strips));
+    Raw8<X> r[2];
+    load(r, p.x + t * p.x_pitch, at, p.aligned32);
+    // The first four rows' numbers are on their way beside the columns.
+    int32_t s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = j < p.picks ? p.slot[t * p.picks + j] : -1;
+    Packed16 q;
+    pack(q, p, to_v8(r[0]), to_v8(r[1]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (there(p, s[j])) put(p, s[j], at, q);
+    for (int j = 4; j < p.picks; ++j) {
+        const int32_t row = p.slot[t * p.picks + j];
+        if (there(p, row)) put(p, row, at, q);
     }
 }
 
 // ---------------------------------------------------------------- rows out
 // A warp takes one token's strip of 256 columns and adds up to four of its rows at
 // a time, all in flight; bound by memory.
+constexpr int kOutStrip = 256;
 template <typename R, typename S, typename Y>
 __global__ void __launch_bounds__(32 * kWarps) mx_expert_combine_kernel(const __grid_constant__ RowsArgs p) {
     griddep_wait();
@@ -319,25 +379,24 @@ __global__ void __launch_bounds__(32 * kWarps) mx_expert_combine_kernel(const __
 }
 
 // ---------------------------------------------------------------- gradient of rows out
-// A block takes one token: dy is read once for up to four of its choices, whose rows'
-// gradients leave as they are made; the products with the rows are added up over the
-// block in a fixed order.  Blocks behind those of the tokens zero the rows without a token.
-constexpr int kAtOnce = 4;
-constexpr int kGradThreads = 256;
-
+// A block takes one token, a warp a strip of 512 columns at a time: dy and up to four of the
+// token's rows (two of fp32, which fill the registers) are read together, the rows' gradients leave as they are made, and the products with
+// the rows are added up over the block in a fixed order.  Blocks before those of the tokens
+// zero the rows without a token.
 template <typename D, typename R>
-__global__ void __launch_bounds__(kGradThreads) mx_expert_combine_backward_kernel(const __grid_constant__ RowsArgs p) {
+__global__ void __launch_bounds__(32 * kWarps, 2) mx_expert_combine_backward_kernel(const __grid_constant__ RowsArgs p) {
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (blockIdx.x >= p.tiles) {
-        zero_rows(p, static_cast<int64_t>(blockIdx.x - p.tiles) * warps + warp);
+    if (blockIdx.x < p.zeros) {
+        zero_rows(p, static_cast<int64_t>(blockIdx.x) * warps + warp);
         return;
     }
-    __shared__ float part[kGradThreads / 32][kAtOnce];
-    const int64_t t = blockIdx.x;
+    constexpr int kAtOnce = R::kBytes == 4 ? 2 : 4;
+    __shared__ float part[kWarps][kAtOnce];
+    const int64_t t = blockIdx.x - p.zeros;
     const uint8_t *dy = p.x + t * p.x_pitch;
-    const uint32_t chunks = static_cast<uint32_t>(p.strips) * 32;
+    const bool writes = p.y.p != nullptr || p.enc.fmt != kEncNone, dots = p.dweights.p != nullptr;
     for (int j0 = 0; j0 < p.picks; j0 += kAtOnce) {
         int32_t s[kAtOnce];
         float w[kAtOnce];
@@ -345,43 +404,44 @@ __global__ void __launch_bounds__(kGradThreads) mx_expert_combine_backward_kerne
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
             const int64_t i = t * p.picks + j0 + k;
-            s[k] = j0 + k < p.picks ? p.slot[i] : -1;
+            const bool has = j0 + k < p.picks;
+            s[k] = has ? p.slot[i] : -1;
+            w[k] = has ? p.weights[i] : 0.0f;
             if (!there(p, s[k])) s[k] = -1;
-            w[k] = s[k] >= 0 ? p.weights[i] : 0.0f;
             dot[k] = 0;
         }
-        for (uint32_t c = threadIdx.x; c < chunks; c += blockDim.x) {
-            const bool in = 8 * c < p.K;
-            Raw8<D> dr;
-            Raw8<R> r[kAtOnce];
-            zero8(dr);
-            if (in) load8(dr, dy + static_cast<size_t>(8 * c) * D::kBytes, p.aligned32);
-            if (p.dweights.p != nullptr) {
+        for (int strip = warp; strip < p.strips; strip += warps) {
+            const Lane16 at = lane16(p, strip);
+            Raw8<D> dr[2];
+            load(dr, dy, at, p.aligned32);
+            Raw8<R> r[kAtOnce][2];
+            if (dots) {
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {
-                    zero8(r[k]);
-                    if (in && s[k] >= 0) load8(r[k], p.rows + s[k] * p.rows_pitch + static_cast<size_t>(8 * c) * R::kBytes, p.aligned32);
+                    zero8(r[k][0]);
+                    zero8(r[k][1]);
+                    if (s[k] >= 0) load(r[k], p.rows + s[k] * p.rows_pitch, at, p.aligned32);
                 }
             }
-            const V8 d = to_v8(dr);
+            const V8 d0 = to_v8(dr[0]), d1 = to_v8(dr[1]);
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 if (s[k] < 0) continue;
-                if (p.dweights.p != nullptr) {
-                    const V8 a = to_v8(r[k]);
+                if (dots) {
+                    const V8 a = to_v8(r[k][0]), b = to_v8(r[k][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) dot[k] = fma2(a.v[i], d.v[i], dot[k]);
+                    for (int i = 0; i < 4; ++i) dot[k] = fma2(b.v[i], d1.v[i], fma2(a.v[i], d0.v[i], dot[k]));
                 }
-                if (p.y.p == nullptr && p.enc.fmt == kEncNone) continue;
-                V8 g;
+                if (!writes) continue;
+                V8 a, b;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) g.v[i] = mul2(d.v[i], same2(w[k]));
-                Codes8 q{{0, 0}, 0};
-                if (p.enc.fmt != kEncNone) q = codes8(p.enc.fmt, g);
-                put8(p, s[k], c, in, g, q);
+                for (int i = 0; i < 4; ++i) a.v[i] = mul2(d0.v[i], same2(w[k])), b.v[i] = mul2(d1.v[i], same2(w[k]));
+                Packed16 q;
+                pack(q, p, a, b);
+                put(p, s[k], at, q);
             }
         }
-        if (p.dweights.p == nullptr) continue;
+        if (!dots) continue;
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
             const float v = sum_lanes(sum2(dot[k]));
@@ -406,7 +466,7 @@ RowsArgs rows_args(const ExpertRows &r, const DeviceInfo &dev) {
     p.P = r.rows;
     p.K = static_cast<uint32_t>(r.K);
     p.picks = static_cast<int>(r.picks);
-    p.strips = static_cast<int>((r.K + 255) / 256);
+    p.strips = static_cast<int>((r.K + kStrip - 1) / kStrip);
     p.status = dev.status;
     return p;
 }
@@ -425,7 +485,7 @@ cudaError_t launch_plan(const PlanArgs &p, cudaStream_t stream) {
 
 int64_t chunk_entries(int64_t n) {
     const int64_t most = (n + kMaxChunks - 1) / kMaxChunks;
-    return most <= kChunk ? kChunk : (most + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+    return (std::max<int64_t>(1, most) + kChunk - 1) / kChunk * kChunk;
 }
 
 template <typename R, typename S>
@@ -468,9 +528,10 @@ cudaError_t launch_expert_dispatch(const RowIn &x, const ExpertRows &r, void *y,
     p.y = {static_cast<uint8_t *>(y), static_cast<size_t>(r.rows) * r.K * 2};
     p.enc = row_encoded(e, r.rows, r.K);
     p.aligned32 = aligned32(x.p);
-    const int64_t tiles = (r.T * p.strips + kWarps - 1) / kWarps, grid = tiles + zero_blocks(p, kWarps);
+    p.aligned_out = y == nullptr || (aligned32(y) && r.K % 16 == 0);
+    const int64_t zeros = zero_blocks(p, kWarps), grid = zeros + (r.T * p.strips + kWarps - 1) / kWarps;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    p.tiles = static_cast<uint32_t>(tiles);
+    p.zeros = static_cast<uint32_t>(zeros);
     return x.f32 ? launch_dependent(mx_expert_dispatch_kernel<F32>, grid, 32 * kWarps, 0, stream, p)
                  : launch_dependent(mx_expert_dispatch_kernel<BF16>, grid, 32 * kWarps, 0, stream, p);
 }
@@ -486,6 +547,7 @@ cudaError_t launch_expert_combine(const RowIn &rows, const ExpertRows &r, const 
     p.y = {static_cast<uint8_t *>(y), static_cast<size_t>(r.T) * r.K * (y_f32 ? 4 : 2)};
     p.aligned32 = aligned32(rows.p) && aligned32(res.p);
     p.aligned_out = aligned32(y);
+    p.strips = static_cast<int>((r.K + kOutStrip - 1) / kOutStrip);
     const int64_t grid = (r.T * p.strips + kWarps - 1) / kWarps;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
     if (rows.f32)
@@ -506,12 +568,13 @@ cudaError_t launch_expert_combine_backward(const RowIn &dy, const RowIn &rows, c
     p.dweights = {reinterpret_cast<uint8_t *>(dweights), static_cast<size_t>(r.T) * r.picks * 4};
     p.enc = row_encoded(e, r.rows, r.K);
     p.aligned32 = aligned32(dy.p) && aligned32(rows.p);
-    // As many threads as a row has chunks of 8 columns, at most a block.
-    const int threads = std::min(kGradThreads, p.strips * 32);
+    p.aligned_out = drows == nullptr || (aligned32(drows) && r.K % 16 == 0);
+    // As many warps as a row has strips, at most a block.
+    const int warps = std::min(kWarps, p.strips), threads = 32 * warps;
     const bool writes = drows != nullptr || e.fmt != kEncNone;
-    const int64_t grid = r.T + (writes ? zero_blocks(p, threads / 32) : 0);
+    const int64_t zeros = writes ? zero_blocks(p, warps) : 0, grid = zeros + r.T;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    p.tiles = static_cast<uint32_t>(r.T);
+    p.zeros = static_cast<uint32_t>(zeros);
     if (dy.f32)
         return rows.f32 ? launch_dependent(mx_expert_combine_backward_kernel<F32, F32>, grid, threads, 0, stream, p)
                         : launch_dependent(mx_expert_combine_backward_kernel<F32, BF16>, grid, threads, 0, stream, p);

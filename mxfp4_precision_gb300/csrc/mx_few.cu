@@ -1,0 +1,417 @@
+// mx_few.cu -- the products of mx_product.cu for few rows of A (tokens of a
+// decoding step), dense and by expert.
+//
+// With a handful of rows the product is a read of B: 2 M N K operations over
+// N K / 2 bytes.  Tiles of 256 columns leave most SMs without one (4096 columns:
+// 16 pairs) and walk their whole contraction one stage after the other.  Here a
+// block takes 32 columns and splits the contraction over its warps, four blocks of 32
+// elements at a time, so that all of B is on its way at once; the warps' sums
+// are joined in shared memory in their order.
+//
+// A warp multiplies 32 lines of B by 8 rows of A per mma.sync.m16n8k16 (f16 in, fp32
+// out): E2M1 and E4M3 values are f16 values, so the products are exact, and the
+// instruction's rate does not matter where memory bounds the kernel.  Which element of
+// the contraction takes which of its places is free as long as both operands
+// agree, so lane c of four takes elements 8 c .. 8 c + 7 of a block: one load, and
+// two instructions to a block, after which the sums get the block's scales.
+#include <algorithm>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "mx_act.cuh"
+#include "mx_encode.cuh"
+#include "mx_internal.h"
+#include "mx_ptx.cuh"
+#include "mx_rows.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kColumns = 32;  // of a block: one block of an encoded row
+// Dense: one block an SM and all of B at once.  By expert: several smaller ones, since each first looks up
+// its expert.
+constexpr int kDenseWarps = 16, kExpertWarps = 8;
+
+struct FewArgs {
+    const uint8_t *Aq, *As, *Bq, *Bs;
+    int64_t M, N;         // rows of A (by expert: the capacity of all segments)
+    int64_t line_bytes;   // codes of a line
+    int64_t katoms, b_groups;
+    int blocks;           // blocks of 32 elements of a line
+    int experts;          // 0: dense
+    const int32_t *offsets, *counts;
+    const uint8_t *bias, *res;
+    int64_t res_pitch;    // bytes
+    uint8_t *y, *z, *codes, *scales;
+    size_t y_bytes, z_bytes, codes_bytes, scales_bytes;
+    int64_t out_katoms;
+    int act, bias_f32, res_f32, y_f32, fmt;
+    int *status;
+};
+
+// Eight elements of a line as four f16 pairs.
+template <bool FP8>
+struct Codes;
+template <>
+struct Codes<false> {
+    static constexpr int kBytes = 4;
+    uint32_t w;
+    __device__ __forceinline__ void load(const uint8_t *p) { w = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ void clear() { w = 0; }
+    __device__ __forceinline__ void values(uint32_t (&h)[4]) const {
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "mov.b32 {a, b, c, d}, %4;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+            : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+            : "r"(w));
+    }
+};
+template <>
+struct Codes<true> {
+    static constexpr int kBytes = 8;
+    uint2 w;
+    __device__ __forceinline__ void load(const uint8_t *p) { w = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void clear() { w = make_uint2(0, 0); }
+    __device__ __forceinline__ void values(uint32_t (&h)[4]) const {
+        asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+            "mov.b32 {a, b}, %4;\n\t"
+            "mov.b32 {c, d}, %5;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+            : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+            : "r"(w.x), "r"(w.y));
+    }
+};
+
+// D += A B: A 16 x 16 (a[0], a[2]: row r, a[1], a[3]: row r + 8), B 16 x 8.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// v 2^(a - 127) 2^(b - 127) for scale bytes a, b (255: NaN), in two steps of half the
+// exponent each, so that nothing overflows that the result does not.
+__device__ __forceinline__ float scaled(float v, uint32_t a, uint32_t b) {
+    const uint32_t e = a + b, half = e >> 1;
+    v = (v * __uint_as_float(half << 23)) * __uint_as_float((e - half) << 23);
+    return a == 255u || b == 255u ? __uint_as_float(0x7FC00000u) : v;
+}
+
+// Where the scale bytes of a line's blocks 0 .. 3 lie; those of 4 n .. 4 n + 3 are 512 n further.
+__device__ __forceinline__ const uint8_t *scales_of(const uint8_t *s, int64_t katoms, int64_t line) {
+    return s + (line >> 7) * katoms * 512 + (line & 31) * 16 + ((line & 127) >> 5) * 4;
+}
+// Whether four scale bytes are all in 63 .. 190: two such powers of two have a product, -128 ..
+// 126, that fp32 holds.  (b + 1 has one of its upper two bits then, and not both.)
+__device__ __forceinline__ bool moderate(uint32_t s) {
+    const uint32_t x = s + 0x01010101u;
+    return ((x ^ (x << 1)) & 0x80808080u) == 0x80808080u;
+}
+__device__ __forceinline__ float power(uint32_t s, int j) { return __uint_as_float(((s >> (8 * j)) & 0xFFu) << 23); }
+constexpr uint32_t kOnes = 0x7F7F7F7Fu;  // four scales of 1
+
+__device__ __forceinline__ float activated(float x, int which) {
+    const uint64_t v = act::same2(x);
+    uint64_t r = v;
+    switch (which) {
+        case act::kRelu: r = act::value2<act::kRelu>(v); break;
+        case act::kRelu2: r = act::value2<act::kRelu2>(v); break;
+        case act::kGelu: r = act::value2<act::kGelu>(v); break;
+        case act::kGeluTanh: r = act::value2<act::kGeluTanh>(v); break;
+        case act::kSilu: r = act::value2<act::kSilu>(v); break;
+        default: break;
+    }
+    float a, b;
+    act::unpack2(r, a, b);
+    return a;
+}
+__device__ __forceinline__ float element(const uint8_t *p, int64_t i, bool f32) {
+    if (f32) return reinterpret_cast<const float *>(p)[i];
+    return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << 16);
+}
+__device__ __forceinline__ void put_bf16(uint8_t *base, int64_t i, float v, size_t bytes, int *status) {
+    uint8_t *p = base + 2 * i;
+    if (MX_STORE_OK(p, 2, base, bytes, status)) *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(rows::bf16x2(v, 0.0f));
+}
+
+// One row's 32 columns, a lane each: v is the product (0 in padding).  Whole warps.
+__device__ __forceinline__ void finish(const FewArgs &g, int64_t row, int expert, int col, bool real, float v) {
+    const bool in = col < g.N;
+    const int64_t e = row * g.N + col;
+    if (real && in && g.bias != nullptr) v += element(g.bias, expert * g.N + col, g.bias_f32);
+    if (g.z != nullptr && in) put_bf16(g.z, e, v, g.z_bytes, g.status);
+    v = activated(v, g.act);
+    if (g.res != nullptr && in) v += element(g.res + row * g.res_pitch, col, g.res_f32);
+    if (g.y != nullptr && in) {
+        if (g.y_f32) {
+            uint8_t *p = g.y + 4 * e;
+            if (MX_STORE_OK(p, 4, g.y, g.y_bytes, g.status)) *reinterpret_cast<float *>(p) = v;
+        } else {
+            put_bf16(g.y, e, v, g.y_bytes, g.status);
+        }
+    }
+    if (g.fmt == kEncNone) return;
+    const int lane = threadIdx.x & 31;
+    float top = fabsf(v);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = enc::absmax2_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float inv;
+    const bool fp8 = g.fmt == kEncMX8;
+    const uint32_t s = fp8 ? enc::scale_of_e4m3(top, inv) : enc::scale_of(top, inv);
+    const float q = v * inv;
+    if (fp8) {
+        const uint32_t c = s == 0xFFu ? 0u : enc::cvt_e4m3x4(q, 0.0f, 0.0f, 0.0f) & 0xFFu;
+        if (in && MX_STORE_OK(g.codes + e, 1, g.codes, g.codes_bytes, g.status)) g.codes[e] = static_cast<uint8_t>(c);
+    } else {
+        const float next = __shfl_down_sync(0xFFFFFFFFu, q, 1);
+        const uint32_t c = s == 0xFFu ? 0u : enc::cvt_e2m1x8(q, next, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f) & 0xFFu;
+        if (in && (lane & 1) == 0 && MX_STORE_OK(g.codes + e / 2, 1, g.codes, g.codes_bytes, g.status))
+            g.codes[e / 2] = static_cast<uint8_t>(c);
+    }
+    if (lane == 0) {
+        uint8_t *p = g.scales + enc::scale_offset(row, col / 32, g.out_katoms);
+        if (MX_STORE_OK(p, 1, g.scales, g.scales_bytes, g.status)) *p = static_cast<uint8_t>(in ? s : 0u);
+    }
+}
+
+// Zeroes the block's columns of rows first .. end - 1 (scales alone: the padding of a dense
+// output's scales).  A thread per (row, 8 columns).
+__device__ __forceinline__ void zero_rows(const FewArgs &g, int col0, int64_t first, int64_t end, bool scales_alone) {
+    for (int64_t i = threadIdx.x; i < (end - first) * 4; i += blockDim.x) {
+        const int64_t row = first + i / 4;
+        const int part = static_cast<int>(i & 3), col = col0 + 8 * part;
+        if (col < g.N && !scales_alone) {
+            const int64_t e = row * g.N + col;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            if (g.z != nullptr && MX_STORE_OK(g.z + 2 * e, 16, g.z, g.z_bytes, g.status)) *reinterpret_cast<uint4 *>(g.z + 2 * e) = none;
+            if (g.y != nullptr)
+                for (int k = 0; k < (g.y_f32 ? 2 : 1); ++k) {
+                    uint8_t *p = g.y + (g.y_f32 ? 4 : 2) * e + 16 * k;
+                    if (MX_STORE_OK(p, 16, g.y, g.y_bytes, g.status)) *reinterpret_cast<uint4 *>(p) = none;
+                }
+            if (g.fmt == kEncMX8 && MX_STORE_OK(g.codes + e, 8, g.codes, g.codes_bytes, g.status))
+                *reinterpret_cast<uint2 *>(g.codes + e) = make_uint2(0, 0);
+            if (g.fmt == kEncMX4 && MX_STORE_OK(g.codes + e / 2, 4, g.codes, g.codes_bytes, g.status))
+                *reinterpret_cast<uint32_t *>(g.codes + e / 2) = 0;
+        }
+        if (part == 0 && g.fmt != kEncNone) {
+            uint8_t *p = g.scales + enc::scale_offset(row, col0 / 32, g.out_katoms);
+            if (MX_STORE_OK(p, 1, g.scales, g.scales_bytes, g.status)) *p = 0;
+        }
+    }
+}
+
+// 32 columns (blockIdx.x; those behind the last are padding of the scales) of all rows, or by
+// expert of 128 rows (blockIdx.y), which are one expert's or lie behind the last segment.
+template <bool FP8, int NT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == kExpertWarps ? 3 : 1) mx_few_kernel(const __grid_constant__ FewArgs g) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int col0 = static_cast<int>(blockIdx.x) * kColumns;
+    int64_t first = 0, real = g.M;  // rows: taken by tokens up to `real`
+    int expert = 0;
+    __shared__ float part[WARPS][8 * NT][kColumns + 1];
+    if (WARPS == kExpertWarps) {
+        __shared__ int found, taken;
+        first = static_cast<int64_t>(blockIdx.y) * 128;
+        if (threadIdx.x == 0) found = -1;
+        __syncthreads();
+        for (int e = threadIdx.x; e < g.experts; e += 32 * WARPS) {
+            const int begin = g.offsets[e];
+            if (begin <= first && first < g.offsets[e + 1]) found = e, taken = g.counts[e] - static_cast<int>(first - begin);
+        }
+        __syncthreads();
+        expert = max(found, 0);
+        real = found < 0 ? first : first + max(0, min(taken, 128));
+        zero_rows(g, col0, real, first + 128, false);
+    } else if (g.fmt != kEncNone) {
+        zero_rows(g, col0, g.M, (g.M + 127) / 128 * 128, true);
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    using E = Codes<FP8>;
+    const bool any = col0 < g.N;
+    const int64_t line0 = expert * g.N + col0;
+    const uint8_t *bs = g.Bs + expert * g.b_groups * g.katoms * 512;
+    // Lines r, r + 8, r + 16, r + 24 of B; those beyond the last column stand on line 0 and are
+    // not stored.
+    const uint8_t *bq[4], *sb_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int line = col0 + 8 * i + r < g.N ? 8 * i + r : 0;
+        bq[i] = g.Bq + (line0 + line) * g.line_bytes + c * E::kBytes;
+        sb_at[i] = scales_of(bs, g.katoms, col0 + line);
+    }
+    for (int64_t row0 = first; row0 < real; row0 += 8 * NT) {
+        // Rows r of A (scales: rows 2 c, 2 c + 1); those beyond the last likewise.
+        const uint8_t *aq[NT], *sa_at[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int64_t row = row0 + 8 * t;
+            aq[t] = g.Aq + min(row + r, real - 1) * g.line_bytes + c * E::kBytes;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) sa_at[t][k] = scales_of(g.As, g.katoms, min(row + 2 * c + k, real - 1));
+        }
+        float sum[2][NT][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sum[i][t][0] = sum[i][t][1] = sum[i][t][2] = sum[i][t][3] = 0.0f;
+        for (int n = warp; any && 4 * n < g.blocks; n += WARPS) {
+            // Four blocks of 32 elements; the last may be fewer (zeros with scales of 1).
+            const int left = g.blocks - 4 * n;
+            const int64_t at = static_cast<int64_t>(n) * 16 * E::kBytes;
+            const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
+            E b[4][4], a[NT][4];
+            uint32_t sb[4], sa[NT][2];
+            bool plain = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sb[i] = *reinterpret_cast<const uint32_t *>(sb_at[i] + 512 * n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    b[i][j].clear();
+                    if (j < left) b[i][j].load(bq[i] + at + j * 4 * E::kBytes);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a[t][j].clear();
+                    if (j < left) a[t][j].load(aq[t] + at + j * 4 * E::kBytes);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    sa[t][k] = *reinterpret_cast<const uint32_t *>(sa_at[t][k] + 512 * n) & keep | kOnes & ~keep;
+                    plain = plain && moderate(sa[t][k]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sb[i] = sb[i] & keep | kOnes & ~keep;
+                plain = plain && moderate(sb[i]);
+            }
+            plain = __all_sync(0xFFFFFFFFu, plain);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t h[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i][j].values(h[i]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    uint32_t x[4];
+                    a[t][j].values(x);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma(d, h[2 * i][0], h[2 * i + 1][0], h[2 * i][1], h[2 * i + 1][1], x[0], x[1]);
+                        mma(d, h[2 * i][2], h[2 * i + 1][2], h[2 * i][3], h[2 * i + 1][3], x[2], x[3]);
+                        if (plain) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                sum[i][t][k] = fmaf(d[k], power(sb[2 * i + (k >> 1)], j) * power(sa[t][k & 1], j), sum[i][t][k]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                sum[i][t][k] += scaled(d[k], (sb[2 * i + (k >> 1)] >> (8 * j)) & 0xFFu, (sa[t][k & 1] >> (8 * j)) & 0xFFu);
+                        }
+                    }
+                }
+            }
+        }
+        // d[k]: line r (k < 2) or r + 8 of the sixteen, row 2 c + (k & 1) of the eight.
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) part[warp][8 * t + 2 * c + (k & 1)][16 * i + 8 * (k >> 1) + r] = sum[i][t][k];
+        __syncthreads();
+        for (int m = warp; m < 8 * NT && row0 + m < real; m += WARPS) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) v += part[w][m][lane];
+            finish(g, row0 + m, expert, col0 + lane, true, v);
+        }
+        __syncthreads();
+    }
+}
+
+template <bool FP8, int NT, int WARPS>
+cudaError_t launch(const FewArgs &g, dim3 grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(32 * WARPS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_few_kernel<FP8, NT, WARPS>, g);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <bool FP8>
+cudaError_t launch_as(const FewArgs &g, dim3 grid, cudaStream_t stream) {
+    if (g.experts > 0) return launch<FP8, 1, kExpertWarps>(g, grid, stream);
+    return g.M > 8 ? launch<FP8, 2, kDenseWarps>(g, grid, stream) : launch<FP8, 1, kDenseWarps>(g, grid, stream);
+}
+
+}  // namespace
+
+// Where the tiles of mx_product.cu (256 columns, at most 76 pairs of SMs at a time) would leave most
+// SMs idle.  Measured, us, these blocks and the tiles (MXFP4): 8 x 4096 x 4096 5.8 and 9.5,
+// 8 x 4096 x 14336 13.2 and 20.8, 16 x 4096 x 14336 17.2 and 20.8; but 8 x 14336 x 4096 (56 tiles)
+// 15.1 and 12.3.  By expert the host knows the capacity alone: up to 128 rows an expert it is 128 times
+// the number of rows (64 experts of 2048 x 2048, 24 rows, 192 tiles: 21.5 and 17.7).
+bool few_rows(const Product &p) {
+    const int64_t n_tiles = (p.N + 255) / 256;
+    if (p.mode == kProductDense) return p.M <= 8 ? n_tiles <= 32 : p.M <= 16 && n_tiles <= 16;
+    return p.mode == kProductRows && p.M <= 128 * p.experts && p.M / 128 * n_tiles <= 32;
+}
+
+cudaError_t launch_few(const Product &p, const DeviceInfo &dev, cudaStream_t stream) {
+    FewArgs g{};
+    g.Aq = static_cast<const uint8_t *>(p.Aq), g.As = static_cast<const uint8_t *>(p.As);
+    g.Bq = static_cast<const uint8_t *>(p.Bq), g.Bs = static_cast<const uint8_t *>(p.Bs);
+    g.M = p.M;
+    g.N = p.N;
+    g.line_bytes = p.fp8 ? p.K : p.K / 2;
+    g.katoms = scale_katoms(p.K);
+    g.b_groups = scale_groups(p.N);
+    g.blocks = static_cast<int>(p.K / 32);
+    g.experts = p.mode == kProductRows ? static_cast<int>(p.experts) : 0;
+    g.offsets = p.offsets;
+    g.counts = p.counts;
+    g.bias = static_cast<const uint8_t *>(p.bias);
+    g.bias_f32 = p.bias_f32;
+    g.res = static_cast<const uint8_t *>(p.res.p);
+    g.res_f32 = p.res.f32;
+    g.res_pitch = p.res.pitch * (p.res.f32 ? 4 : 2);
+    const size_t out = static_cast<size_t>(p.M) * static_cast<size_t>(p.N);
+    g.y = static_cast<uint8_t *>(p.y);
+    g.y_f32 = p.y_f32;
+    g.y_bytes = out * (p.y_f32 ? 4 : 2);
+    g.z = static_cast<uint8_t *>(p.z);
+    g.z_bytes = out * 2;
+    g.fmt = p.enc.fmt;
+    g.codes = static_cast<uint8_t *>(p.enc.codes);
+    g.codes_bytes = p.enc.fmt == kEncMX8 ? out : out / 2;
+    g.scales = static_cast<uint8_t *>(p.enc.scales);
+    g.out_katoms = scale_katoms(p.N);
+    g.scales_bytes = static_cast<size_t>(scale_groups(p.M)) * static_cast<size_t>(g.out_katoms) * 512;
+    g.act = p.act;
+    g.status = dev.status;
+    // Columns up to the end of the scales' padding where there are scales.
+    const int64_t columns = p.enc.fmt == kEncNone ? (p.N + kColumns - 1) / kColumns : g.out_katoms * 4;
+    const dim3 grid(static_cast<unsigned>(columns), static_cast<unsigned>(g.experts > 0 ? p.M / 128 : 1), 1);
+    return p.fp8 ? launch_as<true>(g, grid, stream) : launch_as<false>(g, grid, stream);
+}
+
+}  // namespace mx

@@ -165,6 +165,9 @@ struct Product {
     RowEncode enc;
 };
 cudaError_t launch_product(const Product &p, const DeviceInfo &dev, cudaStream_t stream);
+// Few rows of A (mx_few.cu): whether a product goes there, and its launch.
+bool few_rows(const Product &p);
+cudaError_t launch_few(const Product &p, const DeviceInfo &dev, cudaStream_t stream);
 
 // ---- gradient of bias and activation (mx_act.cu)
 size_t bias_act_backward_ws(int64_t T, int64_t N);

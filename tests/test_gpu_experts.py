@@ -162,7 +162,8 @@ def _rows_case(T, picks, E, N, K, fp8, drop=0.0, skew=0.5, seed=0, scale=-2):
 
 
 @pytest.mark.parametrize("T,picks,E,N,K,drop,skew", [(1, 1, 1, 8, 32, 0, 0), (12, 2, 64, 264, 96, 0, 0.5), (300, 2, 5, 520, 288, 0.1, 1), (700, 3, 6, 256, 1056, 0, 2),
-                                                      (1500, 2, 3, 1032, 544, 0, 0), (40, 8, 512, 64, 64, 0, 0), (600, 1, 4, 136, 128, 0.5, 4), (30, 2, 4, 64, 64, 1.0, 0)])
+                                                      (1500, 2, 3, 1032, 544, 0, 0), (40, 8, 512, 64, 64, 0, 0), (600, 1, 4, 136, 128, 0.5, 4), (30, 2, 4, 64, 64, 1.0, 0),
+                                                      (3, 2, 8, 520, 96, 0, 0), (16, 1, 30, 264, 2080, 0.1, 6), (5, 4, 512, 40, 4128, 0, 1)])
 @pytest.mark.parametrize("fp8", [False, True], ids=["mxfp4", "mxfp8"])
 def test_rows(T, picks, E, N, K, drop, skew, fp8):
     plan, (offsets, counts, slot, source), a, bc, bs, bv = _rows_case(T, picks, E, N, K, fp8, drop, skew, seed=T)
@@ -202,6 +203,15 @@ def test_rows_encoded(fmt):
     y = mx.gemm_experts(*args, bias=bias, act=mx.ACT_SILU, dtype=F32).y
     out = mx.gemm_experts(*args, bias=bias, act=mx.ACT_SILU, want_y=False, fmt=fmt)
     assert_encoding_of(out.codes, out.scales, y.cpu().numpy(), fmt == mx.FMT_MXFP8, "rows")
+
+
+@pytest.mark.parametrize("fmt", [mx.FMT_MXFP4, mx.FMT_MXFP8])
+def test_few_rows_encoded(fmt):
+    T, picks, E, N, K = 4, 2, 20, 288, 96
+    plan, parts, a, bc, bs, _ = _rows_case(T, picks, E, N, K, False, 0.2, 2.0, seed=7)
+    args = (a.codes, a.scales, bc, bs, plan, N, K)
+    out = mx.gemm_experts(*args, act=mx.ACT_GELU_TANH, dtype=F32, fmt=fmt)
+    assert_encoding_of(out.codes, out.scales, out.y.cpu().numpy(), fmt == mx.FMT_MXFP8, "rows")
 
 
 def test_rows_of_experts_hold_what_separate_products_hold():

@@ -51,6 +51,36 @@ def test_sizes(M, N, K, fp8, dtype):
     assert_output(out.z, z, ez, "z")
 
 
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17])
+@pytest.mark.parametrize("N,K", [(32, 32), (40, 96), (288, 4128), (4128, 160), (128, 2048)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["mxfp4", "mxfp8"])
+def test_few_rows(M, N, K, fp8):
+    out, (z, ez, y, ey) = _run(M, N, K, fp8, "gelu_tanh", _vector(N, BF16, 1), _matrix(M, N, F32, 2, pad=8), dtype=F32, want_z=True, scale=-4)
+    assert_output(out.y, y, ey, "y")
+    assert_output(out.z, z, ez, "z")
+
+
+def test_few_rows_keep_scales_at_the_ends_of_their_range():
+    """2^(a - 127) 2^(b - 127) with each factor at an end of its range and the product inside fp32's; NaN scales in their row or column."""
+    from tests.mx_testutil import tile_scales
+    M, N, K = 4, 32, 64
+    for fp8 in (False, True):
+        a, b = Operand(M, K, fp8, 1), Operand(N, K, fp8, 2)
+        ab, bb = np.array([[254, 0], [0, 254], [127, 127], [60, 194]], np.uint8), np.full((N, 2), 127, np.uint8)
+        bb[:, 0], bb[:, 1] = 2, 250
+        bb[8:], bb[20, 1] = 127, 255
+        values = [v.values / np.repeat(np.exp2(v.byte - 127.0), 32, 1) for v in (a, b)]
+        f = lambda x: np.repeat(np.exp2(x.astype(np.float64) - 127), 32, 1)  # noqa: E731
+        y = mx.gemm_bias_act(a.codes, dev(tile_scales(ab, M, K)), b.codes, dev(tile_scales(bb, N, K)), M, N, K, dtype=F32, operands=FMT[fp8]).y
+        ref = (values[0] * f(ab)) @ (values[1] * f(bb)).T
+        size = np.abs(values[0] * f(ab)) @ np.abs(values[1] * f(bb)).T
+        got = f64(y)
+        assert np.isnan(got[:, 20]).all()
+        ok = (size < 3e38) & (np.arange(N) != 20)
+        assert ok.sum() == 8 + 23 + 23   # rows 0 (its first 8 columns), 2 and 3 (the others but the NaN's)
+        assert_within(got[ok], ref[ok], 1e-5 * size[ok] + 2.0 ** -126, "values")
+
+
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("bias", [None, BF16, F32])
 @pytest.mark.parametrize("res", [None, BF16, F32])
@@ -60,6 +90,42 @@ def test_epilogues(act, bias, res):
                                None if res is None else _matrix(M, N, res, 4, pad=24), dtype=F32, want_z=True, scale=-3)
     assert_output(out.y, y, ey, "y")
     assert_output(out.z, z, ez, "z")
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("bias", [None, BF16, F32])
+@pytest.mark.parametrize("res", [BF16, F32])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_epilogues_of_four_lanes_a_row(act, bias, res, dtype):
+    """A residual with N a multiple of 64: the other arrangement of the epilogue."""
+    M, N, K = 200, 320, 160
+    out, (z, ez, y, ey) = _run(M, N, K, False, act, None if bias is None else _vector(N, bias, 3), _matrix(M, N, res, 4, pad=24), dtype=dtype, want_z=True,
+                               scale=-3)
+    assert_output(out.y, y, ey, "y")
+    assert_output(out.z, z, ez, "z")
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 64, 32), (300, 192, 96), (257, 320, 1056), (1000, 1088, 288)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("fmt", [None, mx.FMT_MXFP4, mx.FMT_MXFP8], ids=["plain", "to mxfp4", "to mxfp8"])
+def test_sizes_of_four_lanes_a_row(M, N, K, fp8, fmt):
+    kw = dict(act="silu", bias=_vector(N, F32, 1), res=_matrix(M, N, BF16, 2))
+    out, (z, ez, y, ey) = _run(M, N, K, fp8, dtype=F32, want_z=True, fmt=fmt, **kw)
+    assert_output(out.y, y, ey, "y")
+    assert_output(out.z, z, ez, "z")
+    if fmt is not None:
+        assert_encoding_of(out.codes, out.scales, out.y.cpu().numpy(), fmt == mx.FMT_MXFP8, "rows")
+        alone = _run(M, N, K, fp8, want_y=False, fmt=fmt, **kw)[0]
+        assert torch.equal(alone.codes, out.codes) and torch.equal(alone.scales, out.scales)
+
+
+@pytest.mark.parametrize("M", [3, 16])
+@pytest.mark.parametrize("fmt", [mx.FMT_MXFP4, mx.FMT_MXFP8], ids=["to mxfp4", "to mxfp8"])
+def test_few_rows_encoded(M, fmt):
+    N, K = 288, 224
+    kw = dict(act="relu2", bias=_vector(N, F32, 1), res=_matrix(M, N, BF16, 2))
+    out = _run(M, N, K, True, dtype=F32, fmt=fmt, **kw)[0]
+    assert_encoding_of(out.codes, out.scales, out.y.cpu().numpy(), fmt == mx.FMT_MXFP8, "rows")
 
 
 @pytest.mark.parametrize("N", [2048, 1892])
