@@ -270,14 +270,14 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kExpertWarps ? 3 : 1) mx_
         for (int n = warp; any && 4 * n < g.blocks; n += WARPS) {
             // Four blocks of 32 elements; the last may be fewer (zeros with scales of 1).
             const int left = g.blocks - 4 * n;
-            const int64_t at = static_cast<int64_t>(n) * 16 * E::kBytes;
+            const int64_t at = static_cast<int64_t>(n) * 16 * E::kBytes, at_s = static_cast<int64_t>(n) * 512;
             const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
             E b[4][4], a[NT][4];
             uint32_t sb[4], sa[NT][2];
             bool plain = true;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                sb[i] = *reinterpret_cast<const uint32_t *>(sb_at[i] + 512 * n);
+                sb[i] = *reinterpret_cast<const uint32_t *>(sb_at[i] + at_s);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     b[i][j].clear();
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kExpertWarps ? 3 : 1) mx_
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    sa[t][k] = *reinterpret_cast<const uint32_t *>(sa_at[t][k] + 512 * n) & keep | kOnes & ~keep;
+                    sa[t][k] = *reinterpret_cast<const uint32_t *>(sa_at[t][k] + at_s) & keep | kOnes & ~keep;
                     plain = plain && moderate(sa[t][k]);
                 }
             }

@@ -324,3 +324,21 @@ def test_gradient_of_many_rows_uses_bounded_workspace():
     out = mx.bias_act_backward(dy, want_dz=False, ws=torch.empty(mx.bias_act_backward_workspace_bytes(T, N), dtype=torch.uint8, device="cuda"))
     assert mx.bias_act_backward_workspace_bytes(T, N) <= 128 * N * 4
     assert (out.dbias == T).all()
+
+
+def test_few_rows_whose_scales_pass_32_bits():
+    N, K = 8, 2 ** 29 + 4096     # a line's scales end 2^31 + 16384 bytes behind its first
+    blocks, value = K // 32, {}
+    operands = []
+    for lines in (1, N):
+        codes, scales = (torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (lines * K // 2, mx.lib().mx_scales_bytes(lines, K)))
+        for line in range(lines):
+            for at, b in enumerate((0, 2 ** 24 - 1, 2 ** 24, 2 ** 24 + 5, blocks - 1)):
+                first = line * K // 2 + b * 16
+                codes[first:first + 16] = 0x22   # ones
+                scales[(b >> 2) * 512 + line * 16 + (b & 3)] = 127 + at + (lines > 1) * line
+                value[lines, line, at] = 2.0 ** (at + (lines > 1) * line)
+        operands += [codes, scales]
+    y = mx.gemm_bias_act(*operands, 1, N, K, dtype=F32).y
+    mx.check_status()
+    assert y.tolist() == [[32 * sum(value[1, 0, at] * value[N, line, at] for at in range(5)) for line in range(N)]]
