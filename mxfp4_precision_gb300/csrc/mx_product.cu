@@ -214,8 +214,9 @@ __device__ __forceinline__ int stages_of(const Tile &w) {
     return (w.units + kKSub * Elem<FMT>::kUnits - 1) / (kKSub * Elem<FMT>::kUnits);
 }
 
-// Reads the segments' bounds, held to the rows that exist whatever the plan says (an end
-// before its start: no rows), and counts the tile rows before each expert.  All threads.
+// Reads the segments' bounds, held to the rows that exist whatever the plan says, and counts
+// the tile rows before each expert.  An end before its start: no rows of that expert (depth), or
+// of any (rows: segments that overlap could hold more tiles than the counts do).  All threads.
 template <int MODE>
 __device__ __forceinline__ int read_segments(const ProductArgs &g, SharedCtl *ctl, int64_t rows) {
     const int e = threadIdx.x;
@@ -236,7 +237,12 @@ __device__ __forceinline__ int read_segments(const ProductArgs &g, SharedCtl *ct
         if (lane >= o) sum += v;
     }
     if (lane == 31) ctl->warp_tiles[warp] = sum;
-    __syncthreads();
+    const bool backwards = __syncthreads_or(length < 0) != 0;
+    if (backwards) {
+        if (e <= g.experts) ctl->start[e] = 0;
+        __syncthreads();
+        return 0;
+    }
     uint32_t before = 0, all = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
         if (i < warp) before += ctl->warp_tiles[i];

@@ -107,3 +107,52 @@ def test_plan(libs, T, picks, E):
         assert L.mx_expert_plan(_p(index), 4, T, picks, E, *(_p(t) for t in parts), _p(ws), ws.numel(), None) == 0
         return parts
     _same(libs, call)
+
+
+def _guarded(n, kept):
+    """n bytes between two lines of 4096 that must not change."""
+    t = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    kept.append((t, n))
+    return t.data_ptr() + 4096
+
+
+OFFSETS = {
+    "to and fro": lambda E, P, rng: np.array([0, P] * E)[:E + 1],
+    "any": lambda E, P, rng: rng.integers(-2 ** 31, 2 ** 31, E + 1),
+    "beyond the rows": lambda E, P, rng: np.sort(rng.integers(-P, 3 * P, E + 1)),
+    "one too large": lambda E, P, rng: np.where(np.arange(E + 1) == E // 2, 2 ** 31 - 1, 128 * np.arange(E + 1)),
+    "not whole groups": lambda E, P, rng: np.sort(rng.integers(0, P + 1, E + 1)),
+}
+
+
+@pytest.mark.parametrize("which", list(OFFSETS))
+@pytest.mark.parametrize("E,P", [(512, 131072), (512, 4096), (3, 1024)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_plan_of_any_content_stays_inside_the_buffers(libs, which, E, P, fp8):
+    # No value of the outputs is asked for: what a plan like these means is not defined.
+    rng = np.random.default_rng(E + P)
+    T, picks, N, K, fmt = 200, 3, 160, 32, 2 if fp8 else 1
+    whole = lambda n: dev(rng.integers(-2 ** 31, 2 ** 31, n).astype(np.int32))  # noqa: E731
+    offsets = dev(OFFSETS[which](E, P, rng).astype(np.int32))
+    counts, slot, source = whole(E), whole(T * picks), whole(P)
+    slot[::2] %= P
+    codes = lambda lines, k: torch.zeros(lines * k // (1 if fp8 else 2), dtype=torch.uint8, device="cuda")  # noqa: E731
+    scales = lambda lines, k: torch.full((mx.lib().mx_scales_bytes(lines, k),), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    a, sa, b, sb = codes(P, K), scales(P, K), codes(E * N, K), scales(N, K).repeat(E)
+    ta, tsa, tb, tsb = codes(K, P), scales(K, P), codes(N, P), scales(N, P)
+    x, w, bias = torch.randn(T, K, device="cuda"), torch.rand(T, picks, device="cuda"), torch.randn(E, N, device="cuda")
+    r = torch.randn(P, K, device="cuda").bfloat16()
+    for L in libs:
+        kept = []
+        out = lambda n: _guarded(n, kept)  # noqa: E731
+        rows = lambda n: out(P * n // (1 if fp8 else 2)), lambda n: out(L.mx_scales_bytes(P, n))  # noqa: E731
+        assert L.mx_gemm_experts(_p(a), _p(sa), _p(b), _p(sb), fmt, _p(offsets), _p(counts), E, P, N, K, _p(bias), 1, 5, out(4 * P * N), 1, out(2 * P * N),
+                                 fmt, rows[0](N), rows[1](N), None) == 0
+        assert L.mx_gemm_experts_wgrad(_p(ta), _p(tsa), _p(tb), _p(tsb), fmt, _p(offsets), E, P, K, N, out(4 * E * K * N), 1, None) == 0
+        assert L.mx_expert_dispatch(_p(x), 1, K, _p(slot), _p(source), T, picks, P, K, out(2 * P * K), fmt, rows[0](K), rows[1](K), None) == 0
+        assert L.mx_expert_combine(_p(r), 0, K, _p(slot), _p(w), T, picks, P, K, _p(x), 1, K, out(4 * T * K), 1, None) == 0
+        assert L.mx_expert_combine_backward(_p(x), 1, K, _p(r), 0, K, _p(slot), _p(source), _p(w), T, picks, P, K, out(2 * P * K), fmt, rows[0](K), rows[1](K),
+                                            out(4 * T * picks), None) == 0
+        assert L.mx_check_status(None) == 0
+        for t, n in kept:
+            assert bool((t[:4096] == 0xA5).all()) and bool((t[4096 + n:] == 0xA5).all())
