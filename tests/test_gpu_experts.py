@@ -350,3 +350,37 @@ def test_a_layer_of_experts_forward_backward_and_captured():
     graph.replay()
     for p, q in zip(held, _layer(x, index, w, w1, w2, d_out, E, F)):
         assert torch.equal(p, q)
+
+
+def test_calls_at_once_on_two_streams_hold_what_calls_in_turn_hold():
+    # A layer's forward and weight gradients on each stream, with plans of their own.
+    E, N, K, picks = 6, 520, 288, 2
+
+    def call(seed):
+        x = torch.randn(900 + 100 * seed, K, generator=torch.Generator().manual_seed(seed)).cuda()
+        index = dev(routing(x.shape[0], picks, E, seed, 0.1, 1))
+        w, wt = _experts_operand(E, N, K, False, seed)[:2], torch.rand(x.shape[0], picks, device="cuda", generator=torch.Generator("cuda").manual_seed(seed))
+        torch.cuda.synchronize()
+
+        def run():
+            plan = mx.expert_plan(index, E)
+            rows = mx.expert_dispatch(x, plan, fmt=mx.FMT_MXFP4)
+            o = mx.gemm_experts(rows.codes, rows.scales, *w, plan, N, K, act=mx.ACT_SILU, want_z=True)
+            y = mx.expert_combine(o.y, plan, wt)
+            g = mx.expert_combine_backward(y, o.y, plan, wt)
+            b = mx.bias_act_backward(g.y, o.z, mx.ACT_SILU)
+            return [*plan, rows.y, o.y, y, g.dweights, b.dz, b.dbias, mx.linear_experts_wgrad(b.dz, rows.y, plan)]
+        return run
+    calls = [call(1), call(2)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = []
+        for s, c in zip(streams, calls):
+            with torch.cuda.stream(s):
+                got.append(c())
+        torch.cuda.synchronize()
+        for u, v in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(u, v))
+    mx.check_status()
