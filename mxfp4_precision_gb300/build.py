@@ -127,7 +127,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if torch_obj is not None:
         tmp = TORCH_LIB + f".tmp{os.getpid()}"
         _run(["g++", "-shared", "-o", tmp, torch_obj.result(), "-L", out_dir, "-l:libmx.so", "-Wl,-rpath,$ORIGIN",
-              "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+              "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
         os.replace(tmp, TORCH_LIB)
         with open(TORCH_STAMP, "w") as f:
             f.write(_torch_stamp(torch))

