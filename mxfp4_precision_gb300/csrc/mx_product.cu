@@ -236,17 +236,21 @@ __device__ __forceinline__ int read_segments(const ProductArgs &g, SharedCtl *ct
         const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
         if (lane >= o) sum += v;
     }
-    if (lane == 31) ctl->warp_tiles[warp] = sum;
-    const bool backwards = __syncthreads_or(length < 0) != 0;
-    if (backwards) {
+    constexpr uint32_t kBackwards = 1u << 31;  // beside a warp's tiles, which are below 2^28
+    const bool backwards = __any_sync(0xFFFFFFFFu, length < 0);
+    if (lane == 31) ctl->warp_tiles[warp] = backwards ? kBackwards : sum;
+    __syncthreads();
+    uint32_t before = 0, all = 0, any = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+        const uint32_t v = ctl->warp_tiles[i];
+        if (i < warp) before += v;
+        all += v;
+        any |= v;
+    }
+    if (any & kBackwards) {
         if (e <= g.experts) ctl->start[e] = 0;
         __syncthreads();
         return 0;
-    }
-    uint32_t before = 0, all = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) before += ctl->warp_tiles[i];
-        all += ctl->warp_tiles[i];
     }
     if (e < g.experts) ctl->tiles_before[e] = static_cast<uint16_t>(before + sum - n);
     if (e == 0) ctl->tiles_before[g.experts] = static_cast<uint16_t>(all);
