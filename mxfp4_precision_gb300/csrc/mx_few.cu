@@ -1,5 +1,5 @@
 // mx_few.cu -- the products of mx_product.cu for few rows of A (tokens of a
-// decoding step), dense and by expert.
+// decoding step), dense and by expert (many experts: the second half of this file).
 //
 // With a handful of rows the product is a read of B: 2 M N K operations over
 // N K / 2 bytes.  Tiles of 256 columns leave most SMs without one (4096 columns:
@@ -20,9 +20,12 @@
 // small do not reach the copy rate.)  A ring of asynchronous copies a warp instead of the register
 // loads: 13.4 us where these take 11.2 to 13.2.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
+#include <cstring>
 #include <cuda_runtime.h>
 
+#include "../../include/mx.h"
 #include "mx_act.cuh"
 #include "mx_encode.cuh"
 #include "mx_internal.h"
@@ -44,6 +47,7 @@ struct FewArgs {
     int64_t katoms, b_groups;
     int blocks;           // blocks of 32 elements of a line
     int experts;          // 0: dense
+    int columns;          // by lines: the items' columns, kLines at a time
     const int32_t *offsets, *counts;
     const uint8_t *bias, *res;
     int64_t res_pitch;    // bytes
@@ -348,37 +352,410 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kExpertWarps ? 3 : 1) mx_
     }
 }
 
-template <bool FP8, int NT, int WARPS>
-cudaError_t launch(const FewArgs &g, dim3 grid, cudaStream_t stream) {
+// ---------------------------------------------------------------- by expert, many of them
+// The weights are the instruction's 128 rows and an expert's tokens its columns, as
+// few as there are (a multiple of 16): nothing is decoded, and the tensor cores have a fraction
+// of a tile's work.  A block stays on its SM and takes items in turn, kLines lines of an expert for up to
+// 128 of its rows: one warp copies, one multiplies, four bring the scales to tensor memory, four have a
+// lane quarter (32 lines, which are 32 columns of the output) each at the end, and two zero the rows without a
+// token meanwhile.
+//
+// Measured: 24 rows to 64 experts of 2048 x 2048 (20 of them used, 42 MB, and 13 MB of zeros) 15.2 us; the tiles 17.8, the
+// blocks above 21.5, of which their decoding is 7.  Without the zeros 13.7, and a plain read of 42 MB takes 13.  Items of 64
+// lines 20.4: a step's copies and scales cost the same for half the bytes.  Scales copied from shared to tensor memory by
+// the products' own thread (tcgen05.cp) 23.3, two sets of warps for them 15.4.
+constexpr int kLines = 128;       // of an item: the instruction's
+constexpr int kTokens = 16;       // rows of a copy of A
+constexpr int kRing = 6;
+constexpr int kLineThreads = 384;
+constexpr int kZeroWarp0 = 2, kZeroThreads = 64, kScaleWarp0 = 4, kEndWarp0 = 8;
+constexpr uint32_t kLineBytes = 128;             // of a step
+constexpr uint32_t kWeightBytes = kLines * kLineBytes, kTokenBytes = 128 * kLineBytes;
+constexpr uint32_t kAtomBytes = 1024;            // room for a step's scales of 128 lines
+constexpr uint32_t kAccColumns = 128, kScaleColumn = 2 * kAccColumns, kScaleColumns = 16, kAllColumns = 512;
+static_assert(kScaleColumn + kRing * kScaleColumns <= kAllColumns, "scales fit in tensor memory");
+
+template <bool FP8>
+struct Step {
+    static constexpr int kUnits = FP8 ? 1 : 2;  // of 128 elements, an atom of scales each
+};
+struct LineCtl {
+    uint64_t full[kRing], scaled[kRing], empty[kRing], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort_flag;
+    int backwards;
+    uint32_t warp_groups[kLineThreads / 32];
+    int start[MX_EXPERTS_MAX + 1];   // segments' first rows in units of 128
+    int taken[MX_EXPERTS_MAX];       // rows of a segment with a token
+    int before[MX_EXPERTS_MAX + 1];  // groups of 128 rows with a token of the experts before
+};
+constexpr size_t kLineSmem = 1024 + kRing * (kWeightBytes + kTokenBytes + 2 * kAtomBytes);
+static_assert(kLineSmem + sizeof(LineCtl) + 1024 <= 232448, "shared memory of an SM");
+
+// The last entry of at[0 .. n - 1] that is at most x (the first, if none is).
+__device__ __forceinline__ int last_of(const int *at, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (at[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// An item: the expert, its first row and the end of its rows, the first column.  Items run
+// over the columns, then an expert's rows, then the experts.
+struct Item {
+    int expert, row, end, col;
+};
+__device__ __forceinline__ Item item_of(const FewArgs &g, const LineCtl &ctl, int i) {
+    const int group = i / g.columns, e = last_of(ctl.before, g.experts, group);
+    const int first = ctl.start[e] * 128;
+    return {e, first + 128 * (group - ctl.before[e]), first + ctl.taken[e], (i - group * g.columns) * kLines};
+}
+// The next one; there is one.
+__device__ __forceinline__ void advance(const FewArgs &g, const LineCtl &ctl, Item &it) {
+    it.col += kLines;
+    if (it.col < g.columns * kLines) return;
+    it.col = 0;
+    it.row += 128;
+    if (it.row < it.end) return;
+    do ++it.expert;
+    while (ctl.taken[it.expert] == 0);
+    it.row = ctl.start[it.expert] * 128;
+    it.end = it.row + ctl.taken[it.expert];
+}
+// Its rows in whole copies.
+__device__ __forceinline__ int tokens_of(const Item &it) { return (min(128, it.end - it.row) + kTokens - 1) / kTokens * kTokens; }
+
+// Zeroes part `n` of `parts` of bytes [from, to) of an output (whole 16 bytes).
+__device__ __forceinline__ void zero_bytes(const FewArgs &g, uint8_t *base, int64_t from, int64_t to, size_t bytes, int n, int parts) {
+    const int t = threadIdx.x - 32 * kZeroWarp0;
+    if (base == nullptr) return;
+    for (int64_t i = from + (static_cast<int64_t>(n) * kZeroThreads + t) * 16; i < to; i += static_cast<int64_t>(parts) * kZeroThreads * 16)
+        if (MX_STORE_OK(base + i, 16, base, bytes, g.status)) *reinterpret_cast<uint4 *>(base + i) = make_uint4(0, 0, 0, 0);
+}
+// Rows without a token: of every 128 rows those behind their expert's, all behind the last segment.
+// Each 128 rows are several blocks' (or a block has several).
+__device__ __forceinline__ void zero_padding(const FewArgs &g, const LineCtl &ctl) {
+    const int t = threadIdx.x - 32 * kZeroWarp0;
+    const int groups = static_cast<int>(g.M >> 7), parts = max(1, static_cast<int>(gridDim.x) / groups);
+    for (int u = blockIdx.x; u < groups * parts; u += gridDim.x) {
+        const int n = u / groups, b = u - n * groups;
+        int real = 0;
+        if (b < ctl.start[g.experts]) {
+            const int e = last_of(ctl.start, g.experts, b);
+            real = max(0, min(128, ctl.taken[e] - 128 * (b - ctl.start[e])));
+        }
+        const int64_t from = static_cast<int64_t>(b) * 128 + real, to = static_cast<int64_t>(b) * 128 + 128;
+        zero_bytes(g, g.y, from * g.N * (g.y_f32 ? 4 : 2), to * g.N * (g.y_f32 ? 4 : 2), g.y_bytes, n, parts);
+        zero_bytes(g, g.z, from * g.N * 2, to * g.N * 2, g.z_bytes, n, parts);
+        if (g.fmt == kEncNone) continue;
+        zero_bytes(g, g.codes, g.fmt == kEncMX8 ? from * g.N : from * g.N / 2, g.fmt == kEncMX8 ? to * g.N : to * g.N / 2, g.codes_bytes, n, parts);
+        // A row's four scale bytes of each atom.
+        for (int64_t i = static_cast<int64_t>(n) * kZeroThreads + t; i < g.out_katoms * 128; i += static_cast<int64_t>(parts) * kZeroThreads) {
+            const int row = static_cast<int>(i & 127);
+            if (row < real) continue;
+            uint8_t *p = g.scales + (b * g.out_katoms + (i >> 7)) * 512 + (row & 31) * 16 + (row >> 5) * 4;
+            if (MX_STORE_OK(p, 4, g.scales, g.scales_bytes, g.status)) *reinterpret_cast<uint32_t *>(p) = 0;
+        }
+    }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kLineThreads, 1)
+    mx_few_lines_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ FewArgs g) {
+    constexpr int kUnits = Step<FP8>::kUnits;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ LineCtl ctl;
+    uint8_t *weights = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *tokens = weights + kRing * kWeightBytes, *atoms = tokens + kRing * kTokenBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], 1), mbar_init(&ctl.scaled[i], 4), mbar_init(&ctl.empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ctl.acc_full[i], 1), mbar_init(&ctl.acc_empty[i], kLineThreads / 32 - kEndWarp0);
+        mbar_init(&ctl.drain, 1);
+        ctl.abort_flag = ctl.backwards = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl.tmem, kAllColumns);
+        tmem_relinquish();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    // The segments, held to the rows that exist whatever the plan says; ends before their starts: no rows.
+    const int limit = static_cast<int>(g.M >> 7);
+    for (int e = threadIdx.x; e <= g.experts; e += kLineThreads) {
+        const int s = g.offsets[e] >> 7;
+        ctl.start[e] = s < 0 ? 0 : s > limit ? limit : s;
+        if (e < g.experts) ctl.taken[e] = g.counts[e];
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    static_assert(kLineThreads / 32 - kEndWarp0 == 4 && kEndWarp0 - kScaleWarp0 == 4, "a warp for each lane quarter");
+    static_assert(MX_EXPERTS_MAX <= 2 * kLineThreads, "two experts a thread");
+    int n[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = 2 * threadIdx.x + k;
+        if (e >= g.experts) continue;
+        const int length = ctl.start[e + 1] - ctl.start[e];
+        if (length < 0) ctl.backwards = 1;
+        const int taken = max(0, min(ctl.taken[e], 128 * max(0, length)));
+        ctl.taken[e] = taken;
+        n[k] = (taken + 127) / 128;
+    }
+    uint32_t sum = n[0] + n[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) ctl.warp_groups[warp] = sum;
+    __syncthreads();
+    const bool none = ctl.backwards != 0;
+    int before = sum - n[0] - n[1], all = 0;
+    for (int i = 0; i < kLineThreads / 32; ++i) {
+        const int v = ctl.warp_groups[i];
+        if (i < warp) before += v;
+        all += v;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = 2 * threadIdx.x + k;
+        if (e < g.experts) ctl.before[e] = before + (k ? n[0] : 0);
+    }
+    if (none)
+        for (int e = threadIdx.x; e <= g.experts; e += kLineThreads) ctl.start[e] = 0;
+    __syncthreads();
+    // A block's items follow one another.  Every role walks over the same ones.
+    const int64_t items = none ? 0 : static_cast<int64_t>(all) * g.columns;
+    const int first = static_cast<int>(items * blockIdx.x / gridDim.x), end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+    const int units = (g.blocks + 3) / 4, steps = (units + kUnits - 1) / kUnits;
+    volatile int *abort = &ctl.abort_flag;
+    Item it{};
+    if (first < end) it = item_of(g, ctl, first);
+    // Columns that exist, and something to add up.
+    const auto product = [&]() { return steps > 0 && it.col < g.N; };
+
+    if (warp == 0 && lane == 0) {
+        // ---------------------------------------------------------------- copies
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int i = first; ok && i < end; ++i) {
+            if (i > first) advance(g, ctl, it);
+            if (!product()) continue;
+            const int rows = tokens_of(it);
+            const uint8_t *bs = g.Bs + (it.expert * g.b_groups + (it.col >> 7)) * g.katoms * 512, *as = g.As + (it.row >> 7) * g.katoms * 512;
+            for (int s = 0; s < steps; ++s) {
+                if (!mbar_wait_inl(&ctl.empty[stage], phase ^ 1u, g.status, abort)) {
+                    ok = false;
+                    break;
+                }
+                uint64_t *bar = &ctl.full[stage];
+                constexpr uint32_t scales = kUnits * 512;  // of 128 lines; the layout's width is a multiple of it
+                mbar_arrive_expect_tx(bar, kWeightBytes + rows * kLineBytes + 2 * scales);
+                const int x = s * static_cast<int>(kLineBytes);
+                tma_load_2d(weights + stage * kWeightBytes, &map_b, bar, x, it.expert * static_cast<int>(g.N) + it.col);
+                bulk_load(atoms + stage * 2 * kAtomBytes, bs + static_cast<int64_t>(s) * scales, scales, bar);
+                bulk_load(atoms + stage * 2 * kAtomBytes + kAtomBytes, as + static_cast<int64_t>(s) * scales, scales, bar);
+                for (int m = 0; m < rows; m += kTokens)
+                    tma_load_2d(tokens + stage * kTokenBytes + m * kLineBytes, &map_a, bar, x, it.row + m);
+                if (++stage == kRing) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---------------------------------------------------------------- products
+        const uint32_t tmem = ctl.tmem;
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (int i = first; ok && i < end; ++i) {
+            if (i > first) advance(g, ctl, it);
+            if (!product()) continue;
+            const int rows = tokens_of(it);
+            if (!mbar_wait_inl(&ctl.acc_empty[acc], acc_phase ^ 1u, g.status, abort)) break;
+            tc_fence_after();
+            for (int s = 0; s < steps; ++s) {
+                if (!mbar_wait_inl(&ctl.scaled[stage], phase, g.status, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sf = tmem + kScaleColumn + kScaleColumns * stage;
+                const uint32_t sw = smem_u32(weights + stage * kWeightBytes), st = smem_u32(tokens + stage * kTokenBytes);
+                const int left = min(kUnits, units - s * kUnits);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // 32 bytes of a line each
+                    if (j >= 4 * left / kUnits) break;
+                    const uint32_t more = s > 0 || j > 0 ? 1u : 0u;
+                    if constexpr (FP8) {
+                        mma_mxf8(tmem + kAccColumns * acc, sdesc_sw128(sw + 32u * j), sdesc_sw128(st + 32u * j), idesc_mxf8(128, rows, j, j), sf, sf + 8u, more);
+                    } else {
+                        mma_mxf4(tmem + kAccColumns * acc, sdesc_sw128(sw + 32u * j), sdesc_sw128(st + 32u * j),
+                                 idesc_mxf4(128, rows, 2 * (j & 1), 2 * (j & 1)), sf + 4u * (j / 2), sf + 8u + 4u * (j / 2), more);
+                    }
+                }
+                tc_commit(&ctl.empty[stage]);
+                if (++stage == kRing) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            tc_commit(&ctl.acc_full[acc]);
+            if ((acc ^= 1) == 0) acc_phase ^= 1u;
+        }
+        // Every tensor-core operation has finished before the tensor memory is released.
+        tc_commit(&ctl.drain);
+        mbar_wait_inl(&ctl.drain, 0, g.status, nullptr, 100ull * 1000ull * 1000ull);
+    } else if (warp >= kZeroWarp0 && warp < kScaleWarp0) {
+        zero_padding(g, ctl);
+    } else if (warp >= kScaleWarp0 && warp < kEndWarp0) {
+        // ---------------------------------------------------------------- scales
+        // Lane l of every quarter gets lines l, l + 32, l + 64 and l + 96 of an atom in four columns, which is how
+        // an atom lies in memory.  A step's columns are written again once its products are done (`empty`).
+        const uint32_t lanes = ctl.tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kScaleColumn;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int i = first; ok && i < end; ++i) {
+            if (i > first) advance(g, ctl, it);
+            if (!product()) continue;
+            for (int s = 0; s < steps; ++s) {
+                ok = mbar_wait_inl(&ctl.full[stage], phase, g.status, abort);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint8_t *from = atoms + stage * 2 * kAtomBytes + lane * 16;
+                uint32_t v[16] = {};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(from + k * kAtomBytes + u * 512);
+                        v[8 * k + 4 * u] = w.x, v[8 * k + 4 * u + 1] = w.y, v[8 * k + 4 * u + 2] = w.z, v[8 * k + 4 * u + 3] = w.w;
+                    }
+                tmem_st_32x32b_x16(lanes + kScaleColumns * stage, v);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.scaled[stage]);
+                if (++stage == kRing) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp >= kEndWarp0) {
+        // ---------------------------------------------------------------- ends
+        const int q = warp & 3;  // tensor-memory lane quarter
+        const uint32_t lanes = ctl.tmem + (static_cast<uint32_t>(32 * q) << 16);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int i = first; i < end; ++i) {
+            if (i > first) advance(g, ctl, it);
+            const bool filled = product();
+            const int real = min(128, it.end - it.row), col = it.col + 32 * q + lane;
+            if (filled) {
+                int ok = 1;
+                if (lane == 0) ok = mbar_wait_inl(&ctl.acc_full[acc], acc_phase, g.status, abort) ? 1 : 0;
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            for (int m0 = 0; m0 < real; m0 += 8) {
+                uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (filled) {
+                    tmem_ld_32x32b_x8(lanes + kAccColumns * acc + m0, v);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+                    if (m0 + m < real) finish(g, it.row + m0 + m, it.expert, col, true, __uint_as_float(v[m]));
+            }
+            if (filled) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.acc_empty[acc]);
+                if ((acc ^= 1) == 0) acc_phase ^= 1u;
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(ctl.tmem, kAllColumns);
+    }
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(32 * WARPS, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_few_kernel<FP8, NT, WARPS>, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <bool FP8>
 cudaError_t launch_as(const FewArgs &g, dim3 grid, cudaStream_t stream) {
-    if (g.experts > 0) return launch<FP8, 1, kExpertWarps>(g, grid, stream);
-    return g.M > 8 ? launch<FP8, 2, kDenseWarps>(g, grid, stream) : launch<FP8, 1, kDenseWarps>(g, grid, stream);
+    if (g.experts > 0) return launch(mx_few_kernel<FP8, 1, kExpertWarps>, grid, 32 * kExpertWarps, 0, stream, g);
+    return g.M > 8 ? launch(mx_few_kernel<FP8, 2, kDenseWarps>, grid, 32 * kDenseWarps, 0, stream, g)
+                   : launch(mx_few_kernel<FP8, 1, kDenseWarps>, grid, 32 * kDenseWarps, 0, stream, g);
+}
+template <bool FP8>
+cudaError_t launch_lines(const CUtensorMap &map_a, const CUtensorMap &map_b, const FewArgs &g, const DeviceInfo &dev, cudaStream_t stream) {
+    static std::atomic<uint64_t> ready{0};  // devices that know the kernel's shared memory
+    const uint64_t bit = uint64_t{1} << (dev.ordinal & 63);
+    if ((ready.load(std::memory_order_relaxed) & bit) == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(mx_few_lines_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLineSmem));
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch(mx_few_lines_kernel<FP8>, dim3(dev.sm_count, 1, 1), kLineThreads, kLineSmem, stream, map_a, map_b, g);
 }
 
 }  // namespace
 
 // Where the tiles of mx_product.cu (256 columns, at most 76 pairs of SMs at a time) would leave most
-// SMs idle.  Measured, us, these blocks and the tiles (MXFP4): 8 x 4096 x 4096 5.8 and 9.5,
+// SMs idle.  Measured, us, the blocks of 32 columns and the tiles (MXFP4): 8 x 4096 x 4096 5.8 and 9.5,
 // 8 x 4096 x 14336 13.2 and 20.8, 16 x 4096 x 14336 17.2 and 20.8; but 8 x 14336 x 4096 (56 tiles)
 // 15.1 and 12.3.  By expert the host knows the capacity alone: up to 128 rows an expert it is 128 times
-// the number of rows (64 experts of 2048 x 2048, 24 rows, 192 tiles: 21.5 and 17.7).
+// the number of rows, each of which may be of another expert.
+namespace {
+int64_t expert_tiles(const Product &p) { return p.M / 128 * ((p.N + 255) / 256); }
+// Few tiles: the blocks of 32 columns fill more SMs than the blocks of 128 (2048 x 2048, 2 rows, 16 tiles: 5.4 us and 7.8;
+// 512 x 1024, 16 rows, 32 tiles: 6.0 and 6.7; but 64 tiles of 2048 x 2048: 10.7 and 8.0).
+bool few_blocks(const Product &p) {
+    return p.mode == kProductRows && p.M <= 128 * p.experts && expert_tiles(p) <= 32;
+}
+// More tiles, MXFP4, blocks of 128 columns and tiles: 64 experts of 2048 x 2048, 16 to 128 rows: 11.6 and 13.6 us to 31.1 and
+// 33.8; 256 of 512 x 1024, 128 rows: 10.6 and 16.1; 128 of 1536 x 4096, 128 rows, 768 tiles: 62.3 and 63.6; but 16 of
+// 14336 x 4096, 16 rows, 896 tiles: 64.3 and 62.9.  Few experts whose capacity is full may have many rows each: 8 of
+// 4096 x 4096, 128 rows: 21.8 and 18.9.  (MXFP8: 1 to 20% less than the tiles in all of these.)
+bool few_lines(const Product &p) {
+    return p.mode == kProductRows && (p.M < 128 * p.experts || (p.M == 128 * p.experts && p.experts >= 32)) && expert_tiles(p) <= 768;
+}
+}  // namespace
+
 bool few_rows(const Product &p) {
     const int64_t n_tiles = (p.N + 255) / 256;
     if (p.mode == kProductDense) return p.M <= 8 ? n_tiles <= 32 : p.M <= 16 && n_tiles <= 16;
-    return p.mode == kProductRows && p.M <= 128 * p.experts && p.M / 128 * n_tiles <= 32;
+    return few_blocks(p) || few_lines(p);
 }
 
 cudaError_t launch_few(const Product &p, const DeviceInfo &dev, cudaStream_t stream) {
@@ -414,7 +791,21 @@ cudaError_t launch_few(const Product &p, const DeviceInfo &dev, cudaStream_t str
     g.act = p.act;
     g.status = dev.status;
     // Columns up to the end of the scales' padding where there are scales.
-    const int64_t columns = p.enc.fmt == kEncNone ? (p.N + kColumns - 1) / kColumns : g.out_katoms * 4;
+    const int64_t end = p.enc.fmt == kEncNone ? p.N : g.out_katoms * 128;
+    if (few_lines(p) && !few_blocks(p)) {
+        g.columns = static_cast<int>((end + kLines - 1) / kLines);
+        CUtensorMap map_a, map_b;
+        std::memset(&map_a, 0, sizeof(map_a));
+        std::memset(&map_b, 0, sizeof(map_b));
+        if (p.K > 0) {  // without a contraction nothing is loaded
+            const auto map = [&](CUtensorMap *m, const void *codes, int64_t lines, uint32_t box) {
+                return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, g.line_bytes, lines, g.line_bytes, kLineBytes, box, CU_TENSOR_MAP_SWIZZLE_128B);
+            };
+            if (!map(&map_a, p.Aq, p.M, kTokens) || !map(&map_b, p.Bq, p.N * p.experts, kLines)) return cudaErrorInvalidValue;
+        }
+        return p.fp8 ? launch_lines<true>(map_a, map_b, g, dev, stream) : launch_lines<false>(map_a, map_b, g, dev, stream);
+    }
+    const int64_t columns = (end + kColumns - 1) / kColumns;
     const dim3 grid(static_cast<unsigned>(columns), static_cast<unsigned>(g.experts > 0 ? p.M / 128 : 1), 1);
     return p.fp8 ? launch_as<true>(g, grid, stream) : launch_as<false>(g, grid, stream);
 }

@@ -428,6 +428,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
           "=r"(r[31])
         : "r"(taddr));
 }
+// ... 8 of them.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 // 16 lanes by 64 columns: thread 4 r + c gets columns 8 i + 2 c, 8 i + 2 c + 1 of lane r in
 // registers 4 i, 4 i + 1 and of lane r + 8 in 4 i + 2, 4 i + 3 (i = 0 .. 7).
 __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
@@ -496,6 +502,19 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int a_sf_id, int
            | (1u << 23)                                   // scale format: UE8M0
            | (static_cast<uint32_t>(M >> 4) << 24)        // M / 16
            | (static_cast<uint32_t>(a_sf_id & 3) << 29);  // A scale-factor id
+}
+
+// The MXFP8 form of mma_mxf4 (K = 32 per instruction).
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
 }
 
 // The MXFP8 form of mma_mxf4_pair (K = 32 per instruction).

@@ -400,3 +400,60 @@ def test_a_plan_s_parts_are_tensors_of_their_own():
     torch.empty(1 << 20, device="cuda").fill_(1)   # what the other parts took is not given away while one is in use
     assert np.array_equal(source.cpu().numpy(), want[3])
     assert mx.expert_plan(index[:0], 5).source.shape == (0,)
+
+
+# Blocks of 128 columns: more than 32 tiles of 256 columns, and no more than 128 rows an expert.
+@pytest.mark.parametrize("T,picks,E,N,K,skew", [(33, 1, 64, 8, 32, 0), (150, 1, 64, 264, 416, 20), (150, 1, 64, 520, 1056, 4), (9, 4, 40, 1032, 96, 1),
+                                                (20, 3, 512, 136, 2080, 0), (60, 2, 512, 72, 4128, 3), (40, 1, 64, 264, 0, 1)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["mxfp4", "mxfp8"])
+def test_many_experts_of_few_rows(T, picks, E, N, K, skew, fp8):
+    plan, (offsets, counts, slot, source), a, bc, bs, bv = _rows_case(T, picks, E, N, K, fp8, 0.1, skew, seed=T)
+    assert source.size <= 128 * E and source.size // 128 * -(-N // 256) > 32
+    bias = torch.randn(E, N, generator=torch.Generator().manual_seed(1)).cuda()
+    want = [np.zeros((source.size, N)) for _ in range(4)]
+    for e in np.flatnonzero(counts):
+        r = slice(offsets[e], offsets[e] + counts[e])
+        for w, v in zip(want, epilogue64(a.values[r], bv[e], f64(bias[e]), "silu", None)):
+            w[r] = v
+    for dtype in (F32, BF16):
+        out = mx.gemm_experts(a.codes, a.scales, bc, bs, plan, N, K, bias=bias, act=mx.ACT_SILU, dtype=dtype, want_z=True, operands=FMT[fp8])
+        mx.check_status()
+        assert_output(out.y, want[2], want[3], "y")
+        assert_output(out.z, want[0], want[1], "z")
+
+
+@pytest.mark.parametrize("fmt", [mx.FMT_MXFP4, mx.FMT_MXFP8])
+@pytest.mark.parametrize("T,skew", [(20, 0), (150, 20)])
+def test_many_experts_of_few_rows_encoded(fmt, T, skew):
+    E, N, K = 64, 288, 160
+    plan, (_, _, _, source), a, bc, bs, _ = _rows_case(T, 1, E, N, K, False, 0.1, skew, seed=3, scale=-3)
+    args = (a.codes, a.scales, bc, bs, plan, N, K)
+    y32 = mx.gemm_experts(*args, act=mx.ACT_GELU, dtype=F32).y
+    for want_y in (False, True):
+        out = mx.gemm_experts(*args, act=mx.ACT_GELU, want_y=want_y, fmt=fmt)
+        mx.check_status()
+        assert_encoding_of(out.codes, out.scales, y32.cpu().numpy(), fmt == mx.FMT_MXFP8, "y")
+        assert not out.codes[dev(source) < 0].any()
+
+
+def test_many_experts_captured_and_replayed_with_another_plan():
+    T, picks, E, N, K = 40, 2, 64, 264, 288
+    weights = _experts_operand(E, N, K, False, 1)[:2]
+    index, x = [dev(routing(T, picks, E, seed, 0.1, 1)) for seed in (1, 2)], torch.randn(T, K, device="cuda")
+
+    def call(i):
+        plan = mx.expert_plan(i, E)
+        rows = mx.expert_dispatch(x, plan, fmt=mx.FMT_MXFP4)
+        return mx.gemm_experts(rows.codes, rows.scales, *weights, plan, N, K, act=mx.ACT_RELU).y
+    want = [call(i) for i in index]
+    held = index[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call(held)
+    for i, w in ((1, want[1]), (0, want[0])):
+        held.copy_(index[i])
+        y.fill_(7)
+        graph.replay()
+        assert torch.equal(y, w)
+    mx.check_status()

@@ -67,7 +67,7 @@ def test_gradient(libs, T, N):
     _same(libs, call)
 
 
-@pytest.mark.parametrize("T,picks,E,N,K", [(1, 1, 1, 32, 32), (130, 2, 5, 288, 160), (700, 3, 4, 1056, 96)])
+@pytest.mark.parametrize("T,picks,E,N,K", [(1, 1, 1, 32, 32), (130, 2, 5, 288, 160), (700, 3, 4, 1056, 96), (20, 2, 64, 288, 160)])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_experts(libs, T, picks, E, N, K, fp8):
     plan, parts = device_plan(routing(T, picks, E, 1, 0.1), E)
@@ -126,7 +126,7 @@ OFFSETS = {
 
 
 @pytest.mark.parametrize("which", list(OFFSETS))
-@pytest.mark.parametrize("E,P", [(512, 131072), (512, 4096), (3, 1024)])
+@pytest.mark.parametrize("E,P", [(512, 131072), (512, 65536), (512, 16384), (512, 4096), (3, 1024)])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_a_plan_of_any_content_stays_inside_the_buffers(libs, which, E, P, fp8):
     # No value of the outputs is asked for: what a plan like these means is not defined.
