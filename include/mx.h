@@ -481,7 +481,8 @@ mx_status mx_bias_act_backward(const void *d_dy, int dy_type, int64_t dy_pitch, 
  * rows = mx_expert_rows(T, picks, experts): what the segments can take at most, a
  * multiple of 128.  A plan lies on the device and is read there; a call needs no copy
  * of it.  Whatever it holds, the calls stay inside the buffers of the
- * sizes they are given.  At most MX_EXPERTS_MAX experts.
+ * sizes they are given; what the outputs hold where offsets go backwards or beyond
+ * `rows` is not defined.  At most MX_EXPERTS_MAX experts.
  *
  * mx_expert_plan -- makes one from d_index [T][picks] (int32, or int64 with
  * index_bytes 8): the expert of each choice.  Numbers outside 0 .. experts - 1 are dropped
@@ -539,7 +540,7 @@ mx_status mx_quantize_experts(const void *d_src, int64_t experts, int64_t rows, 
  * A [rows] lines, B as mx_quantize_experts leaves [experts] times N lines, d_bias
  * [experts][N] or NULL; outputs and the rest as mx_gemm_bias_act with M = rows.  For
  * the Dgrad, B holds the transposed weights (mx_quantize_experts with
- * MX_CONTRACT_ROWS).  experts * N < 2^31.
+ * MX_CONTRACT_ROWS).  experts * N < 2^31; rows / 256 + experts above 65535: MX_ERR_UNSUPPORTED.
  *
  * mx_gemm_experts_wgrad -- C[e] [M][N] = A_e . B_e^T over expert e's rows: A with M and
  * B with N lines, contraction `rows`, encoded down the rows (mx_quantize,
