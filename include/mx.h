@@ -506,7 +506,7 @@ mx_status mx_expert_plan(const void *d_index, int index_bytes, int64_t T, int64_
  * and / or encoded; all other rows zero) and d_dweights [T][picks] fp32 = dy[token] .
  * rows[slot] (0 for dropped choices; NULL: not computed, d_rows not read).
  * K and pitches % 8 == 0 (K % 32 == 0 to encode).  T == 0 or picks == 0: rows without a
- * token are still zeroed, and y = res.
+ * token are still zeroed, and y = res; d_x, d_dy and d_slot are not read and may be NULL.
  */
 mx_status mx_expert_dispatch(const void *d_x, int x_type, int64_t x_pitch, const int32_t *d_slot,
                              const int32_t *d_source, int64_t T, int64_t picks, int64_t rows,

@@ -534,7 +534,8 @@ cudaError_t launch_expert_dispatch(const RowIn &x, const ExpertRows &r, void *y,
     p.enc = row_encoded(e, r.rows, r.K);
     p.aligned32 = aligned32(x.p);
     p.aligned_out = y == nullptr || (aligned32(y) && r.K % 16 == 0);
-    const int64_t zeros = zero_blocks(p, kWarps), grid = zeros + (r.T * p.strips + kWarps - 1) / kWarps;
+    if (r.picks == 0) p.T = 0;  // x is not read (and may be null)
+    const int64_t zeros = zero_blocks(p, kWarps), grid = zeros + (p.T * p.strips + kWarps - 1) / kWarps;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.zeros = static_cast<uint32_t>(zeros);
     return x.f32 ? launch_dependent(mx_expert_dispatch_kernel<F32>, grid, 32 * kWarps, 0, stream, p)
