@@ -613,7 +613,7 @@ PyObject *expert_combine_backward(PyObject *const *a) {
         rm = matrix_of(matrix(a[1], "rows"), "rows", plan.rows, K);
         dweights = empty(dy, {plan.T, plan.picks}, at::kFloat);
     }
-    if (weights == nullptr) refuse("weights must be a torch.Tensor");
+    if (a[6] == Py_None) refuse("weights must be a torch.Tensor");  // no tokens: a tensor without memory
     if (truth(a[8])) drows = empty(dy, {plan.rows, K}, at::kBFloat16);
     const EncodedRows e(dy, a[7], plan.rows, K);
     check(mx_expert_combine_backward(dm.p, dm.type, dm.pitch, rm.p, rm.type, rm.pitch, plan.slot, plan.source, weights, plan.T,

@@ -48,3 +48,22 @@ def test_tokens_without_choices_from_torch():
     assert mx.expert_dispatch(res, plan).y.shape == (0, K)
     assert torch.equal(mx.expert_combine(torch.empty(0, K, device="cuda"), plan, residual=res), res)
     mx.check_status()
+
+
+@pytest.mark.parametrize("T,picks", [(0, 2), (37, 0)])
+def test_a_layer_s_gradients_of_no_rows(T, picks):
+    E, K, F, bf16 = 3, 128, 64, torch.bfloat16
+    plan = mx.expert_plan(torch.empty(T, picks, dtype=torch.int64, device="cuda"), E)
+    dy, w = torch.ones(T, K, device="cuda"), torch.empty(T, picks, device="cuda")
+    weights = torch.randn(E, K, F, device="cuda").to(bf16)
+    g = mx.expert_combine_backward(dy, torch.empty(0, K, device="cuda"), plan, w, fmt=mx.FMT_MXFP4)
+    assert g.y.shape == (0, K) and g.dweights.shape == (T, picks)
+    dh = mx.gemm_experts(g.codes, g.scales, *mx.quantize_experts(weights, mx.CONTRACT_ROWS), plan, F, K)
+    assert dh.y.shape == (0, F)
+    dz = mx.bias_act_backward(dh.y, torch.empty(0, F, dtype=bf16, device="cuda"), mx.ACT_GELU, fmt=mx.FMT_MXFP4)
+    assert dz.dz.shape == (0, F) and not dz.dbias.any()
+    assert not mx.linear_experts_wgrad(g.y, dz.dz, plan, out=torch.ones(E, K, F, device="cuda")).any()
+    assert torch.equal(mx.expert_combine(g.y, plan, residual=dy), dy)
+    with pytest.raises(ValueError, match="weights"):
+        mx.expert_combine_backward(dy, torch.empty(0, K, device="cuda"), plan, None)
+    mx.check_status()
