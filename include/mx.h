@@ -536,7 +536,8 @@ mx_status mx_quantize_experts(const void *d_src, int64_t experts, int64_t rows, 
 
 /*
  * mx_gemm_experts -- z[s] = A[s] . B_e^T + bias_e,  y = act(z), for the rows s of every
- * expert e; rows without a token, and rows behind the last segment, are zero.
+ * expert e; rows without a token are zero, those before the first segment and behind the
+ * last too.
  * A [rows] lines, B as mx_quantize_experts leaves [experts] times N lines, d_bias
  * [experts][N] or NULL; outputs and the rest as mx_gemm_bias_act with M = rows.  For
  * the Dgrad, B holds the transposed weights (mx_quantize_experts with

@@ -435,7 +435,8 @@ __device__ __forceinline__ void zero_bytes(const FewArgs &g, uint8_t *base, int6
     for (int64_t i = from + (static_cast<int64_t>(n) * kZeroThreads + t) * 16; i < to; i += static_cast<int64_t>(parts) * kZeroThreads * 16)
         if (MX_STORE_OK(base + i, 16, base, bytes, g.status)) *reinterpret_cast<uint4 *>(base + i) = make_uint4(0, 0, 0, 0);
 }
-// Rows without a token: of every 128 rows those behind their expert's, all behind the last segment.
+// Rows without a token: of every 128 rows those behind their expert's, all before the first segment and behind
+// the last.
 // Each 128 rows are several blocks' (or a block has several).
 __device__ __forceinline__ void zero_padding(const FewArgs &g, const LineCtl &ctl) {
     const int t = threadIdx.x - 32 * kZeroWarp0;
@@ -443,7 +444,7 @@ __device__ __forceinline__ void zero_padding(const FewArgs &g, const LineCtl &ct
     for (int u = blockIdx.x; u < groups * parts; u += gridDim.x) {
         const int n = u / groups, b = u - n * groups;
         int real = 0;
-        if (b < ctl.start[g.experts]) {
+        if (b >= ctl.start[0] && b < ctl.start[g.experts]) {
             const int e = last_of(ctl.start, g.experts, b);
             real = max(0, min(128, ctl.taken[e] - 128 * (b - ctl.start[e])));
         }

@@ -646,10 +646,12 @@ __device__ __forceinline__ void finish_rows(const ProductArgs &g, const EpiTile 
     put_scales(g, at, 8 * c, (c < 2 ? low : high) >> (16 * (c & 1)));
 }
 
-// Zeroes [from, base + bytes) of an output, 16 bytes at a time: the n-th of `threads` threads.
-__device__ __forceinline__ void zero_from(uint8_t *base, size_t from, size_t bytes, size_t n, size_t threads, int *status) {
+// Zeroes an output's bytes [0, until) and [from, bytes), 16 at a time: the n-th of `threads` threads.
+__device__ __forceinline__ void zero_around(uint8_t *base, size_t until, size_t from, size_t bytes, size_t n, size_t threads, int *status) {
     if (base == nullptr) return;
     const uint32_t none[4] = {0, 0, 0, 0};
+    for (size_t i = 16 * n; i < until; i += 16 * threads)
+        if (MX_STORE_OK(base + i, 16, base, bytes, status)) st_out16(base + i, none);
     for (size_t i = from + 16 * n; i < bytes; i += 16 * threads)
         if (MX_STORE_OK(base + i, 16, base, bytes, status)) st_out16(base + i, none);
 }
@@ -961,15 +963,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             else finish_row<MODE>(g, at, v0, v1);
         }
         if constexpr (MODE == kRows) {
-            // Rows behind the last segment are zero.
-            const size_t row = static_cast<size_t>(ctl->start[g.experts]) * 128;
+            // Rows before the first segment and behind the last are zero.
+            const size_t first = static_cast<size_t>(ctl->start[0]), last = static_cast<size_t>(ctl->start[g.experts]);
             const size_t n = static_cast<size_t>(blockIdx.x) * 32 * kEpiWarps + threadIdx.x - 32 * kEpiWarp0,
                          all = static_cast<size_t>(gridDim.x) * 32 * kEpiWarps;
             const size_t N = static_cast<size_t>(g.N);
-            zero_from(g.y, row * N * (g.y_f32 ? 4 : 2), g.y_bytes, n, all, g.status);
-            zero_from(g.z, row * N * 2, g.z_bytes, n, all, g.status);
-            zero_from(g.codes, g.fmt == kEncMX8 ? row * N : row * N / 2, g.codes_bytes, n, all, g.status);
-            zero_from(g.scales, (row >> 7) * static_cast<size_t>(g.out_katoms) * 512, g.scales_bytes, n, all, g.status);
+            const auto zero = [&](uint8_t *base, size_t group_bytes, size_t bytes) {  // of 128 rows
+                zero_around(base, first * group_bytes, last * group_bytes, bytes, n, all, g.status);
+            };
+            zero(g.y, 128 * N * (g.y_f32 ? 4 : 2), g.y_bytes);
+            zero(g.z, 128 * N * 2, g.z_bytes);
+            zero(g.codes, g.fmt == kEncMX8 ? 128 * N : 64 * N, g.codes_bytes);
+            zero(g.scales, static_cast<size_t>(g.out_katoms) * 512, g.scales_bytes);
         }
     }
 

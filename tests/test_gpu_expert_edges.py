@@ -67,3 +67,54 @@ def test_a_layer_s_gradients_of_no_rows(T, picks):
     with pytest.raises(ValueError, match="weights"):
         mx.expert_combine_backward(dy, torch.empty(0, K, device="cuda"), plan, None)
     mx.check_status()
+
+
+# ---------------------------------------------------------------------------- plans of one's own
+# Blocks of 32 columns, blocks of 128, tiles.
+KERNELS = {"blocks": (12, 96), "lines": (12, 2080), "tiles": (3, 2080)}
+
+
+def _placed(E, before, taken, behind):
+    """A plan whose first segment begins `before` rows in, with `taken[e]` rows for expert e and `behind` rows after the last; its rows with a token."""
+    offsets, real = [before], []
+    for n in taken:
+        real += range(offsets[-1], offsets[-1] + n)
+        offsets.append(offsets[-1] + -(-n // 128) * 128)
+    whole = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    source = torch.full((offsets[-1] + behind,), -1, dtype=torch.int32, device="cuda")
+    source[real] = whole(range(len(real)))
+    return mx.ExpertPlan(whole(offsets), whole(list(taken) + [0] * (E - len(taken))), whole(real)[:, None], source), real
+
+
+def _product(plan, E, N, K, operands, **kw):
+    """Products of ones by expert e + 1: (outputs in memory that held other values, the row's values)."""
+    P = plan.source.numel()
+    ones = lambda lines: (torch.full((lines, K if operands == mx.FMT_MXFP8 else K // 2), 0x38 if operands == mx.FMT_MXFP8 else 0x22, dtype=torch.uint8,  # noqa: E731
+                                     device="cuda"))
+    scales = lambda lines, byte: torch.full((mx.scales_bytes(lines, K),), byte, dtype=torch.uint8, device="cuda")  # noqa: E731
+    b = torch.cat([scales(N, 127 + e % 4) for e in range(E)])
+    L = mx.lib()
+    y, z = torch.full((P, N), float("nan"), device="cuda"), torch.full((P, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    codes, s = _filled(P * N // (1 if operands == mx.FMT_MXFP8 else 2)), _filled(mx.scales_bytes(P, N))
+    rows, weights = (ones(P), scales(P, 127)), (ones(E * N), b)
+    assert L.mx_gemm_experts(*(t.data_ptr() for t in (*rows, *weights)), operands, plan.offsets.data_ptr(), plan.counts.data_ptr(), E, P, N, K, None, 0, 0,
+                             y.data_ptr(), 1, z.data_ptr(), operands, codes.data_ptr(), s.data_ptr(), None) == 0
+    mx.check_status()
+    return y, z, codes.view(P, -1), s.view(P // 128, -1, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(P, -1)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("operands", [mx.FMT_MXFP4, mx.FMT_MXFP8])
+@pytest.mark.parametrize("before,behind", [(128, 0), (256, 128), (0, 256)])
+def test_rows_around_the_segments_are_zero(kernel, operands, before, behind):
+    E, N = KERNELS[kernel]
+    K, taken = 64, [5, 0, 130]
+    plan, real = _placed(E, before, taken + [0] * (E - 3), behind)
+    y, z, codes, scales = _product(plan, E, N, K, operands)
+    want = torch.zeros_like(y)
+    want[real[:5]] = K * 1.0
+    want[real[5:]] = K * 4.0
+    assert torch.equal(y, want) and torch.equal(z, want.bfloat16())
+    other = torch.ones(y.shape[0], dtype=torch.bool, device="cuda")
+    other[real] = False
+    assert not codes[other].any() and not scales[other].any() and bool(codes[real].all())
