@@ -480,9 +480,11 @@ mx_status mx_bias_act_backward(const void *d_dy, int dy_type, int64_t dy_pitch, 
  *   source  [rows] int32          token * picks + choice of each row, -1 for none
  * rows = mx_expert_rows(T, picks, experts): what the segments can take at most, a
  * multiple of 128.  A plan lies on the device and is read there; a call needs no copy
- * of it.  Whatever it holds, the calls stay inside the buffers of the
- * sizes they are given; what the outputs hold where offsets go backwards or beyond
- * `rows` is not defined.  At most MX_EXPERTS_MAX experts.
+ * of it.  Whatever it holds, the calls stay inside the buffers of the sizes they are
+ * given: offsets are held to 0 .. rows, and mx_gemm_experts takes a plan whose offsets
+ * then go backwards for one without rows (its outputs are zero).  What else comes of a
+ * plan whose offsets go backwards or beyond `rows` is not defined.  At most MX_EXPERTS_MAX
+ * experts.
  *
  * mx_expert_plan -- makes one from d_index [T][picks] (int32, or int64 with
  * index_bytes 8): the expert of each choice.  Numbers outside 0 .. experts - 1 are dropped

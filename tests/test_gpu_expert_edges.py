@@ -118,3 +118,19 @@ def test_rows_around_the_segments_are_zero(kernel, operands, before, behind):
     other = torch.ones(y.shape[0], dtype=torch.bool, device="cuda")
     other[real] = False
     assert not codes[other].any() and not scales[other].any() and bool(codes[real].all())
+
+
+BACKWARDS = {"to and fro": lambda E, P: [0, P] * E, "overlapping": lambda E, P: [0, 256, 128] + [P] * E, "at the end": lambda E, P: [128] * E + [0],
+             "ends before the rows": lambda E, P: [0, P] + [-128] * E}
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("operands", [mx.FMT_MXFP4, mx.FMT_MXFP8])
+@pytest.mark.parametrize("which", list(BACKWARDS))
+def test_offsets_that_go_backwards_hold_no_rows(kernel, operands, which):
+    E, N = KERNELS[kernel]
+    P = 640
+    whole = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    plan = mx.ExpertPlan(whole(BACKWARDS[which](E, P)[:E + 1]), whole([100] * E), whole([[0]]), whole([-1] * P))
+    for out in _product(plan, E, N, 64, operands):
+        assert not out.any()
