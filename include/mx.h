@@ -457,7 +457,8 @@ mx_status mx_gemm_bias_act(const void *d_Aq, const void *d_As, const void *d_Bq,
  *           order fixed by T and N
  *   d_ws    mx_bias_act_backward_workspace_bytes(T, N) bytes, 256-byte aligned
  *           (only for d_dbias; may be NULL where that is 0)
- * At least one output.  N, pitches % 8 == 0.  T == 0: d_dbias is zero-filled.
+ * At least one output.  N, pitches % 8 == 0.  T == 0: d_dbias is zero-filled.  dz of a NaN z
+ * is NaN, whatever the activation that reads it.
  */
 size_t mx_bias_act_backward_workspace_bytes(int64_t T, int64_t N);
 mx_status mx_bias_act_backward(const void *d_dy, int dy_type, int64_t dy_pitch, const void *d_z,
