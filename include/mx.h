@@ -480,7 +480,7 @@ mx_status mx_bias_act_backward(const void *d_dy, int dy_type, int64_t dy_pitch, 
  *   slot    [T][picks] int32      row of each choice, -1 if it was dropped
  *   source  [rows] int32          token * picks + choice of each row, -1 for none
  * rows = mx_expert_rows(T, picks, experts): what the segments can take at most, a
- * multiple of 128.  A plan lies on the device and is read there; a call needs no copy
+ * multiple of 128 (0 for T * picks >= 2^31, which no call takes).  A plan lies on the device and is read there; a call needs no copy
  * of it.  Whatever it holds, the calls stay inside the buffers of the sizes they are
  * given: offsets are held to 0 .. rows, and mx_gemm_experts takes a plan whose offsets
  * then go backwards for one without rows (its outputs are zero).  What else comes of a

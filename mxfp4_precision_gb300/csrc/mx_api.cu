@@ -940,7 +940,7 @@ mx_status mx_bias_act_backward(const void *d_dy, int dy_type, int64_t dy_pitch, 
 int64_t mx_expert_rows(int64_t T, int64_t picks, int64_t experts) {
     if (T <= 0 || picks <= 0 || experts <= 0 || T > 0x7FFFFFFF || picks > 0x7FFFFFFF) return 0;
     const int64_t n = T * picks;
-    return (n + 127 * std::min(experts, n)) / 128 * 128;
+    return n > 0x7FFFFFFF ? 0 : (n + 127 * std::min(experts, n)) / 128 * 128;
 }
 
 size_t mx_expert_plan_workspace_bytes(int64_t T, int64_t picks, int64_t experts) {

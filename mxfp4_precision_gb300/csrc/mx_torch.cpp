@@ -532,6 +532,7 @@ PyObject *expert_plan(PyObject *const *a) {
         refuse("experts must be contiguous and int32 or int64");
     const int64_t T = x.size(0), picks = x.size(1), count = integer(a[1]);
     if (count < 1) refuse("there must be an expert");
+    if (count > MX_EXPERTS_MAX) check(MX_ERR_UNSUPPORTED, "mx_expert_plan");  // before anything is allocated for them
     // One allocation: a call for a few tokens took 7.8 us with four, 4.4 us with one.
     const Parts<4> plan(x, at::kInt, {{{count + 1}, {count}, {T, picks}, {mx_expert_rows(T, picks, count)}}});
     const at::Tensor &offsets = plan.t[0], &counts = plan.t[1], &slot = plan.t[2], &source = plan.t[3];

@@ -69,6 +69,16 @@ def test_a_layer_s_gradients_of_no_rows(T, picks):
     mx.check_status()
 
 
+@pytest.mark.parametrize("experts", [513, 1 << 40, (1 << 63) - 1])
+def test_too_many_experts_are_refused_before_memory_is_taken(experts):
+    index = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    with pytest.raises(mx.MXError):
+        mx.expert_plan(index, experts)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+
+
 # ---------------------------------------------------------------------------- plans of one's own
 # Blocks of 32 columns, blocks of 128, tiles.
 KERNELS = {"blocks": (12, 96), "lines": (12, 2080), "tiles": (3, 2080)}
