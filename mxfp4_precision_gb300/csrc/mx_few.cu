@@ -740,14 +740,19 @@ cudaError_t launch_lines(const CUtensorMap &map_a, const CUtensorMap &map_b, con
 // Where the tiles of mx_product.cu (256 columns, at most 76 pairs of SMs at a time) would leave most
 // SMs idle.  Measured, us, the blocks of 32 columns and the tiles (MXFP4): 8 x 4096 x 4096 5.8 and 9.5,
 // 8 x 4096 x 14336 13.2 and 20.8, 16 x 4096 x 14336 17.2 and 20.8; but 8 x 14336 x 4096 (56 tiles)
-// 15.1 and 12.3.  By expert the host knows the capacity alone: up to 128 rows an expert it is 128 times
-// the number of rows, each of which may be of another expert.
+// 15.1 and 12.3.  By expert the host knows the capacity alone.  Below 128 rows an expert it is 128 times
+// the number of rows, n < experts, each of which may be of another expert; at 128 rows an expert, n
+// is anything from `experts` to experts + 127, and all may be of one.
 namespace {
 int64_t expert_tiles(const Product &p) { return p.M / 128 * ((p.N + 255) / 256); }
 // Few tiles: the blocks of 32 columns fill more SMs than the blocks of 128 (2048 x 2048, 2 rows, 16 tiles: 5.4 us and 7.8;
-// 512 x 1024, 16 rows, 32 tiles: 6.0 and 6.7; but 64 tiles of 2048 x 2048: 10.7 and 8.0).
+// 512 x 1024, 16 rows, 32 tiles: 6.0 and 6.7; but 64 tiles of 2048 x 2048: 10.7 and 8.0).  They read an expert's weights once
+// for every 8 of its rows, so few experts whose capacity is full go to the tiles (blocks and tiles, MXFP4): one of 4096 x 4096,
+// 1, 16 and 128 rows: 8.3, 13.7, 82.5 and 11.9; two of 2048 x 2048, 2, 17 and 129 rows in equal shares: 5.8, 8.5, 28.7 and 9.5;
+// four of 512 x 1024, 4, 67 and 131 rows: 3.9, 7.4, 10.8 and 7.9, all 131 in one: 29.4.  With eight, of 17 rows at most in the
+// mean, 8, 71 and 135 rows: 4.3, 6.0, 7.7 and 8.3 (256 x 4096: 8.5, 13.2, 18.2 and 11.9; 135 in one expert 80).
 bool few_blocks(const Product &p) {
-    return p.mode == kProductRows && p.M <= 128 * p.experts && expert_tiles(p) <= 32;
+    return p.mode == kProductRows && (p.M < 128 * p.experts || (p.M == 128 * p.experts && p.experts >= 8)) && expert_tiles(p) <= 32;
 }
 // More tiles, MXFP4, blocks of 128 columns and tiles: 64 experts of 2048 x 2048, 16 to 128 rows: 11.6 and 13.6 us to 31.1 and
 // 33.8; 256 of 512 x 1024, 128 rows: 10.6 and 16.1; 128 of 1536 x 4096, 128 rows, 768 tiles: 62.3 and 63.6; but 16 of

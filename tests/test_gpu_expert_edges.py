@@ -1,9 +1,12 @@
 """Calls by expert that the documentation allows and few programs make."""
+import numpy as np
 import pytest
 import torch
 
 import mxfp4_precision_gb300 as mx
 from mxfp4_precision_gb300 import build
+from tests.mx_testutil import GEMM_TOL
+from tests.product_testutil import Operand, assert_within, device_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +147,39 @@ def test_offsets_that_go_backwards_hold_no_rows(kernel, operands, which):
     plan = mx.ExpertPlan(whole(BACKWARDS[which](E, P)[:E + 1]), whole([100] * E), whole([[0]]), whole([-1] * P))
     for out in _product(plan, E, N, 64, operands):
         assert not out.any()
+
+
+# ---------------------------------------------------------------------------- full capacity
+def _all_in_one(E, n, N, K, fp8):
+    """n rows of the last of E experts: operands, the plan, the rows alone and that expert's weights."""
+    plan, (_, _, _, source) = device_plan(np.full((n, 1), E - 1, np.int32), E)
+    rows, weights = Operand(source.size, K, fp8, 1, spread=9, lines_zero=source < 0), [Operand(N, K, fp8, 2 + e, spread=9) for e in range(E)]
+    dense = Operand(n, K, fp8, 1)
+    dense.codes, dense.scales = rows.codes[:n], rows.scales[:mx.scales_bytes(n, K)]
+    return plan, rows, torch.cat([w.codes for w in weights]), torch.cat([w.scales for w in weights]), dense, weights[-1]
+
+
+@pytest.mark.parametrize("E,n", [(1, 17), (1, 128), (2, 129), (4, 131)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["mxfp4", "mxfp8"])
+def test_few_experts_that_one_may_fill_have_the_dense_product_s_bits(E, n, fp8):
+    # Rows of one expert enough for the dense product's tiles: the same kernel, so the same bits.
+    N, K, operands = 264, 4128, mx.FMT_MXFP8 if fp8 else mx.FMT_MXFP4
+    plan, rows, codes, scales, dense, b = _all_in_one(E, n, N, K, fp8)
+    assert plan.source.numel() == 128 * E
+    y = mx.gemm_experts(rows.codes, rows.scales, codes, scales, plan, N, K, dtype=torch.float32, operands=operands).y
+    want = mx.gemm_bias_act(dense.codes, dense.scales, b.codes, b.scales, n, N, K, dtype=torch.float32, operands=operands).y
+    mx.check_status()
+    assert torch.equal(y[:n], want) and not y[n:].any()
+
+
+@pytest.mark.parametrize("E,n", [(7, 7), (8, 8), (8, 135), (16, 143)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["mxfp4", "mxfp8"])
+def test_a_full_capacity_of_one_expert_s_rows(E, n, fp8):
+    N, K = 96, 288
+    plan, rows, codes, scales, _, b = _all_in_one(E, n, N, K, fp8)
+    assert plan.source.numel() == 128 * E
+    y = mx.gemm_experts(rows.codes, rows.scales, codes, scales, plan, N, K, dtype=torch.float32, operands=mx.FMT_MXFP8 if fp8 else mx.FMT_MXFP4).y
+    mx.check_status()
+    a = rows.values[:n]
+    assert_within(y[:n], a @ b.values.T, GEMM_TOL * (np.abs(a) @ np.abs(b.values).T), "y")
+    assert not y[n:].any()
