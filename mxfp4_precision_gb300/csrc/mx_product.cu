@@ -476,13 +476,13 @@ __device__ __forceinline__ void finish_row(const ProductArgs &g, const EpiTile &
 // scale writers gather the lines' scales in that order.  Four lanes then write a line together.
 __device__ __forceinline__ uint32_t line_of(uint32_t p) { return 16u * ((p >> 1) & 3u) + 2u * (p >> 3) + (p & 1u); }
 
-// Brings the bias of a warp's 64 columns into L1 while it waits for the tile.
+// Brings the bias of a warp's 64 columns into L1 while it waits for the tile (dense).
 template <int MODE>
 __device__ __forceinline__ void warm_bias(const ProductArgs &g, const EpiTile &at) {
     const int lane = threadIdx.x & 31, per = g.bias_f32 ? 4 : 8;  // columns of 16 bytes
     if (MODE == kDepth || g.bias == nullptr || per * lane >= kEpiCols || at.col >= g.N) return;
     asm volatile("{\n\t.reg .b32 a, b, c, d;\n\tld.global.v4.b32 {a, b, c, d}, [%0];\n\t}" ::"l"(
-        g.bias + ((MODE == kRows ? at.expert * g.N : 0) + at.col + per * lane) * (g.bias_f32 ? 4 : 2)));
+        g.bias + static_cast<int64_t>(at.col + per * lane) * (g.bias_f32 ? 4 : 2)));
 }
 
 // Adds 16 columns of a bf16 or fp32 row (16-byte aligned).
@@ -576,10 +576,11 @@ __device__ __forceinline__ uint32_t encode16(const ProductArgs &g, int64_t e, co
     return stored ? s : 0u;
 }
 
-// The lane's 16 columns of rows `more` and `more + 8` below its own.
+// The lane's 16 columns of rows `more` and `more + 8` below its own (dense and depth).
 // Returns both rows' two scale bytes (in lane 0 of four), the first row's in the low half.
 template <int MODE>
 __device__ __forceinline__ uint32_t finish_two(const ProductArgs &g, const EpiTile &at, int more, const uint32_t (&acc)[32]) {
+    static_assert(MODE == kDense || MODE == kDepth, "an expert's rows and their padding are finish_row's");
     const int col = at.col + 16 * static_cast<int>(threadIdx.x & 3);
     uint64_t v[16];
 #pragma unroll
@@ -595,26 +596,16 @@ __device__ __forceinline__ uint32_t finish_two(const ProductArgs &g, const EpiTi
         return 0;
     }
     if (g.bias != nullptr) {
-        const uint8_t *p = g.bias + ((MODE == kRows ? at.expert * g.N : 0) + col) * (g.bias_f32 ? 4 : 2);
+        const uint8_t *p = g.bias + static_cast<int64_t>(col) * (g.bias_f32 ? 4 : 2);
         add16(v, p, g.bias_f32);
         add16(v + 8, p, g.bias_f32);
-    }
-    if constexpr (MODE == kRows) {  // padding: zero, which every activation keeps
-        if (more >= at.real) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0;
-        }
-        if (more + 8 >= at.real) {
-#pragma unroll
-            for (int i = 8; i < 16; ++i) v[i] = 0;
-        }
     }
     if (g.z != nullptr) {
         if (first) put16_bf16(g.z + 2 * e0, g.z, g.z_bytes, v, g.wide, g.status);
         if (second) put16_bf16(g.z + 2 * e1, g.z, g.z_bytes, v + 8, g.wide, g.status);
     }
     activate(g, v);
-    if (MODE == kDense && g.res != nullptr) {
+    if (g.res != nullptr) {
         const uint8_t *p = g.res + (at.row + more) * g.res_pitch + static_cast<int64_t>(col) * (g.res_f32 ? 4 : 2);
         if (first) add16(v, p, g.res_f32);
         if (second) add16(v + 8, p + 8 * g.res_pitch, g.res_f32);
