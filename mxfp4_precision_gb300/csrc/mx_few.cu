@@ -230,19 +230,18 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kExpertWarps ? 3 : 1) mx_
         // Offsets are held to the rows that exist; any that go backwards: no rows (of segments that overlap
         // none would be the one).
         __shared__ int found, taken, backwards;
-        const int group = static_cast<int>(blockIdx.y), limit = static_cast<int>(g.M >> 7);
-        first = static_cast<int64_t>(group) * 128;
-        if (threadIdx.x == 0) found = -1, backwards = 0;
+        first = static_cast<int64_t>(blockIdx.y) * 128;
+        if (threadIdx.x == 0) found = taken = backwards = 0;
         __syncthreads();
         for (int e = threadIdx.x; e < g.experts; e += 32 * WARPS) {
+            const int group = static_cast<int>(blockIdx.y), limit = static_cast<int>(g.M >> 7);
             const int begin = max(0, min(limit, g.offsets[e] >> 7)), end = max(0, min(limit, g.offsets[e + 1] >> 7));
             if (end < begin) backwards = 1;
-            if (begin <= group && group < end) found = e, taken = max(0, g.counts[e]) - 128 * (group - begin);
+            if (begin <= group && group < end) found = e, taken = max(0, min(128, max(0, g.counts[e]) - 128 * (group - begin)));
         }
         __syncthreads();
-        const bool none = found < 0 || backwards != 0;
-        expert = none ? 0 : found;
-        real = none ? first : first + max(0, min(taken, 128));
+        expert = found;
+        real = first + (backwards != 0 ? 0 : taken);
         zero_rows(g, col0, real, first + 128, false);
     } else if (g.fmt != kEncNone) {
         zero_rows(g, col0, g.M, (g.M + 127) / 128 * 128, true);
