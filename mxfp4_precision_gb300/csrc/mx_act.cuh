@@ -62,6 +62,13 @@ __device__ __forceinline__ float step(float x) {
     asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(0.0f));
     return r;
 }
+// The same, NaN for NaN: max(step(x), min(x, 0)).
+__device__ __forceinline__ float step_or_nan(float x) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(0.0f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(step(x)));
+    return r;
+}
 __device__ __forceinline__ uint64_t step2(uint64_t x) {
     float a, b;
     unpack2(x, a, b);
@@ -145,23 +152,22 @@ __device__ __forceinline__ uint64_t value2(uint64_t x) {
 // Phi(x) + x phi(x) for gelu.  h and the second term are even and odd in x.  NaN stays NaN.
 template <int ACT>
 __device__ __forceinline__ uint64_t slope2(uint64_t x) {
-    if constexpr (ACT == kRelu2) {
+    if constexpr (ACT == kRelu || ACT == kRelu2) {
         float a, b;
         unpack2(x, a, b);
-        return mul2(same2(2.0f), pack2(positive(a), positive(b)));
+        return ACT == kRelu ? pack2(step_or_nan(a), step_or_nan(b)) : mul2(same2(2.0f), pack2(positive(a), positive(b)));
     }
     if constexpr (ACT == kNone) return same2(1.0f);
-    uint64_t low = 0;  // the slope at -|x|: h - |x| (-h')
-    if constexpr (ACT != kRelu) {
-        const uint64_t n = bounded2(x, most<ACT>());
-        const Part q = part2<ACT>(n);
-        if constexpr (ACT == kGelu) low = fma2(mul2(n, q.more), same2(0.3989422804f), q.h);  // 1 / sqrt(2 pi)
-        else if constexpr (ACT == kSilu) low = fma2(n, mul2(q.h, q.more), q.h);
-        else low = fma2(mul2(n, mul2(q.h, q.more)), fma2(mul2(n, n), same2(3.0f * kTanh * kCubic), same2(kTanh)), q.h);
-    }
+    const uint64_t n = bounded2(x, most<ACT>());
+    const Part q = part2<ACT>(n);
+    uint64_t low;  // the slope at -|x|: h - |x| (-h')
+    if constexpr (ACT == kGelu) low = fma2(mul2(n, q.more), same2(0.3989422804f), q.h);  // 1 / sqrt(2 pi)
+    else if constexpr (ACT == kSilu) low = fma2(n, mul2(q.h, q.more), q.h);
+    else low = fma2(mul2(n, mul2(q.h, q.more)), fma2(mul2(n, n), same2(3.0f * kTanh * kCubic), same2(kTanh)), q.h);
     float u, v, xa, xb;
     unpack2(low, u, v);
     unpack2(x, xa, xb);
+    // x > 0: 1 - low; NaN stays NaN.
     u = xa > 0.0f ? 1.0f - u : xa <= 0.0f ? u : xa;
     v = xb > 0.0f ? 1.0f - v : xb <= 0.0f ? v : xb;
     return pack2(u, v);
