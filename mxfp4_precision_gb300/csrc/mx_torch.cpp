@@ -18,7 +18,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/record_function.h>
-#include <c10/core/impl/TorchDispatchModeTLS.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -108,13 +108,23 @@ const at::Tensor &vector(PyObject *o, const char *name, int64_t n, int *type) {
     return t;
 }
 
-// Without the dispatcher, which takes 0.5 us of a call with two outputs; through it where somebody looks: a
-// dispatch mode, the profiler, torch's fill of fresh memory in deterministic runs.
+// Whether somebody looks at what a call allocates: a dispatch mode, the profiler, torch's fill of fresh
+// memory in deterministic runs.  Asked once a call (50 ns); a mode's own code may make calls in between.
+struct Watched {
+    static thread_local bool now;
+    const bool before = now;
+    Watched() {
+        const at::Context &torch = at::globalContext();
+        now = c10::impl::tls_is_dispatch_key_included(c10::DispatchKey::Python) || at::hasCallbacks() ||
+              (torch.deterministicAlgorithms() && torch.deterministicFillUninitializedMemory());
+    }
+    ~Watched() { now = before; }
+};
+thread_local bool Watched::now = false;
+
+// Without the dispatcher, which takes 0.5 us of a call with two outputs, unless it is watched.
 at::Tensor empty(const at::Tensor &like, at::IntArrayRef sizes, at::ScalarType type) {
-    const at::Context &torch = at::globalContext();
-    if (c10::impl::TorchDispatchModeTLS::any_modes_set() || at::hasCallbacks() ||
-        (torch.deterministicAlgorithms() && torch.deterministicFillUninitializedMemory()))
-        return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+    if (Watched::now) return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
     return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
 
@@ -162,6 +172,7 @@ PyObject *tuple_of(const T &...t) {
 // Device of the call and its current stream.
 struct Here {
     c10::cuda::CUDAGuard guard;
+    Watched watched;
     void *stream;
     explicit Here(const at::Tensor &t)
         : guard(t.device()),
