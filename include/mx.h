@@ -531,7 +531,8 @@ mx_status mx_expert_combine_backward(const void *d_dy, int dy_type, int64_t dy_p
  * nearest: expert e's codes at e * mx_codes_bytes(lines, k) (mx_mxfp8_codes_bytes), its
  * scales at e * mx_scales_bytes(lines, k).  MXFP4 with the arguments of mx_quantize; MXFP8
  * (rot MX_ROT_NONE) with MX_CONTRACT_ROWS alone, as mx_quantize_mxfp8, else
- * MX_ERR_UNSUPPORTED.
+ * MX_ERR_UNSUPPORTED.  One launch with MX_CONTRACT_COLS where rows % 128 == 0, else one
+ * for each expert.
  */
 mx_status mx_quantize_experts(const void *d_src, int64_t experts, int64_t rows, int64_t cols,
                               int operands, int contract, int rot, int rot_block, uint64_t seed,

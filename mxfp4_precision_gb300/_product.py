@@ -5,7 +5,8 @@ and back.
 Operands are the codes and scales that quantize, rmsnorm, swiglu and the calls
 here leave; other matrices are 2-D CUDA tensors of torch.bfloat16 (or raw 16-bit
 patterns) or torch.float32 whose rows are contiguous.  All tensors of a call are on
-one device.  Outputs and workspaces are allocated with torch unless given.
+one device.  Outputs and workspaces are allocated with torch unless given (through the
+dispatcher where a dispatch mode, the profiler or torch's deterministic fill looks).
 A `stream` other than the current one becomes the current one for the call.  None of them
 records an autograd node, copies to the host or waits: plans are made and read on
 the device, and every call can be captured in a CUDA graph.
@@ -98,7 +99,8 @@ def bias_act_backward_workspace_bytes(T: int, N: int) -> int:
 def bias_act_backward(dy, z=None, act: int = ACT_NONE, want_dz: bool = True, want_dbias: bool = True, fmt=None,
                       ws=None, stream=None) -> BiasActGrad:
     """dz = dy * act'(z) in bf16 (want_dz) and / or encoded along its rows (fmt) as the Dgrad's operand,
-    and dbias = its sum over the rows in fp32 (want_dbias).  See mx_bias_act_backward."""
+    and dbias = its sum over all rows in fp32 (want_dbias; of gemm_experts' bias, not by expert).
+    See mx_bias_act_backward."""
     if stream is not None:
         with _block._on(stream, dy):
             return bias_act_backward(dy, z, act, want_dz, want_dbias, fmt, ws)
@@ -154,7 +156,8 @@ def expert_combine_backward(dy, rows, plan: ExpertPlan, weights, fmt=None, want_
 def quantize_experts(w, contract: int = _b.CONTRACT_COLS, operands: int = FMT_MXFP4, rot: int = _b.ROT_NONE,
                      rot_block: int = 32, seed: int = 0, stream=None):
     """(codes, scales) of w [experts, rows, columns] in bf16, each matrix an operand of its own, as
-    gemm_experts reads them.  See mx_quantize_experts."""
+    gemm_experts reads them.  FMT_MXFP8 takes contract=CONTRACT_ROWS (lines are the columns).  One launch
+    along the columns where the rows are a multiple of 128, else one an expert.  See mx_quantize_experts."""
     if stream is not None:
         with _block._on(stream, w):
             return quantize_experts(w, contract, operands, rot, rot_block, seed)

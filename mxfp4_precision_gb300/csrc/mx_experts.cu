@@ -11,8 +11,8 @@
 // Slots that lie outside the rows stand for dropped choices.
 //
 // Measured, 8192 tokens of 4096 columns to 4 of 64 experts (32768 rows and 8064 without a token, bf16): plan
-// 10 us (two launches), rows in with bf16 and MXFP8 90 us = 6.4 TB/s, rows out 64 us = 6.3 TB/s, their gradient with
-// the weights' 119 us = 5.6 TB/s (128 registers leave two blocks an SM; two rows at a time with three blocks 122,
+// 9 us (two launches), rows in with bf16 and MXFP8 90 us = 6.4 TB/s, rows out 64 us = 6.3 TB/s, their gradient with
+// the weights' 120 us = 5.6 TB/s (128 registers leave two blocks an SM; two rows at a time with three blocks 122,
 // and 135 with four).
 #include <algorithm>
 #include <cstdint>

@@ -15,10 +15,9 @@
 // agree, so lane c of four takes elements 8 c .. 8 c + 7 of a block: one load, and
 // two instructions to a block, after which the sums get the block's scales.
 //
-// Measured: 8 x 4096 x 4096 5.8 us, of which an empty launch is 2.5 (the tiles: 9.5), 5 x 4128 x 2080 in MXFP8
-// 5.5 us; 1 x 4096 x 14336 11.2 us = 2.8 TB/s.  (A plain sum over 67 MB runs at 3.4 TB/s here: reads this
-// small do not reach the copy rate.)  A ring of asynchronous copies a warp instead of the register
-// loads: 13.4 us where these take 11.2 to 13.2.
+// Measured: 8 x 4096 x 4096 6.0 us, of which an empty launch is 2.5 (the tiles: 9.5), 5 x 4128 x 2080 in MXFP8
+// 5.0 us; 1 x 4096 x 14336 11.3 us = 2.8 TB/s.  (A plain sum over 67 MB, not written for this, runs at 3.4 TB/s.)  A
+// ring of asynchronous copies a warp instead of the register loads: 13.4 us where these took 11.2 to 13.2.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -364,10 +363,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kExpertWarps ? 3 : 1) mx_
 // lane quarter (32 lines, which are 32 columns of the output) each at the end, and two zero the rows without a
 // token meanwhile.
 //
-// Measured: 24 rows to 64 experts of 2048 x 2048 (20 of them used, 42 MB, and 13 MB of zeros) 15.2 us; the tiles 17.8, the
-// blocks above 21.5, of which their decoding is 7.  Without the zeros 13.7, and a plain read of 42 MB takes 13.  Items of 64
-// lines 20.4: a step's copies and scales cost the same for half the bytes.  Scales copied from shared to tensor memory by
-// the products' own thread (tcgen05.cp) 23.3, two sets of warps for them 15.4.
+// Measured: 24 rows to 64 experts of 2048 x 2048 (20 of them used, 42 MB, and 13 MB of zeros) 14.4 us; the tiles 17.8, the
+// blocks above 21.5, of which their decoding is 7.  Without the zeros 1.5 less; a plain read of 42 MB takes 13, 2.5 of
+// them the launch.  Items of 64 lines 20.4: a step's copies and scales cost the same for half the bytes.  Scales copied
+// from shared to tensor memory by the products' own thread (tcgen05.cp) 23.3, two sets of warps for them 15.4.
 constexpr int kLines = 128;       // of an item: the instruction's
 constexpr int kTokens = 16;       // rows of a copy of A
 constexpr int kRing = 6;
@@ -753,10 +752,11 @@ int64_t expert_tiles(const Product &p) { return p.M / 128 * ((p.N + 255) / 256);
 bool few_blocks(const Product &p) {
     return p.mode == kProductRows && (p.M < 128 * p.experts || (p.M == 128 * p.experts && p.experts >= 8)) && expert_tiles(p) <= 32;
 }
-// More tiles, MXFP4, blocks of 128 columns and tiles: 64 experts of 2048 x 2048, 16 to 128 rows: 11.6 and 13.6 us to 31.1 and
-// 33.8; 256 of 512 x 1024, 128 rows: 10.6 and 16.1; 128 of 1536 x 4096, 128 rows, 768 tiles: 62.3 and 63.6; but 16 of
-// 14336 x 4096, 16 rows, 896 tiles: 64.3 and 62.9.  Few experts whose capacity is full may have many rows each: 8 of
-// 4096 x 4096, 128 rows: 21.8 and 18.9.  (MXFP8: 1 to 20% less than the tiles in all of these.)
+// More tiles, MXFP4, blocks of 128 columns and tiles: 64 experts of 2048 x 2048, 16 to 128 rows: 11.3 and 13.3 us to 31.2 and
+// 33.6; 256 of 512 x 1024, 128 rows: 10.6 and 16.1; 128 of 1536 x 4096, 128 rows, 768 tiles: 63.0 and 63.1; but 16 of
+// 14336 x 4096, 16 rows, 896 tiles: 63.7 and 62.3.  Few experts whose capacity is full may have many rows each: 8 of
+// 4096 x 4096, 64 rows: 21.2 and 20.1, 128 rows: 22.6 and 20.1.  MXFP8 goes by the same bounds: 64 of 2048 x 2048 18.3 and
+// 20.1 to 50.9 and 51.0; 896 tiles 128 and 133; 8 of 4096 x 4096 33.3 and 33.7, 35.1 and 33.5.
 bool few_lines(const Product &p) {
     return p.mode == kProductRows && (p.M < 128 * p.experts || (p.M == 128 * p.experts && p.experts >= 32)) && expert_tiles(p) <= 768;
 }

@@ -24,13 +24,15 @@
 // Epilogue.  Bias, activation, residual, both outputs and the codes take some 30 instructions a column
 // where all are asked for (GELU 13 of them, two columns at a time), against which the tensor cores' time for
 // a tile of K = 4096 is 5.3 us.  Sixteen warps of 64 columns and not eight of 128: 8192 x 14336 x 4096
-// with bias, GELU, z, bf16 y and MXFP8 rows takes 209 us, 244 with eight, whose instructions wait for one another
+// with bias, GELU, z, bf16 y and MXFP8 rows takes 210 us, 244 with eight, whose instructions wait for one another
 // (96 registers hold 64 columns and what they need, so the 768 threads' 80 at launch are split
-// 48 / 96).  With bf16 y alone it is 149 us, the tensor cores' time.  Stores leave as they come: spreading them over
-// the next tile's stages, which mx_gemm.cu gains by, cost 5 to 25% in every form here.  So did an L2 prefetch of
-// the next B panel: nothing.  z and y are rounded from fp32 once each, codes from y in fp32.
-// Measured, of the tensor cores' 9,650 TFLOP/s for FP4: bf16 y alone 67%, everything 48%, 8 experts of 14336 x
-// 4096 over 16384 rows with bias and SiLU 55% (361 us); their Wgrad writes 1.88 GB of fp32 in 450 us.
+// 48 / 96).  With bf16 y alone it is 148 us, where the operations at the tensor cores' measured rate take 100.
+// Stores leave as they come: spreading them over the next tile's stages, which mx_gemm.cu gains by, cost 5 to 25% in
+// every form here.  An L2 prefetch of the next B panel made no difference.  z and y are rounded from fp32
+// once each, codes from y in fp32.
+// Measured (calls replayed one after another), as shares of the tensor cores' 9,650 TFLOP/s for FP4 and half of it for
+// FP8: MXFP4 operands, bf16 y alone 67%, everything 47%; 8 experts of 14336 x 4096 over 16384 rows with bias and SiLU 54%
+// (366 us); their Wgrad writes 1.88 GB of fp32 in 453 us.  MXFP8 operands: bf16 y alone 262 us (76%), everything 314 to 323.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -1040,8 +1042,8 @@ cudaError_t launch_product(const Product &p, const DeviceInfo &dev, cudaStream_t
     const int64_t row_bytes = p.fp8 ? p.K : p.K / 2;
     // Four lanes a row (GATHER) where lines are what the epilogue waits for: a residual is read
     // (8192 x 14336 x 4096: 167 us, 230 without), and the experts' Wgrad, whose outputs are many
-    // for the length of its products (8 experts of 14336 x 4096 over 16384 rows, fp32: 437 us, 510
-    // without).  Elsewhere a lane's own row is no slower (bf16 150 us, 151 to 156) or faster
+    // for the length of its products (8 experts of 14336 x 4096 over 16384 rows, fp32: 453 us, 543
+    // without).  Elsewhere a lane's own row is no slower (bf16 148 us, 151 to 156) or faster
     // (z, y and codes with gelu 210 us, 242).  Whole groups of 64 lines alone can be loaded in
     // that order: a partial one could not be kept inside its buffer.
     const bool gather = p.N % 64 == 0 && (depth || p.res.p != nullptr);
